@@ -530,6 +530,49 @@ moe_status_t moe_ffn_mxfp4act_down(const uint8_t* w2, const uint8_t* s2, const f
 moe_status_t moe_ffn_mxfp4act_h_offsets(int T, int H, int I, int Et, int Kt, int tile_m,
                                         size_t* codes_offset, size_t* scales_offset);
 
+/*
+ * ------------------------------------------------------- dense projections
+ * The projections around the layer (attention, a dense FFN, the output head)
+ * with the same weight format.  The pages name the format and the GEMM (OR,
+ * section "how far from the ceiling"), not this call; the rounding rule is the
+ * one above.
+ */
+
+/* Element types of the rows a call reads and writes. */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype_t;
+
+/*
+ * moe_linear_mxfp4act -- out = [residual +] W xq with MXFP4 weights and
+ * activations quantised to MXFP4 inside the call.
+ *   x        [T] rows of K values of x_type, row t at x + t * ldx.
+ *   codes    uint8 [N, K/2] packed E2M1 codes of W; scales uint8 [N, K/32] E8M0.
+ *   residual NULL, or [T] rows of N values of out_type, ldr elements apart; may
+ *            be out itself (same pointer, ldr = ldo).
+ *   out      [T] rows of N values of out_type, ldo elements apart.
+ *   ldx >= 0, ldr >= 0, ldo >= N: rows may be slices of wider ones; those that
+ *   are only read may overlap (0: one row for every token).
+ * For each token t:
+ *   xq = decode(quantise(x_t))                  (blocks of 32 along K)
+ *   out[t, n] = round(residual[t, n] + sum over k of decode(W)[n, k] * xq[k])
+ * with fp32 sums (in another order than k's) and one rounding, to out_type.
+ * A block of x that holds an infinity or a NaN encodes as NaN, so every output
+ * of its token is NaN; other tokens are not touched.  Weight scale byte 255 is NaN
+ * likewise.
+ * One or two launches: the encoding and the product, whose tiles follow T (see
+ * linear_mxfp4.cu).  T = 0 is a no-op.  The result does not vary from run to
+ * run.
+ * Limits: K % 32 == 0, K <= 65536, N <= 2^24, T <= 2^20.  codes and workspace
+ * 16-byte aligned, scales 4-byte, the others to their element; x and out rows
+ * on 16-byte boundaries are read and written faster.  A call needs
+ * moe_linear_mxfp4act_workspace_size() bytes of device workspace (0 for sizes
+ * outside the limits), whose contents it overwrites.
+ */
+size_t moe_linear_mxfp4act_workspace_size(int T, int N, int K);
+moe_status_t moe_linear_mxfp4act(const void* x, moe_dtype_t x_type, int64_t ldx, const uint8_t* codes,
+                                 const uint8_t* scales, const void* residual, int64_t ldr, void* out,
+                                 moe_dtype_t out_type, int64_t ldo, int T, int N, int K,
+                                 void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 /* The regime MOE_PATH_AUTO picks for these sizes [VL, small-M vs large-M]:
  * MOE_PATH_DECODE or MOE_PATH_PREFILL (the large-M regime, whichever of its
  * two paths moe_ffn_auto_path_shape names). */

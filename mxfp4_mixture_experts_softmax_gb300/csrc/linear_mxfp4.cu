@@ -1,0 +1,464 @@
+// linear_mxfp4.cu -- a dense projection with MXFP4 weights and activations
+// quantised to MXFP4 inside the call:
+//   xq = decode(quantise(x))  per token, blocks of 32 along K
+//   out[t, n] = residual[t, n] + sum_k decode(W)[n, k] * xq[t, k]
+// with fp32 sums and one rounding to the output type.
+//
+// quantize_rows_kernel encodes x; linear_stream_kernel multiplies, on the
+// block-scaled tensor cores (tcgen05.mma kind::mxf4, both scales applied by the
+// MMA, K = 64 an instruction).
+//
+// The weights are the MMA's M side (128 rows a CTA) and the tokens its N side
+// (NT = 16 .. 128 columns), so one token costs no more tensor work than
+// sixteen and the weight stream, which bounds small batches, is read once per
+// token tile.  A stage is 256 k: one 128-byte row of packed codes per weight row and
+// token, two TMA boxes in the 128-byte swizzle.  Few weight tiles do not fill the
+// GPU, so a cluster of S CTAs splits K: each multiplies its range of stages,
+// leaves its fp32 partial tile in shared memory, and the CTAs of the cluster
+// each add a share of the tile over the S partials (distributed shared
+// memory, in rank order: the result does not depend on timing).
+// 192 threads, two CTAs per SM, so that one CTA's start and end overlap the
+// other's stream:
+//   * producer warp: the TMA loads.  The weights of the first stages are asked for
+//     before the quantisation kernel has finished (programmatic launch);
+//   * MMA warp: one thread;
+//   * 4 warps, one per tensor-memory lane quadrant: write each stage's scale
+//     factors into tensor memory (layout as in ffn_mxfp4act.cu), then drain the
+//     accumulator.
+// Every wait is bounded (see mbar_wait).
+#include <algorithm>
+
+#include "moe_internal.h"
+#include "mxf4.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBK = 256;  // k per stage: one 128-byte row of packed codes
+constexpr int kRowBytes = kBK / 2;
+constexpr int kMRows = 128;
+constexpr int kABytes = kMRows * kRowBytes;
+
+// ------------------------------------------------------------ quantisation
+
+// Eight values of a row from `p`: one or two 16-byte loads, or element by
+// element where the row's start is not 16-byte aligned.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load8(const void* p, float v[8]) {
+    if (F32) {
+        const float* f = reinterpret_cast<const float*>(p);
+        if (VEC) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(f));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(f) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __ldg(f + i);
+        }
+    } else if (VEC) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
+    } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)__ldg(h + i) << 16);
+    }
+}
+
+// The MXFP4 encoding of a 32-value block held by four neighbouring lanes, eight
+// values each: this lane's four code bytes, and the block's scale byte in all
+// four.  The rule of moe_quantize_mxfp4, except that a block that holds an
+// infinity or a NaN gets scale byte 255 (E8M0's NaN) and codes 0, so that it
+// decodes to NaN and the MMA carries it into every output of its token.
+__device__ __forceinline__ uint32_t quantize8(const float v[8], uint32_t& sbyte) {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    if (mx >= 0x7F800000u) {
+        sbyte = 255u;
+        return 0u;
+    }
+    sbyte = mx_scale_byte(__uint_as_float(mx));
+    return e2m1x8(v, mx_inv_scale(sbyte));
+}
+
+// x [T] rows of K values, ldx elements apart -> codes [T][K/2] and scales, a
+// row of `pitch` bytes per token (K/32 bytes, zeros up to the next multiple of
+// 8).  One warp takes 256 values of a row at a time, eight per lane: every load
+// and store is coalesced.  Bound by HBM for long prompts (2 bytes read and
+// 17/32 written per value), by launch latency for short ones.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256)
+    quantize_rows_kernel(const void* __restrict__ x, long long ldx, int T, int K,
+                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int pitch) {
+    pdl_begin();
+    const int lane = threadIdx.x & 31;
+    const int segs = (K + kBK - 1) / kBK;
+    const long long items = (long long)T * segs;
+    const int esize = F32 ? 4 : 2;
+    for (long long it = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items;
+         it += (long long)gridDim.x * (blockDim.x >> 5)) {
+        const int t = (int)(it / segs), seg = (int)(it - (long long)t * segs);
+        const int k = seg * kBK + lane * 8;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (k < K)
+            load8<F32, VEC>(reinterpret_cast<const char*>(x) + ((size_t)t * ldx + k) * esize, v);
+        uint32_t sb;
+        const uint32_t c = quantize8(v, sb);
+        if (k < K) *reinterpret_cast<uint32_t*>(codes + (size_t)t * (K / 2) + k / 2) = c;
+        // lanes 0 and 16: the four scale bytes of their 128 values
+        uint32_t w = sb;
+        w |= __shfl_down_sync(0xFFFFFFFFu, sb, 4) << 8;
+        w |= __shfl_down_sync(0xFFFFFFFFu, sb, 8) << 16;
+        w |= __shfl_down_sync(0xFFFFFFFFu, sb, 12) << 24;
+        if ((lane & 15) == 0)
+            *reinterpret_cast<uint32_t*>(scales + (size_t)t * pitch + seg * 8 + (lane >> 4) * 4) = w;
+    }
+    pdl_end();
+}
+
+// ----------------------------------------------------------------- product
+
+struct StreamArgs {
+    const uint8_t* scales;   // [N][K/32]
+    const uint8_t* xscales;  // [T][xpitch]
+    int xpitch;
+    const void* residual;    // [T] rows, ldr elements apart, of the output's type; or null
+    void* out;               // [T] rows, ldo elements apart
+    long long ldr, ldo;
+    int T, N, K;
+    int out_f32;
+};
+
+// out[t][n] = residual + v, rounded once
+__device__ __forceinline__ void store_out(const StreamArgs& a, int t, int n, float v) {
+    if (a.out_f32) {
+        if (a.residual) v += reinterpret_cast<const float*>(a.residual)[(size_t)t * a.ldr + n];
+        reinterpret_cast<float*>(a.out)[(size_t)t * a.ldo + n] = v;
+    } else {
+        if (a.residual)
+            v += __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.residual)[(size_t)t * a.ldr + n] << 16);
+        reinterpret_cast<uint16_t*>(a.out)[(size_t)t * a.ldo + n] = f32_to_bf16_bits(v);
+    }
+}
+
+constexpr int kStreamThreads = 192;
+
+template <int NT>
+struct StreamLayout {
+    static constexpr int kBBytes = NT * kRowBytes;
+    static constexpr int kStage = kABytes + kBBytes;  // a multiple of 1024
+    // two CTAs per SM: at most 110 KB each
+    static constexpr int kFit = (110 * 1024) / kStage;
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kBar = kStages * kStage;
+    static constexpr int kTotal = kBar + 256 + 1024;  // + barriers, alignment slack
+    static_assert(kStages >= 3, "ring depth");
+    static_assert(NT * kMRows * 4 <= kBar, "the partial tile takes the ring's place");
+    static constexpr int kNJ = (NT + 31) / 32;        // scale columns of the tokens
+    // tensor memory: the accumulator, then per stage 32 columns of scale
+    // factors, each 128-k chunk's block on a multiple of 8 columns (weights at
+    // +0 and +8, tokens at +16 and +24)
+    static constexpr int kSfCols = 32;
+    static constexpr int kSfCol0 = NT < 32 ? 32 : NT;
+    static constexpr int kCols = 256;
+    static_assert(kSfCol0 + kStages * kSfCols <= kCols, "tensor memory, half an SM's");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kStreamThreads, 2)
+    linear_stream_kernel(const StreamArgs a, const int splits,
+                         const __grid_constant__ CUtensorMap w_map,
+                         const __grid_constant__ CUtensorMap x_map) {
+    using L = StreamLayout<NT>;
+    constexpr int kStages = L::kStages, kNJ = L::kNJ;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* tma_full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    uint64_t* sf_full = tma_full + kStages;
+    uint64_t* stage_free = sf_full + kStages;
+    uint64_t* acc_full = stage_free + kStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)blockIdx.x % splits;  // the cluster is `splits` neighbours in x
+    const int n0 = (int)blockIdx.x / splits * kMRows, t0 = (int)blockIdx.y * NT;
+    const int KG = a.K / 32;
+    const int nk = (a.K + kBK - 1) / kBK;
+    const int st0 = (int)((long long)nk * rank / splits), st1 = (int)((long long)nk * (rank + 1) / splits);
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&tma_full[s], 1);
+            mbar_init(&sf_full[s], 4);
+            mbar_init(&stage_free[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<false>(tmem_slot, L::kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool done = false;  // this thread's warp saw the finished accumulator
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer
+        if (lane == 0) {
+            auto load_w = [&](int i) {
+                const int s = i % kStages;
+                mbar_arrive_expect_tx(&tma_full[s], (uint32_t)L::kStage);
+                tma_load_2d(smem_u32(smem + s * L::kStage), &w_map, (st0 + i) * kRowBytes, n0, &tma_full[s]);
+            };
+            auto load_x = [&](int i) {
+                const int s = i % kStages;
+                tma_load_2d(smem_u32(smem + s * L::kStage + kABytes), &x_map, (st0 + i) * kRowBytes, t0,
+                            &tma_full[s]);
+            };
+            const int n = st1 - st0, first = min(n, kStages);
+            for (int i = 0; i < first; ++i) load_w(i);
+            pdl_begin();
+            for (int i = 0; i < first; ++i) load_x(i);
+            int i = first;
+            for (; i < n; ++i) {
+                if (!mbar_wait(&stage_free[i % kStages], ((i / kStages) - 1) & 1)) break;
+                load_w(i);
+                load_x(i);
+            }
+            // wait (bounded) until the last loads landed before the CTA can exit
+            for (int d = 0; d < kStages && d < i; ++d) {
+                const int u = i - 1 - d;
+                if (!mbar_wait(&tma_full[u % kStages], (u / kStages) & 1)) break;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        if (lane == 0) {
+            constexpr uint32_t id0 = idesc_mxf4(kMRows, NT, 0), id2 = idesc_mxf4(kMRows, NT, 2);
+            for (int i = 0; i < st1 - st0; ++i) {
+                const int s = i % kStages;
+                const uint32_t par = (i / kStages) & 1;
+                if (!mbar_wait(&tma_full[s], par) || !mbar_wait(&sf_full[s], par)) break;
+                tc_fence_after();
+                const uint64_t ad = sdesc_sw128(smem_u32(smem + s * L::kStage));
+                const uint64_t bd = sdesc_sw128(smem_u32(smem + s * L::kStage + kABytes));
+                const uint32_t sf = tmem + (uint32_t)(L::kSfCol0 + s * L::kSfCols);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // K = 64 each: +32 bytes in the swizzle atom
+                    mma_mxf4(tmem, ad + 2u * kk, bd + 2u * kk, (kk & 1) ? id2 : id0, sf + 8u * (kk >> 1),
+                             sf + 16u + 8u * (kk >> 1), (i | kk) != 0 ? 1u : 0u);
+                mma_commit(&stage_free[s]);
+            }
+            mma_commit(acc_full);  // every MMA issued has completed when this arrives
+            mbar_wait(acc_full, 0);
+        }
+    } else {
+        // ------------------------------------- scale factors, then the drain
+        const int quad = warp & 3;
+        const int wrow = n0 + 32 * quad + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
+        const uint8_t* sa = wrow < a.N ? a.scales + (size_t)wrow * KG : nullptr;
+        const bool vec = KG % 8 == 0 && ((uintptr_t)a.scales & 7) == 0;
+        if (sa)  // this row's scale bytes of the CTA's range, on their way into L2
+            for (int g = 8 * st0; g < min(8 * st1, KG); g += 32)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(sa + g));
+        auto load_sa = [&](int st) {
+            uint2 r = make_uint2(0, 0);
+            if (!sa) return r;
+            if (vec) return __ldg(reinterpret_cast<const uint2*>(sa + 8 * st));
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (8 * st + j < KG) w[j >> 2] |= (uint32_t)__ldg(sa + 8 * st + j) << (8 * (j & 3));
+            return make_uint2(w[0], w[1]);
+        };
+        uint2 an = load_sa(st0);
+        pdl_begin();
+        const uint8_t* sb[kNJ];
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j) {
+            const int t = t0 + 32 * j + lane;
+            sb[j] = (32 * j + lane < NT && t < a.T) ? a.xscales + (size_t)t * a.xpitch : nullptr;
+        }
+        uint2 bn[kNJ];
+        auto load_sb = [&](int st) {
+#pragma unroll
+            for (int j = 0; j < kNJ; ++j)
+                bn[j] = sb[j] ? *reinterpret_cast<const uint2*>(sb[j] + 8 * st) : make_uint2(0, 0);
+        };
+        load_sb(st0);
+        bool ok = true;
+        for (int i = 0; i < st1 - st0 && ok; ++i) {
+            const int s = i % kStages;
+            const uint32_t av[2] = {an.x, an.y};
+            uint32_t bv[2][kNJ];
+#pragma unroll
+            for (int j = 0; j < kNJ; ++j) bv[0][j] = bn[j].x, bv[1][j] = bn[j].y;
+            if (i + 1 < st1 - st0) {
+                an = load_sa(st0 + i + 1);
+                load_sb(st0 + i + 1);
+            }
+            if (i >= kStages && !mbar_wait_warp(&stage_free[s], ((i / kStages) - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();  // after the MMAs that last read these columns
+            const uint32_t col = lane_base + (uint32_t)(L::kSfCol0 + s * L::kSfCols);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                tmem_st_cols<1>(col + 8u * c + (uint32_t)quad, &av[c]);
+                tmem_st_cols<kNJ>(col + 16u + 8u * c, bv[c]);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sf_full[s]);
+        }
+        done = ok && mbar_wait_warp(acc_full, 0);
+        if (done) {
+            tc_fence_after();
+            float* part = reinterpret_cast<float*>(smem);  // [NT][128], over the ring: its loads are used
+            const int ncol = min(NT, a.T - t0);
+#pragma unroll 1
+            for (int c0 = 0; c0 < ncol; c0 += 16) {
+                uint32_t v[16];
+                tmem_ld16_nowait(lane_base + (uint32_t)c0, v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (c0 + i >= ncol) break;
+                    if (splits > 1)
+                        part[(c0 + i) * kMRows + 32 * quad + lane] = __uint_as_float(v[i]);
+                    else if (wrow < a.N)
+                        store_out(a, t0 + c0 + i, wrow, __uint_as_float(v[i]));
+                }
+            }
+            tc_fence_before();
+        }
+    }
+
+    __syncwarp();
+    if (splits > 1) {
+        // the partial tiles of the cluster's CTAs, each element added in rank
+        // order by one thread
+        cluster_sync_all();
+        const int total = min(NT, a.T - t0) * kMRows;
+        const uint32_t base = smem_u32(smem);
+        uint32_t peer[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer[r]) : "r"(base), "r"(r < splits ? r : 0));
+        for (int i = rank * kStreamThreads + tid; i < total; i += splits * kStreamThreads) {
+            float p[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < splits)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[r]) : "r"(peer[r] + 4u * (uint32_t)i));
+            float v = p[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < splits) v += p[r];
+            const int n = n0 + (i & (kMRows - 1));
+            if (n < a.N) store_out(a, t0 + i / kMRows, n, v);
+        }
+        cluster_sync_all();  // no CTA leaves while another reads its partial tile
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<false>(tmem, L::kCols);
+    }
+    pdl_end();
+}
+
+template <int NT>
+cudaError_t launch_stream(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* xscales, int xpitch,
+                          cudaStream_t s) {
+    const size_t smem = StreamLayout<NT>::kTotal;
+    cudaError_t err = ensure_dynamic_smem((const void*)linear_stream_kernel<NT>, smem);
+    if (err != cudaSuccess) return err;
+    CUtensorMap w_map, x_map;
+    err = encode_codes_map(&w_map, p.codes, p.K / 2, (uint64_t)p.N, kRowBytes, kMRows);
+    if (err != cudaSuccess) return err;
+    err = encode_codes_map(&x_map, xcodes, p.K / 2, (uint64_t)p.T, kRowBytes, NT);
+    if (err != cudaSuccess) return err;
+    StreamArgs a;
+    a.scales = p.scales;
+    a.xscales = xscales;
+    a.xpitch = xpitch;
+    a.residual = p.residual;
+    a.out = p.out;
+    a.ldr = p.ldr;
+    a.ldo = p.ldo;
+    a.T = p.T;
+    a.N = p.N;
+    a.K = p.K;
+    a.out_f32 = p.out_f32;
+    const int row_tiles = (p.N + kMRows - 1) / kMRows, tok_tiles = (p.T + NT - 1) / NT;
+    const int nk = (p.K + kBK - 1) / kBK;
+    // split K while the CTAs do not fill two per SM and every split has a stage
+    int splits = 1;
+    while (splits < 8 && 2 * splits <= nk && (long long)row_tiles * tok_tiles * 2 * splits <= 2LL * num_sms())
+        splits *= 2;
+    return launch_pdl_cluster(linear_stream_kernel<NT>, dim3((unsigned)row_tiles * splits, (unsigned)tok_tiles),
+                              dim3(kStreamThreads), smem, s, (unsigned)splits, a, splits, w_map, x_map);
+}
+
+template <bool F32>
+cudaError_t launch_quantize_rows(const LinearMxfp4& p, uint8_t* codes, uint8_t* scales, int pitch,
+                                 cudaStream_t s) {
+    const long long items = (long long)p.T * ((p.K + kBK - 1) / kBK);
+    const int blocks = (int)std::min<long long>((items + 7) / 8, (long long)num_sms() * 8);
+    // 16-byte loads where every row starts on a 16-byte boundary
+    const bool vec = ((uintptr_t)p.x % 16) == 0 && (p.ldx * (F32 ? 4 : 2)) % 16 == 0;
+    return vec ? launch_pdl(quantize_rows_kernel<F32, true>, dim3(blocks), dim3(256), 0, s, p.x, p.ldx, p.T, p.K,
+                            codes, scales, pitch)
+               : launch_pdl(quantize_rows_kernel<F32, false>, dim3(blocks), dim3(256), 0, s, p.x, p.ldx, p.T, p.K,
+                            codes, scales, pitch);
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// bytes of a token's scale row: whole stages
+int xscale_pitch(int K) { return (K + kBK - 1) / kBK * 8; }
+
+}  // namespace
+
+size_t linear_mxfp4_workspace(int T, int N, int K) {
+    (void)N;
+    return align256((size_t)T * (K / 2)) + align256((size_t)T * xscale_pitch(K));
+}
+
+cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStream_t s) {
+    uint8_t* codes = reinterpret_cast<uint8_t*>(workspace);
+    uint8_t* scales = codes + align256((size_t)p.T * (p.K / 2));
+    const int pitch = xscale_pitch(p.K);
+    cudaError_t err = p.x_f32 ? launch_quantize_rows<true>(p, codes, scales, pitch, s)
+                              : launch_quantize_rows<false>(p, codes, scales, pitch, s);
+    if (err != cudaSuccess) return err;
+    // the narrowest token tile that holds the batch
+    if (p.T <= 16) return launch_stream<16>(p, codes, scales, pitch, s);
+    if (p.T <= 32) return launch_stream<32>(p, codes, scales, pitch, s);
+    if (p.T <= 64) return launch_stream<64>(p, codes, scales, pitch, s);
+    return launch_stream<128>(p, codes, scales, pitch, s);
+}
+
+cudaError_t read_device_error_linear(int* flag, int clear) {
+    int wait = 0;
+    cudaError_t err = cudaMemcpyFromSymbol(&wait, g_device_error, sizeof(int));
+    if (err != cudaSuccess) return err;
+    *flag = wait ? 1 : 0;
+    if (!clear) return cudaSuccess;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+}
+
+}  // namespace moe

@@ -200,7 +200,9 @@ moe_status_t moe_device_error(int* flag, int clear) {
     if (err == cudaSuccess) err = read_device_error_decode(&b, clear);
     if (err == cudaSuccess) err = read_device_error_mxfp4act(&c, clear);
     if (err == cudaSuccess) err = read_device_error_fp8x2(&d, clear);
-    *flag = a | b | c | d;
+    int e = 0;
+    if (err == cudaSuccess) err = read_device_error_linear(&e, clear);
+    *flag = a | b | c | d | e;
     return cuda_status(err);
 }
 
@@ -928,6 +930,51 @@ moe_status_t moe_ffn_mxfp4act(const uint16_t* x, const uint8_t* w13, const uint8
     if (st != MOE_OK) return st;
     return moe_ffn_mxfp4act_down(w2, s2, topk_w, sorted_pairs, inv_pairs, tile_expert, num_tiles, T,
                                  H, I, Et, Kt, tile_m, out, workspace, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------ dense projection
+
+static bool linear_shape_ok(int T, int N, int K) {
+    return K % 32 == 0 && K <= 65536 && N <= (1 << 24) && T <= (1 << 20);
+}
+
+size_t moe_linear_mxfp4act_workspace_size(int T, int N, int K) {
+    if (T < 0 || N < 1 || K < 1 || !linear_shape_ok(T, N, K)) return 0;
+    return linear_mxfp4_workspace(T, N, K);
+}
+
+moe_status_t moe_linear_mxfp4act(const void* x, moe_dtype_t x_type, int64_t ldx, const uint8_t* codes,
+                                 const uint8_t* scales, const void* residual, int64_t ldr, void* out,
+                                 moe_dtype_t out_type, int64_t ldo, int T, int N, int K,
+                                 void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (T < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+    if ((x_type != MOE_DTYPE_BF16 && x_type != MOE_DTYPE_F32) ||
+        (out_type != MOE_DTYPE_BF16 && out_type != MOE_DTYPE_F32))
+        return MOE_ERR_INVALID_ARG;
+    if (!linear_shape_ok(T, N, K)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    const size_t xa = x_type == MOE_DTYPE_F32 ? 4 : 2, oa = out_type == MOE_DTYPE_F32 ? 4 : 2;
+    if (!ptrs_ok({x}, xa) || !ptrs_ok({out}, oa) || (residual && !aligned(residual, oa)) ||
+        !ptrs_ok({codes, workspace}, 16) || !ptrs_ok({scales}, 4))
+        return MOE_ERR_INVALID_ARG;
+    // rows that are only read may overlap (0: one row for every token), written ones may not
+    if (ldx < 0 || (residual && ldr < 0) || ldo < N) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < linear_mxfp4_workspace(T, N, K)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    LinearMxfp4 p;
+    p.x = x;
+    p.x_f32 = x_type == MOE_DTYPE_F32;
+    p.ldx = ldx;
+    p.codes = codes;
+    p.scales = scales;
+    p.residual = residual;
+    p.ldr = residual ? ldr : 0;
+    p.out = out;
+    p.out_f32 = out_type == MOE_DTYPE_F32;
+    p.ldo = ldo;
+    p.T = T;
+    p.N = N;
+    p.K = K;
+    return cuda_status(launch_linear_mxfp4(p, workspace, stream));
 }
 
 }  // extern "C"

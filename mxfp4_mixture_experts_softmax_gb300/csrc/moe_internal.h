@@ -287,6 +287,25 @@ cudaError_t launch_split_rows(const uint16_t* x, int cols, int rows, const int32
                               cudaStream_t s);
 cudaError_t read_device_error_fp8x2(int* flag, int clear);
 
+// A dense projection with MXFP4 weights and activations quantised inside the
+// call (linear_mxfp4.cu).
+struct LinearMxfp4 {
+    const void* x;             // [T] rows of K values, ldx elements apart
+    int x_f32;                 // fp32 rows, else bf16
+    long long ldx;
+    const uint8_t* codes;      // [N][K/2]
+    const uint8_t* scales;     // [N][K/32]
+    const void* residual;      // [T] rows, ldr elements apart, of out's type; or null
+    long long ldr;
+    void* out;                 // [T] rows, ldo elements apart
+    int out_f32;               // fp32, else bf16
+    long long ldo;
+    int T, N, K;
+};
+size_t linear_mxfp4_workspace(int T, int N, int K);
+cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStream_t s);
+cudaError_t read_device_error_linear(int* flag, int clear);
+
 // grouping of one dense expert over T tokens (Kt = 1); ones[T] = 1 if given
 cudaError_t launch_identity_perm(int T, int tile_m, int cap, int max_tiles, int32_t* sorted_pairs,
                                  int32_t* tile_expert, int32_t* num_tiles, float* ones,

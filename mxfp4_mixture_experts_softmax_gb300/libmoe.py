@@ -25,6 +25,9 @@ MOE_PATH_DECODE = 1
 MOE_PATH_PREFILL = 2
 MOE_PATH_PREFILL_FP8X2 = 3
 
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F32 = 1
+
 EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_route_ex", "moe_permute_capacity",
            "moe_permute_max_tiles", "moe_permute", "moe_route_permute", "moe_ffn_workspace_size",
            "moe_ffn",
@@ -34,7 +37,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_route_ex", "moe
            "moe_selftest_wait_timeout", "moe_selftest_wait_split", "moe_set_gemm_events",
            "moe_quantize_mxfp4", "moe_ffn_mxfp4act_workspace_size",
            "moe_ffn_mxfp4act", "moe_ffn_mxfp4act_gate_up", "moe_ffn_mxfp4act_down",
-           "moe_ffn_mxfp4act_h_offsets", "moe_ffn_down_combine", "moe_split_e4m3x2", "moe_ffn_auto_path_shape")
+           "moe_ffn_mxfp4act_h_offsets", "moe_ffn_down_combine", "moe_split_e4m3x2", "moe_ffn_auto_path_shape",
+           "moe_linear_mxfp4act_workspace_size", "moe_linear_mxfp4act")
 
 # bytes of the fixed device scratch behind moe_ffn_noalloc (include/moe.h)
 MOE_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -135,6 +139,12 @@ def load(build: bool = True):
         L.moe_ffn_mxfp4act_down.restype = ci
         L.moe_ffn_mxfp4act_h_offsets.argtypes = [ci, ci, ci, ci, ci, ci, vp, vp]
         L.moe_ffn_mxfp4act_h_offsets.restype = ci
+        i64 = ctypes.c_int64
+        L.moe_linear_mxfp4act_workspace_size.argtypes = [ci, ci, ci]
+        L.moe_linear_mxfp4act_workspace_size.restype = sz
+        L.moe_linear_mxfp4act.argtypes = [vp, ci, i64, vp, vp, vp, i64, vp, ci, i64, ci, ci, ci, vp, sz,
+                                          vp]
+        L.moe_linear_mxfp4act.restype = ci
         L.moe_device_error.argtypes = [vp, ci]
         L.moe_device_error.restype = ci
         _lib = L
@@ -549,3 +559,54 @@ def mxfp4act_h_views(workspace, T: int, H: int, I: int, Et: int, Kt: int, tile_m
     codes = workspace[co.value:co.value + cap * (I // 2)].view(cap, I // 2)
     scales = workspace[so.value:so.value + cap * (I // 32)].view(cap, I // 32)
     return codes, scales
+
+
+# ------------------------------------------------------------- dense projections
+
+def moe_linear_mxfp4act_workspace_size(T: int, N: int, K: int) -> int:
+    return int(load().moe_linear_mxfp4act_workspace_size(T, N, K))
+
+
+def alloc_workspace_linear(T: int, N: int, K: int, device="cuda"):
+    import torch
+    n = moe_linear_mxfp4act_workspace_size(T, N, K)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _rows(t, what: str):
+    """(element type, row stride) of a 2D CUDA tensor whose rows are contiguous."""
+    import torch
+    types = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+    assert t.is_cuda and t.dim() == 2, f"{what} must be a 2D CUDA tensor"
+    assert t.dtype in types, f"{what} must be bfloat16 or float32"
+    assert t.shape[1] <= 1 or t.stride(1) == 1, f"{what}'s rows must be contiguous"
+    # a single row has no neighbour: its stride means nothing
+    return types[t.dtype], max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def moe_linear_mxfp4act(x, codes, scales, residual=None, out=None, out_dtype=None, workspace=None,
+                        stream=None):
+    """bf16 or fp32 x [T, K] times MXFP4 weights (codes [N, K/2], scales [N, K/32]), x quantised
+    to MXFP4 inside the call, plus residual [T, N] (include/moe.h).  x, residual and out may be
+    row slices of wider tensors; out_dtype: torch.bfloat16 (default) or torch.float32."""
+    import torch
+    T, K = x.shape
+    N = codes.shape[0]
+    _dev(codes, "codes")
+    _dev(scales, "scales")
+    assert codes.shape == (N, K // 2) and scales.shape == (N, K // 32), "weights do not match x"
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+    assert out.shape == (T, N) and out_dtype in (None, out.dtype)
+    x_type, ldx = _rows(x, "x")
+    out_type, ldo = _rows(out, "out")
+    ldr = 0
+    if residual is not None:
+        assert residual.shape == (T, N) and residual.dtype == out.dtype, "residual must match out"
+        _, ldr = _rows(residual, "residual")
+    if workspace is None:
+        workspace = alloc_workspace_linear(T, N, K, x.device)
+    _check(load().moe_linear_mxfp4act(_ptr(x), x_type, ldx, _ptr(codes), _ptr(scales), _ptr(residual), ldr,
+                                      _ptr(out), out_type, ldo, T, N, K, _ptr(workspace),
+                                      workspace.numel(), _stream(stream)), "moe_linear_mxfp4act")
+    return out
