@@ -531,6 +531,54 @@ moe_status_t moe_ffn_mxfp4act_h_offsets(int T, int H, int I, int Et, int Kt, int
                                         size_t* codes_offset, size_t* scales_offset);
 
 /*
+ * ------------------------------------------------ the layer for a few tokens
+ * moe_layer_few -- the whole layer, router product included, for up to 16
+ * tokens in one launch: what a step of a few sequences spends between launches
+ * and re-reading its own intermediates is most of its time [VS, "kernels and
+ * graph capture"].
+ *
+ *   x              bf16 [T, H].
+ *   w_router       bf16 [E, H]: router logits l = w_router x (fp32 sums).
+ *   w_shared_gate  bf16 [H], or NULL: the shared expert's weight is
+ *                  sigmoid(w_shared_gate . x), or 1.  Only with with_shared.
+ *   w13, s13, w2, s2: the experts' weights as for moe_ffn, E of them and, with
+ *                  with_shared, the shared one as expert E.
+ *   out            bf16 [T, H] out; may be x itself.
+ *   topk_ids, topk_w  int32 and fp32 [T, K + (with_shared ? 1 : 0)] out, as
+ *                  moe_route_ex gives them for those logits; either may be NULL.
+ * out_t = bf16(sum of w_te W2[e] h_te), h_te = silu(W_gate[e] x_t) * (W_up[e] x_t).
+ * As in moe_ffn's decode path x enters the products as f16 scaled per row by a
+ * power of two (exact for elements at least 2^-29 of their row's largest).  h is
+ * not rounded to bf16: it is kept in fp32 and enters the down product as f16
+ * scaled per (token, expert) row by a power of two (11 significant bits).
+ * Sums are fp32, over k in blocks of 32 and then over the experts, in an order
+ * that depends on the sizes and the touched experts alone: results do not vary
+ * from run to run.  Weight scale bytes 7..247.  A token whose x holds an infinity
+ * or a NaN gets NaN outputs; other tokens are not touched.
+ * Limits: T <= MOE_LAYER_FEW_MAX_T (0 is a no-op), H % 32 == I % 32 == 0, I <= 8192,
+ * H <= 8192 (T <= 8) or 4096, E <= 1024, K <= min(E, 32).  Pointers 16-byte
+ * aligned; s13, s2, topk_ids and topk_w 4-byte.
+ *
+ * The launch is cooperative: its blocks wait for one another, so they start
+ * when the GPU has room for all of them.  Their barriers count in the first 256
+ * bytes of the workspace, which must be zero when a call starts:
+ * moe_layer_few_workspace_init() zeroes them once after the workspace is
+ * allocated, and every call leaves them zero.  (After a call that gave up,
+ * moe_device_error value 1, initialise again.)  The rest of the workspace needs
+ * no initialisation.  Calls that may run at the same time need workspaces of
+ * their own.  moe_layer_few_workspace_size returns 0 for sizes outside the
+ * limits.
+ */
+#define MOE_LAYER_FEW_MAX_T 16
+size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int K, int with_shared);
+moe_status_t moe_layer_few_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream);
+moe_status_t moe_layer_few(const uint16_t* x, const uint16_t* w_router, const uint16_t* w_shared_gate,
+                           const uint8_t* w13, const uint8_t* s13, const uint8_t* w2, const uint8_t* s2,
+                           int T, int H, int I, int E, int K, int with_shared, int renormalize,
+                           uint16_t* out, int32_t* topk_ids, float* topk_w, void* workspace,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/*
  * ------------------------------------------------------- dense projections
  * The projections around the layer (attention, a dense FFN, the output head)
  * with the same weight format.  The pages name the format and the GEMM (OR,

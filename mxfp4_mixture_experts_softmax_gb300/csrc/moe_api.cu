@@ -201,8 +201,10 @@ moe_status_t moe_device_error(int* flag, int clear) {
     if (err == cudaSuccess) err = read_device_error_mxfp4act(&c, clear);
     if (err == cudaSuccess) err = read_device_error_fp8x2(&d, clear);
     int e = 0;
+    int f = 0;
     if (err == cudaSuccess) err = read_device_error_linear(&e, clear);
-    *flag = a | b | c | d | e;
+    if (err == cudaSuccess) err = read_device_error_few(&f, clear);
+    *flag = a | b | c | d | e | f;
     return cuda_status(err);
 }
 
@@ -975,6 +977,59 @@ moe_status_t moe_linear_mxfp4act(const void* x, moe_dtype_t x_type, int64_t ldx,
     p.N = N;
     p.K = K;
     return cuda_status(launch_linear_mxfp4(p, workspace, stream));
+}
+
+// ------------------------------------------------ the layer for a few tokens
+
+static moe_status_t check_few(int T, int H, int I, int E, int K) {
+    if (T < 0 || H < 1 || I < 1 || E < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+    if (T > kFewMaxT || H % 32 || I % 32 || H > few_max_h(T) || I > kFewMaxI || E > 1024 || K > 32 || K > E)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int K, int with_shared) {
+    if (check_few(T, H, I, E, K) != MOE_OK) return 0;
+    return layer_few_workspace(T, H, I, E, K + (with_shared ? 1 : 0));
+}
+
+moe_status_t moe_layer_few_workspace_init(void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!ptrs_ok({workspace}, 16)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < kFewSyncBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    return cuda_status(cudaMemsetAsync(workspace, 0, kFewSyncBytes, stream));
+}
+
+moe_status_t moe_layer_few(const uint16_t* x, const uint16_t* w_router, const uint16_t* w_shared_gate,
+                           const uint8_t* w13, const uint8_t* s13, const uint8_t* w2, const uint8_t* s2,
+                           int T, int H, int I, int E, int K, int with_shared, int renormalize,
+                           uint16_t* out, int32_t* topk_ids, float* topk_w, void* workspace,
+                           size_t ws_bytes, cudaStream_t stream) {
+    const moe_status_t st = check_few(T, H, I, E, K);
+    if (st != MOE_OK || T == 0) return st;
+    if (!ptrs_ok({x, w_router, w13, w2, out, workspace}, 16) || !ptrs_ok({s13, s2}, 4) ||
+        !aligned(w_shared_gate, 16) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+        (w_shared_gate && !with_shared))
+        return MOE_ERR_INVALID_ARG;
+    LayerFew p;
+    p.x = x;
+    p.w_router = w_router;
+    p.w_shared_gate = w_shared_gate;
+    p.w13 = w13;
+    p.s13 = s13;
+    p.w2 = w2;
+    p.s2 = s2;
+    p.T = T;
+    p.H = H;
+    p.I = I;
+    p.E = E;
+    p.K = K;
+    p.shared = with_shared ? 1 : 0;
+    p.renormalize = renormalize ? 1 : 0;
+    p.out = out;
+    p.topk_ids = topk_ids;
+    p.topk_w = topk_w;
+    if (ws_bytes < layer_few_workspace(T, H, I, E, K + p.shared)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    return cuda_status(launch_layer_few(p, workspace, stream));
 }
 
 }  // extern "C"

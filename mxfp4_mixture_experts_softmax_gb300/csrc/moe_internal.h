@@ -306,6 +306,26 @@ size_t linear_mxfp4_workspace(int T, int N, int K);
 cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStream_t s);
 cudaError_t read_device_error_linear(int* flag, int clear);
 
+// The whole layer for a few tokens in one cooperative launch (layer_few.cu).
+constexpr int kFewMaxT = 16, kFewMaxI = 8192;
+// widest H for this many tokens (the x fragments stay in registers)
+inline int few_max_h(int T) { return T > 8 ? 4096 : 8192; }
+struct LayerFew {
+    const uint16_t* x;              // bf16 [T][H]
+    const uint16_t* w_router;       // bf16 [E][H]
+    const uint16_t* w_shared_gate;  // bf16 [H] or null
+    const uint8_t *w13, *s13, *w2, *s2;
+    int T, H, I, E, K, shared, renormalize;
+    uint16_t* out;                  // bf16 [T][H]
+    int32_t* topk_ids;              // [T][K + shared] or null
+    float* topk_w;                  // [T][K + shared] or null
+};
+// the first kFewSyncBytes of the workspace are zero between calls
+constexpr size_t kFewSyncBytes = 256;
+size_t layer_few_workspace(int T, int H, int I, int E, int Kt);
+cudaError_t launch_layer_few(const LayerFew& p, void* workspace, cudaStream_t s);
+cudaError_t read_device_error_few(int* flag, int clear);
+
 // grouping of one dense expert over T tokens (Kt = 1); ones[T] = 1 if given
 cudaError_t launch_identity_perm(int T, int tile_m, int cap, int max_tiles, int32_t* sorted_pairs,
                                  int32_t* tile_expert, int32_t* num_tiles, float* ones,

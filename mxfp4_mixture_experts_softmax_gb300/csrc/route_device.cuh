@@ -28,8 +28,9 @@ __device__ __forceinline__ float key_to_float(uint32_t k) {
 }
 
 // Routes logits row l (E values) into ids / w (Kt entries each); called by all
-// 32 lanes of a warp.  shared_weight is the shared slot's weight.
-template <int VPL>
+// 32 lanes of a warp.  shared_weight is the shared slot's weight.  COHERENT:
+// the logits were written by this kernel, so they are read from L2.
+template <int VPL, bool COHERENT = false>
 __device__ __forceinline__ void route_token(const float* __restrict__ l, int E, int K,
                                             int with_shared, int renormalize, float shared_weight,
                                             int32_t* ids, float* w, int lane) {
@@ -38,7 +39,7 @@ __device__ __forceinline__ void route_token(const float* __restrict__ l, int E, 
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + 32 * i;
-        v[i] = e < E ? __ldg(l + e) : -INFINITY;
+        v[i] = e < E ? (COHERENT ? __ldcg(l + e) : __ldg(l + e)) : -INFINITY;
         m = fmaxf(m, v[i]);
     }
 #pragma unroll

@@ -38,10 +38,13 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_route_ex", "moe
            "moe_quantize_mxfp4", "moe_ffn_mxfp4act_workspace_size",
            "moe_ffn_mxfp4act", "moe_ffn_mxfp4act_gate_up", "moe_ffn_mxfp4act_down",
            "moe_ffn_mxfp4act_h_offsets", "moe_ffn_down_combine", "moe_split_e4m3x2", "moe_ffn_auto_path_shape",
-           "moe_linear_mxfp4act_workspace_size", "moe_linear_mxfp4act")
+           "moe_linear_mxfp4act_workspace_size", "moe_linear_mxfp4act",
+           "moe_layer_few_workspace_size", "moe_layer_few_workspace_init", "moe_layer_few")
 
 # bytes of the fixed device scratch behind moe_ffn_noalloc (include/moe.h)
 MOE_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
+# most tokens of moe_layer_few (include/moe.h)
+MOE_LAYER_FEW_MAX_T = 16
 # batches up to this many tokens route and permute in one launch (include/moe.h)
 MOE_ROUTE_PERMUTE_FUSED_MAX_T = 32
 
@@ -145,6 +148,12 @@ def load(build: bool = True):
         L.moe_linear_mxfp4act.argtypes = [vp, ci, i64, vp, vp, vp, i64, vp, ci, i64, ci, ci, ci, vp, sz,
                                           vp]
         L.moe_linear_mxfp4act.restype = ci
+        L.moe_layer_few_workspace_size.argtypes = [ci] * 6
+        L.moe_layer_few_workspace_size.restype = sz
+        L.moe_layer_few_workspace_init.argtypes = [vp, sz, vp]
+        L.moe_layer_few_workspace_init.restype = ci
+        L.moe_layer_few.argtypes = [vp] * 7 + [ci] * 7 + [vp, vp, vp, vp, sz, vp]
+        L.moe_layer_few.restype = ci
         L.moe_device_error.argtypes = [vp, ci]
         L.moe_device_error.restype = ci
         _lib = L
@@ -559,6 +568,64 @@ def mxfp4act_h_views(workspace, T: int, H: int, I: int, Et: int, Kt: int, tile_m
     codes = workspace[co.value:co.value + cap * (I // 2)].view(cap, I // 2)
     scales = workspace[so.value:so.value + cap * (I // 32)].view(cap, I // 32)
     return codes, scales
+
+
+# ------------------------------------------------- the layer for a few tokens
+
+def moe_layer_few_workspace_size(T: int, H: int, I: int, E: int, K: int, with_shared: bool) -> int:
+    return int(load().moe_layer_few_workspace_size(T, H, I, E, K, int(with_shared)))
+
+
+def alloc_workspace_few(T: int, H: int, I: int, E: int, K: int, with_shared: bool = True,
+                        device="cuda"):
+    """An initialised workspace for moe_layer_few, to be kept from call to call (one for each
+    stream that calls may overlap on)."""
+    import torch
+    n = moe_layer_few_workspace_size(T, H, I, E, K, with_shared)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def moe_layer_few_workspace_init(workspace, stream=None):
+    """Zero the barrier counters of a workspace that did not come from alloc_workspace_few
+    (include/moe.h)."""
+    _check(load().moe_layer_few_workspace_init(_ptr(workspace), workspace.numel(), _stream(stream)),
+           "moe_layer_few_workspace_init")
+
+
+def moe_layer_few(x, w_router, w13, s13, w2, s2, K: int, with_shared: bool = True,
+                  renormalize: bool = True, w_shared_gate=None, out=None, topk_ids=None, topk_w=None,
+                  workspace=None, stream=None):
+    """The whole layer for up to 16 tokens in one launch: bf16 x [T, H], router weights bf16
+    [E, H], expert weights as for moe_ffn -> (bf16 out [T, H], int32 ids [T, Kt], fp32 weights
+    [T, Kt]).  w_shared_gate (bf16 [H], optional): the shared expert's weight is
+    sigmoid(w_shared_gate . x).  workspace: from alloc_workspace_few (include/moe.h)."""
+    import torch
+    T, H = x.shape
+    E, I = w_router.shape[0], w13.shape[1] // 2
+    Kt, Et = K + (1 if with_shared else 0), E + (1 if with_shared else 0)
+    for t in (x, w_router, w13, s13, w2, s2):
+        _dev(t, "layer input")
+    bf16 = torch.bfloat16
+    assert x.dtype == bf16 and w_router.dtype == bf16 and w_router.shape[1] == H
+    if w13.shape != (Et, 2 * I, H // 2) or w2.shape != (Et, H, I // 2):
+        raise ValueError("weights must hold E experts plus the shared one when with_shared")
+    assert s13.shape == (Et, 2 * I, H // 32) and s2.shape == (Et, H, I // 32)
+    if w_shared_gate is not None:
+        _dev(w_shared_gate, "w_shared_gate")
+        assert w_shared_gate.dtype == bf16 and w_shared_gate.shape == (H,)
+    if out is None:
+        out = torch.empty((T, H), dtype=bf16, device=x.device)
+    if topk_ids is None:
+        topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=x.device)
+    if topk_w is None:
+        topk_w = torch.empty((T, Kt), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = alloc_workspace_few(T, H, I, E, K, with_shared, x.device)
+    _check(load().moe_layer_few(_ptr(x), _ptr(w_router), _ptr(w_shared_gate), _ptr(w13), _ptr(s13),
+                                _ptr(w2), _ptr(s2), T, H, I, E, K, int(with_shared), int(renormalize),
+                                _ptr(out), _ptr(topk_ids), _ptr(topk_w), _ptr(workspace),
+                                workspace.numel(), _stream(stream)), "moe_layer_few")
+    return out, topk_ids, topk_w
 
 
 # ------------------------------------------------------------- dense projections
