@@ -549,14 +549,14 @@ moe_status_t moe_ffn_mxfp4act_h_offsets(int T, int H, int I, int Et, int Kt, int
  * out_t = bf16(sum of w_te W2[e] h_te), h_te = silu(W_gate[e] x_t) * (W_up[e] x_t).
  * As in moe_ffn's decode path x enters the products as f16 scaled per row by a
  * power of two (exact for elements at least 2^-29 of their row's largest).  h is
- * not rounded to bf16: it is kept in fp32 and enters the down product as f16
- * scaled per (token, expert) row by a power of two (11 significant bits).
- * Sums are fp32, over k in blocks of 32 and then over the experts, in an order
- * that depends on the sizes and the touched experts alone: results do not vary
- * from run to run.  Weight scale bytes 7..247.  A token whose x holds an infinity
+ * not rounded to bf16: it enters the down product as f16 scaled by powers of two
+ * (11 significant bits; elements below 2^-25 of the largest |h| of their token and
+ * expert are dropped).
+ * Sums are fp32, over k in blocks of 32 and then over a token's slots in
+ * ascending order; results do not vary from run to run.  Weight scale bytes 1..254.  A token whose x holds an infinity
  * or a NaN gets NaN outputs; other tokens are not touched.
- * Limits: T <= MOE_LAYER_FEW_MAX_T (0 is a no-op), H % 32 == I % 32 == 0, I <= 8192,
- * H <= 8192 (T <= 8) or 4096, E <= 1024, K <= min(E, 32).  Pointers 16-byte
+ * Limits: T <= MOE_LAYER_FEW_MAX_T (0 is a no-op), H % 32 == I % 32 == 0, H <= 8192,
+ * I <= 8192, E <= 1024, K <= min(E, 32).  Pointers 16-byte
  * aligned; s13, s2, topk_ids and topk_w 4-byte.
  *
  * The launch is cooperative: its blocks wait for one another, so they start

@@ -10,33 +10,44 @@
 // What bounds it: the weights of the touched experts are read once (11 x 6.7
 // MB for one token of a 4096/1024 layer with top-10 of 512 and a shared
 // expert) and everything else is latency, so one grid of one CTA per SM keeps
-// one TMA ring running through all phases and only two grid-wide barriers
-// stand between them (logits complete; h complete).  While the CTAs meet at a
+// one TMA ring running through all phases and three grid-wide barriers stand
+// between them (logits complete; h complete; y complete).  While the CTAs meet at a
 // barrier the ring fills with the next phase's weights: the shared expert's
 // before the routing is known, W2's before h is.
 //
-// Weights are the M side of m16n8k16 MMAs, tokens the N side (8 per n-tile):
-// all tokens are multiplied with every touched expert, which costs nothing at
-// N = 8, and an n-tile none of whose tokens chose the expert is skipped.  A
-// slot is 16 weight rows x 256 k (2 KB of codes in the 128-byte TMA swizzle),
-// a stage 16 slots, one per consumer warp:
-//   gate_up  a unit is 8 gate and the 8 matching up rows of one expert over
-//            all of H, one slot per 256 k: warp w always multiplies the same
-//            256 k, so its x fragment stays in registers for the whole phase
-//            (f16 rows scaled by a power of two, as in ffn_decode.cu, exact for
-//            elements within 2^29 of the row's largest).  Units go round the CTAs.
-//   down     16 output rows x the slots (expert, 256 of I), in one sequence that
-//            is cut into equal ranges, one per CTA.  A warp adds its slots'
-//            products, times routing weight, into registers until the output
-//            rows change.  Rows that a cut divides are joined by the CTA that
-//            finishes last, adding the CTAs' partial sums in their order: the
-//            result does not depend on timing.
-// h stays in fp32 between the phases; the down product reads it as f16 scaled by
-// a power of two per (token, expert) row (11 significant bits for elements
-// within 2^14 of the row's largest, 2^-25 of that largest below).
-// Warps: 16 consumers, one producer (TMA), one epilogue (adds the consumers'
-// partial sums over k, SwiGLU, stores).  Every wait is bounded (mbar_wait,
-// grid_wait).
+// Weights are the M side of m16n8k16 MMAs, tokens the N side.  The work list holds
+// an entry per touched expert and 8 of its tokens (an expert with 9 to 16 tokens has two
+// entries and is streamed twice, the second time from L2).  A slot is 16
+// weight rows x 256 k (2 KB of codes in the 128-byte TMA swizzle), a stage
+// up to 16 slots, one per consumer warp, and their scale bytes:
+//   gate_up  a unit is 8 gate and the 8 matching up rows of one entry over all
+//            of H, one slot per 256 k.  Each CTA takes an equal share of the
+//            shared expert's units and a contiguous range of the others, so that a
+//            warp keeps its x fragment (its 256 k of the entry's tokens) in
+//            registers until the entry changes, once or twice in a call.  x
+//            enters as f16 rows scaled by a power of two, as in ffn_decode.cu
+//            (exact for elements within 2^29 of the row's largest).
+//   down     an item is 16 output rows of one entry, one slot per 256 of I; each
+//            CTA takes a contiguous range of the items, an entry's rows next to
+//            each other, so the h fragment too stays in registers.  y goes to the
+//            workspace in fp32 by (token, expert) pair; after a third barrier
+//            each CTA adds up its share of the outputs, a token's pairs in slot
+//            order, times routing weight.
+// What a warp does for a stage beside its products (waits, arrivals, handing its sums
+// over) takes longer than one slot's products, so the consumers take the stages two
+// at a time, and one warp turns the scale bytes into fp32 factors for all of them
+// (each of the four lanes that share a row would otherwise do it again: 130 of the
+// 330 cycles that 16 warps take per slot and scheduler).
+// h passes between the phases as f16 with a power of two per 8 values (11
+// significant bits); the down product brings a pair's row to one power of two
+// (elements below 2^-14 of the row's largest keep fewer bits, those below 2^-25 of
+// it are dropped).  No result depends on timing.
+// Warps: 16 consumers, one producer (TMA), one for the scale factors, two epilogue
+// warps, one per stage of a pair (adding the consumers' partial sums over k, SwiGLU,
+// stores).  Every wait
+// is bounded (mbar_wait, grid_wait).
+#include <string.h>
+
 #include <algorithm>
 
 #include "moe_internal.h"
@@ -49,13 +60,18 @@ namespace {
 constexpr int kConsumerWarps = 16;
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kProducerWarp = kConsumerWarps;
-constexpr int kThreads = kConsumers + 64;  // the last warp is the epilogue
+constexpr int kScaleWarp = kConsumerWarps + 1;
+constexpr int kEpiWarp0 = kConsumerWarps + 2;
+constexpr int kThreads = kConsumers + 4 * 32;
 constexpr int kSlotBytes = 16 * 128;
-constexpr int kStageBytes = kConsumerWarps * kSlotBytes;
+constexpr int kCodeBytes = kConsumerWarps * kSlotBytes;    // a stage's codes,
+constexpr int kScaleBytes = kConsumerWarps * 16 * 8;       // its scale bytes
+constexpr int kFactorRow = kConsumerWarps * 32 + 16;       // and the factors made of them: 8 floats a slot,
+constexpr int kFactorBytes = 16 * kFactorRow;              // rows 4 banks apart
+constexpr int kStageBytes = (kCodeBytes + kScaleBytes + kFactorBytes + 1023) / 1024 * 1024;
 constexpr int kSmemLimit = 232448;
-constexpr int kMaxList = 528;   // touched experts, and (token, slot) pairs: 16 * 33
-constexpr int kMaxGrid = 256;   // CTAs that the workspace holds partial sums of
-constexpr int kMaxTasks = 64;   // router dot products (row x k range) of one CTA
+constexpr int kMaxPairs = 528;  // (token, slot) pairs: 16 * 33; also the most list entries
+constexpr int kMaxGrid = 256;
 
 struct FewArgs {
     const uint16_t* x;       // [T][H] bf16
@@ -66,38 +82,43 @@ struct FewArgs {
     uint16_t* out;           // [T][H] bf16
     int32_t* ids;            // [T][Kt] or null
     float* w;                // [T][Kt] or null
-    uint32_t* sync;          // [3] barrier counters, zero between calls
-    float* logits;           // [T][E + 1]: the last one the shared expert's gate
+    uint32_t* sync;          // [4] barrier counters, zero between calls
+    float* logits;           // [T][E + 1]: column E the shared expert's gate
     uint32_t* hmax;          // [T * Kt] largest |h| of a pair, as bits
-    uint32_t* joined;        // [H / 16] CTAs that left a partial sum of these output rows
-    float* h;                // [T * Kt][I]
-    float4* partial;         // [grid][2][NT * 32] partial sums of cut output rows
+    uint16_t* h;             // [T * Kt][I] f16, times 2^shift of its 8 values
+    int8_t* hshift;          // [T * Kt][shift_pitch(I)], see shift_at
+    float* y;                // [T * Kt][H] expert outputs by pair
     int T, H, I, E, K, shared, renorm;
-    // decode group factor 2^(s-126) as fp32 bits s * exp_one + exp_bias, runtime
-    // values so that the multiply-add stays one instruction
-    uint32_t exp_one, exp_bias;
+    int router_rows;         // rows of [Wr; gate] per CTA, at most 16
 };
 
-template <int NT>
-struct FewLayout {
-    static constexpr int kPartBytes = NT * kConsumerWarps * 32 * 16;  // one partial-sum buffer
-    static constexpr int kListBytes = kMaxList * (4 + 4 + 4) + 16 * 4 + 64;
-    static constexpr int kFixed = 2 * kPartBytes + kListBytes + 256 + 1024;
-    static constexpr int kStages = (kSmemLimit - kFixed) / kStageBytes;
-    static_assert(kStages >= 4, "ring depth");
-    static constexpr int kPart = kStages * kStageBytes;
-    static constexpr int kList = kPart + 2 * kPartBytes;
-    static constexpr int kBar = (kList + kListBytes + 7) / 8 * 8;
-    static constexpr int kTotal = kBar + 256 + 1024;
-    static_assert(kTotal <= kSmemLimit, "shared memory");
-    // scratch of the routing phase, over the partial-sum buffers
-    static constexpr int kMask = kPart;                 // [1025] token masks by expert
-    static constexpr int kFirst = kMask + 1028 * 4;     // [1025] first pair by expert (16 bits)
-    static constexpr int kIds = kFirst + 1028 * 2;      // [16][33]
-    static constexpr int kW = kIds + 16 * 33 * 4;
-    static constexpr int kRed = kW + 16 * 33 * 4;       // [kMaxTasks][16]
-    static_assert(kRed + kMaxTasks * 16 * 4 + 256 <= kList, "routing scratch");
+// The weights as the TMA reads them: whole 256-k slices (w13 [slice][gate, up][row],
+// w2 [slice][row]), the first 16 in one box, the rest of a row of more than 16 in
+// another, and what is left of a row past its last whole slice; and the scale bytes.
+struct FewMaps {
+    CUtensorMap w13, w13_rest, w13_tail, w2, w2_rest, w2_tail, s13, s2;
 };
+
+// shared memory
+constexpr int kPartBytes = 2 * kConsumerWarps * 32 * 16;  // one buffer: the sums of a pair of stages
+constexpr int kListBytes = kMaxPairs * (2 + 2 + 2 + 4 + 1) + 64 + 32;
+constexpr int kBarBytes = 192;
+constexpr int kStages = (kSmemLimit - 1024 - kBarBytes - kListBytes - 2 * kPartBytes) / kStageBytes;
+static_assert(kStages >= 4, "ring depth");
+constexpr int kPart = kStages * kStageBytes;
+constexpr int kList = kPart + 2 * kPartBytes;
+constexpr int kBar = (kList + kListBytes + 7) / 8 * 8;
+constexpr int kSmemBytes = kBar + kBarBytes + 1024;  // + alignment slack
+static_assert(kSmemBytes <= kSmemLimit, "shared memory");
+static_assert((3 * kStages + 5) * 8 <= kBarBytes, "barriers");
+// scratch of the routing phase: over the partial sums, and the logits over the last stages
+constexpr int kMask = kPart;                 // [1025] token masks by expert
+constexpr int kFirst = kMask + 1028 * 4;     // [1025] first pair by expert (16 bits)
+constexpr int kIds = kFirst + 1028 * 2;      // [16][33]
+constexpr int kSums = kIds + 16 * 33 * 4;    // [16][2]
+static_assert(kSums + 16 * 2 * 4 <= kList, "routing scratch");
+constexpr int kLogitStages = 2;              // 64 KB: 16 tokens x 1024 experts
+constexpr int kEarlyStages = kStages - kLogitStages;  // loads before the routing is known
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     uint32_t v;
@@ -105,8 +126,8 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     return v;
 }
 
-// Adds one to a grid-wide counter; the caller's earlier writes (and those of
-// threads it has synchronised with) are visible to whoever reads the sum.
+// Adds one to a grid-wide counter; the caller's earlier writes, and those of
+// threads it has synchronised with, are visible to whoever reads the sum.
 __device__ __forceinline__ uint32_t add_release(uint32_t* p) {
     uint32_t v;
     asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
@@ -133,7 +154,9 @@ __device__ __forceinline__ void consumers_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
 }
 
-__device__ __forceinline__ float bf16f(uint32_t bits) { return __uint_as_float(bits << 16); }
+// v / d for v < 2^20 and d < 2^12, m = div_magic(d)
+__device__ __forceinline__ uint32_t div_magic(uint32_t d) { return d > 1 ? 0xFFFFFFFFu / d + 1u : 0u; }
+__device__ __forceinline__ uint32_t div_by(uint32_t v, uint32_t m) { return m ? __umulhi(v, m) : v; }
 
 // Eight codes (two per byte, the even k in the low nibble) -> four f16x2.
 __device__ __forceinline__ void codes_to_f16x2(uint32_t w, uint32_t out[4]) {
@@ -147,139 +170,218 @@ __device__ __forceinline__ void codes_to_f16x2(uint32_t w, uint32_t out[4]) {
         : "r"(w));
 }
 
-// acc[n] += one slot (16 rows x 256 k) times the token fragments b[n]: per 32-k
-// scale group two MMAs into a fresh partial sum, added times 2^(s - 126).
-// lm: this lane's four ldmatrix offsets within a slot.
-template <int NT>
-__device__ __forceinline__ void slot_mma(uint32_t slot, const uint32_t lm[4], uint2 sc0, uint2 sc1,
-                                         const uint4 (&b)[NT][8], uint32_t need, const FewArgs& a,
-                                         float (&acc)[NT][4]) {
+// d = a b (+ d): m16n8k16, fp32 sums.  Not volatile, so that independent products are
+// interleaved (the helpers of moe_device.cuh keep their order).
+__device__ __forceinline__ void mma_first(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_next(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The router's products: bf16, 32 k of rows r and r + 8 (wa, wb) by 32 k of token r (x)
+__device__ __forceinline__ void mma_bf16_32(float d[4], uint4 wa, uint4 wb, uint4 x) {
+    asm("{\n\t"
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%6,%5,%7}, {%12,%13}, "
+        "{%16,%16,%16,%16};\n\t"
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%8,%10,%9,%11}, {%14,%15}, "
+        "{%0,%1,%2,%3};\n\t}"
+        : "=&f"(d[0]), "=&f"(d[1]), "=&f"(d[2]), "=&f"(d[3])
+        : "r"(wa.x), "r"(wa.y), "r"(wb.x), "r"(wb.y), "r"(wa.z), "r"(wa.w), "r"(wb.z), "r"(wb.w), "r"(x.x),
+          "r"(x.y), "r"(x.z), "r"(x.w), "f"(0.0f));
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sts_f4(uint32_t addr, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// acc += one slot (16 rows x 256 k) times the token fragment b: per 32-k scale
+// group two MMAs into a fresh partial sum, added times the group's factor.  lm:
+// this lane's four ldmatrix offsets within a slot; fr: the factors of its row r.
+__device__ __forceinline__ void slot_mma(uint32_t slot, const uint32_t lm[4], uint32_t fr, const uint4 (&b)[8],
+                                         float (&acc)[4]) {
 #pragma unroll
-    for (int gp = 0; gp < 4; ++gp) {
-        uint32_t w[4];
-        ldmatrix_x4(slot + lm[gp], w);
+    for (int half = 0; half < 2; ++half) {
+        const float4 fa = lds_f4(fr + 16 * half), fb = lds_f4(fr + 8 * kFactorRow + 16 * half);
+        const float f0[4] = {fa.x, fa.y, fa.z, fa.w}, f1[4] = {fb.x, fb.y, fb.z, fb.w};
+        uint32_t w[2][4];
+        ldmatrix_x4(slot + lm[2 * half], w[0]);
+        ldmatrix_x4(slot + lm[2 * half + 1], w[1]);
 #pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-            const int gl = 2 * gp + gi;
-            const uint32_t b0 = __byte_perm(gl < 4 ? sc0.x : sc0.y, 0, 0x4440 + (gl & 3));
-            const uint32_t b1 = __byte_perm(gl < 4 ? sc1.x : sc1.y, 0, 0x4440 + (gl & 3));
-            const float f0 = __uint_as_float(b0 * a.exp_one + a.exp_bias);
-            const float f1 = __uint_as_float(b1 * a.exp_one + a.exp_bias);
+        for (int q = 0; q < 4; ++q) {
+            const int gl = 4 * half + q;
             uint32_t ta[4], tb[4];
-            codes_to_f16x2(w[gi ? 2 : 0], ta);
-            codes_to_f16x2(w[gi ? 3 : 1], tb);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (NT > 1 && !((need >> n) & 1u)) continue;  // warp-uniform
-                float t4[4];
-                mma_f16_16816_z(t4, ta[0], tb[0], ta[1], tb[1], b[n][gl].x, b[n][gl].y);
-                mma_f16_16816_acc(t4, ta[2], tb[2], ta[3], tb[3], b[n][gl].z, b[n][gl].w);
-                acc[n][0] = fmaf(t4[0], f0, acc[n][0]);
-                acc[n][1] = fmaf(t4[1], f0, acc[n][1]);
-                acc[n][2] = fmaf(t4[2], f1, acc[n][2]);
-                acc[n][3] = fmaf(t4[3], f1, acc[n][3]);
-            }
+            codes_to_f16x2(w[q >> 1][q & 1 ? 2 : 0], ta);
+            codes_to_f16x2(w[q >> 1][q & 1 ? 3 : 1], tb);
+            float t4[4];
+            mma_first(t4, ta[0], tb[0], ta[1], tb[1], b[gl].x, b[gl].y);
+            mma_next(t4, ta[2], tb[2], ta[3], tb[3], b[gl].z, b[gl].w);
+            acc[0] = fmaf(t4[0], f0[q], acc[0]);
+            acc[1] = fmaf(t4[1], f0[q], acc[1]);
+            acc[2] = fmaf(t4[2], f1[q], acc[2]);
+            acc[3] = fmaf(t4[3], f1[q], acc[3]);
         }
     }
 }
 
-// Eight scale bytes of a row from group 8 * slice on (zeros past its end).
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int slice, int groups, bool vec) {
-    if (vec) return __ldg(reinterpret_cast<const uint2*>(row + 8 * slice));
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (8 * slice + j < groups) w[j >> 2] |= (uint32_t)__ldg(row + 8 * slice + j) << (8 * (j & 3));
-    return make_uint2(w[0], w[1]);
+// Eight bytes from byte `at` of a matrix of `words` 32-bit words on, of which the
+// first n count (zeros for the others): three aligned words and a shift, whatever
+// the row's alignment, and no word past the matrix.
+__device__ __forceinline__ uint2 load_scales(const uint8_t* base, size_t at, int n, size_t words) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(base);
+    const size_t w = at >> 2;
+    const uint32_t sh = (uint32_t)(at & 3) * 8u;
+    const uint32_t w0 = __ldg(p + w), w1 = __ldg(p + min(w + 1, words - 1)), w2 = __ldg(p + min(w + 2, words - 1));
+    uint2 v = make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
+    if (n < 8) v.y = n > 4 ? v.y & ((1u << (8 * (n - 4))) - 1u) : 0u;
+    if (n < 4) v.x &= (1u << (8 * n)) - 1u;
+    return v;
+}
+
+// 2^(s - 127) of four scale bytes (0 for byte 0)
+__device__ __forceinline__ float4 factors(uint32_t w) {
+    return make_float4(__uint_as_float((w << 23) & 0x7F800000u), __uint_as_float((w << 15) & 0x7F800000u),
+                       __uint_as_float((w << 7) & 0x7F800000u), __uint_as_float((w >> 1) & 0x7F800000u));
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// The range of the down phase's slots that CTA b of G multiplies.
-__device__ __forceinline__ long long cut(long long slots, int b, int G) { return slots * b / G; }
+// h's shifts: one byte per 8 values, those of 256 values (32 bytes) ordered so
+// that the lane that multiplies values 32 g + 8 c .. 32 g + 8 c + 7, g = 0..7, finds
+// its eight in one 8-byte word.
+__host__ __device__ __forceinline__ int shift_pitch(int I) { return (I + 255) / 256 * 32; }
+__device__ __forceinline__ int shift_at(int blk) { return (blk & ~31) | ((blk & 3) << 3) | ((blk >> 2) & 7); }
 
-// NT: n-tiles of 8 tokens; NC: 256-k slices of H per consumer warp.
-template <int NT, int NC>
+// The first of n things that CTA b of G takes (n * G < 2^32).
+__device__ __forceinline__ int cut(int n, int b, int G) { return (int)((uint32_t)n * (uint32_t)b / (uint32_t)G); }
+
+// NC: stages of a gate_up unit (H <= NC * 4096).  SF: the scale bytes come with the
+// codes (rows of whole 16-byte units, which the TMA can read); else the scale warp
+// loads them.
+template <int NC, bool SF>
 __global__ void __launch_bounds__(kThreads, 1)
-    layer_few_kernel(const FewArgs a, const __grid_constant__ CUtensorMap w13_map,
-                     const __grid_constant__ CUtensorMap w2_map) {
+    layer_few_kernel(const FewArgs a, const __grid_constant__ FewMaps maps) {
     pdl_begin();
-    using L = FewLayout<NT>;
-    constexpr int kStages = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float4* part = reinterpret_cast<float4*>(smem + L::kPart);        // [2][NT][16 warps][32]
-    int32_t* list_e = reinterpret_cast<int32_t*>(smem + L::kList);    // touched experts
-    uint32_t* list_m = reinterpret_cast<uint32_t*>(list_e + kMaxList);  // first pair << 16 | token mask
-    float* pair_w = reinterpret_cast<float*>(list_m + kMaxList);      // routing weight of a pair
-    float* rscale = pair_w + kMaxList;                                // [16] factor undoing x's scaling
-    int32_t* info = reinterpret_cast<int32_t*>(rscale + 16);          // [0] list length, [1] barrier outcome,
-                                                                      // [2] outcome of the second one
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    float4* part = reinterpret_cast<float4*>(smem + kPart);             // [2 buffers][2 stages][16 warps][32]
+    float* w_s = reinterpret_cast<float*>(smem + kList);                // [T][Kt] routing weights
+    float* rscale = w_s + kMaxPairs;                                    // [16] factor undoing x's scaling
+    int32_t* info = reinterpret_cast<int32_t*>(rscale + 16);            // [0] entries, [1] outcome of the first
+                                                                        // barrier, [2] of the second, [3] of the
+                                                                        // third
+    uint16_t* list_e = reinterpret_cast<uint16_t*>(info + 8);           // an entry's expert
+    uint16_t* list_p = list_e + kMaxPairs;                              // its first pair << 4 | its tokens
+    uint16_t* pair_of = list_p + kMaxPairs;                             // [T][Kt] pair of a token's slot
+    uint8_t* pair_t = reinterpret_cast<uint8_t*>(pair_of + kMaxPairs);  // a pair's token
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBar);
     uint64_t* empty = full + kStages;
-    uint64_t* part_full = empty + kStages;  // [2]
-    uint64_t* part_free = part_full + 2;    // [2]
+    uint64_t* sf_full = empty + kStages;      // codes and factors
+    uint64_t* part_full = sf_full + kStages;  // [2]
+    uint64_t* part_free = part_full + 2;      // [2]
     uint64_t* h_ready = part_free + 2;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = (int)blockIdx.x, G = (int)gridDim.x;
     const int T = a.T, H = a.H, I = a.I;
     const int Kt = a.K + a.shared, Et = a.E + a.shared;
-    // gate_up: slots per unit, units per stage (NC == 1), units per expert
-    const int sg = (H + 255) / 256;
+    const int KGH = H / 32, KGI = I / 32;
+    // gate_up: slots per unit, units per stage (NC == 1), units per entry
+    const int sg = (H + 255) / 256, sg_whole = H / 256;
     const int ups = NC == 1 ? kConsumerWarps / sg : 1;
     const int upe = I / 8;
-    const int KGH = H / 32, KGI = I / 32;
+    const uint32_t upe_m = div_magic((uint32_t)upe);
+    const int sfp = NC == 1 ? KGH : 128;  // bytes between a unit's scale rows in a stage
+    // down: items per entry, slots per item, items per stage or stages per item
+    const int RU = H / 16;
+    const uint32_t ru_m = div_magic((uint32_t)RU);
+    const int sd = (I + 255) / 256, sd_whole = I / 256;
+    const int spi = (sd + kConsumerWarps - 1) / kConsumerWarps;
+    const int ips = spi == 1 ? kConsumerWarps / sd : 1;
+    const int sfp2 = spi == 1 ? KGI : 128;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kConsumerWarps);
+            mbar_init(&sf_full[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&part_full[i], kConsumerWarps);
-            mbar_init(&part_free[i], 1);
+            mbar_init(&part_free[i], 2);
         }
         mbar_init(h_ready, 1);
-        info[2] = 0;
+        info[2] = info[3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
 
-    // gate_up stage `st` of this CTA: unit k (k-th of the CTA: b + k G) and slice of slot w
-    auto gate_up_slot = [&](int st, int w, int& k, int& slice) {
-        if (NC == 1) {
-            k = st * ups + w / sg;
-            slice = w % sg;
-            return w / sg < ups;
-        }
-        k = st / NC;
-        slice = (st % NC) * kConsumerWarps + w;
-        return slice < sg;
+    // The shared expert's entries come first: its units are dealt out before the routing is
+    // known (from the last CTA on, as the others' are from the first: a CTA that gets one
+    // more of these tends to get one less of those).
+    const int shared_units = a.shared ? (T + 7) / 8 * upe : 0;
+    const int sh0 = cut(shared_units, G - 1 - b, G), nsh = cut(shared_units, G - b, G) - sh0;
+    int other0 = 0, nunits = nsh;  // first of the others, units in all
+    // entry and 8-row block of this CTA's k-th unit
+    auto unit_at = [&](int k, int& i, int& blk) {
+        const int u = k < nsh ? sh0 + k : shared_units + other0 + k - nsh;
+        i = (int)div_by((uint32_t)u, upe_m);
+        blk = u - i * upe;
     };
-    auto my_units = [&](int units) { return units > b ? (units - b + G - 1) / G : 0; };
-    auto gate_up_stages = [&](int n) { return NC == 1 ? (n + ups - 1) / ups : n * NC; };
 
-    // producer: one gate_up stage; lane w loads slot w (8 gate rows, 8 up rows)
-    auto issue_gate_up = [&](uint32_t gs, int st, int nunits, bool routed) {
+    // producer: gate_up stage `st`.  Lane j loads the stage's j-th unit: 8 gate and 8
+    // up rows, as many 256-k slices as the stage takes
+    auto issue_gate_up = [&](uint32_t gs, int st, bool routed) {
         const int s = gs % kStages;
-        int k, slice;
-        const bool on = gate_up_slot(st, lane & 15, k, slice) && lane < kConsumerWarps && k < nunits;
-        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, on));
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], n * kSlotBytes);
+        const int k0 = NC == 1 ? st * ups : st / NC;
+        const int sl0 = NC == 1 ? 0 : (st % NC) * kConsumerWarps;  // the stage's first slice
+        const int n = min(ups, nunits - k0);
+        const int whole = min(max(sg_whole - sl0, 0), kConsumerWarps);  // slices in the box
+        const bool tail = sg_whole < sg && sg_whole - sl0 < kConsumerWarps;
+        const uint32_t bytes =
+            (uint32_t)(whole + (tail ? 1 : 0)) * kSlotBytes + (SF ? 16u * (uint32_t)sfp : 0u);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)n * bytes);
         __syncwarp();
-        if (on) {
-            const int u = b + k * G, i = u / upe, blk = u - i * upe;
-            const int e = routed ? list_e[i] : a.E;  // the shared expert is first in the list
-            const int row = e * 2 * I + blk * 8;
-            const uint32_t dst = smem_u32(smem + s * kStageBytes + lane * kSlotBytes);
-            tma_load_2d(dst, &w13_map, slice * 128, row, &full[s]);
-            tma_load_2d(dst + 1024, &w13_map, slice * 128, row + I, &full[s]);
-            // the scale bytes of this slot's rows, shared by the unit's slots
-            for (int r = slice; r < 16; r += sg) {
-                const uint8_t* p = a.s13 + (size_t)(row + (r < 8 ? r : I + r - 8)) * KGH;
+        if (lane < n) {
+            int i, blk;
+            unit_at(k0 + lane, i, blk);
+            const int row = (routed ? (int)list_e[i] : a.E) * 2 * I + blk * 8;
+            const uint32_t base = smem_u32(smem + s * kStageBytes);
+            const uint32_t dst = base + (NC == 1 ? lane * sg : 0) * kSlotBytes;
+            if (whole)
+                tma_load_4d(dst, NC > 1 && sl0 > 0 ? &maps.w13_rest : &maps.w13, 0, row, 0, sl0, &full[s]);
+            if (tail)
+                tma_load_3d(dst + whole * kSlotBytes, &maps.w13_tail, sg_whole * 128, row, 0, &full[s]);
+            if (SF)
+                tma_load_3d(base + kCodeBytes + lane * 16 * sfp, &maps.s13, sl0 * 8, row, 0, &full[s]);
+        }
+        if (!SF && (NC == 1 || sl0 == 0)) {  // the units' scale rows, on their way into L2
+            for (int q = lane; q < n * 16; q += 32) {
+                int i, blk;
+                unit_at(k0 + q / 16, i, blk);
+                const int r = q % 16, row = blk * 8 + (r < 8 ? r : I + r - 8);
+                const uint8_t* p = a.s13 + ((size_t)(routed ? (int)list_e[i] : a.E) * 2 * I + row) * KGH;
                 for (int o = 0; o < KGH; o += 128) prefetch_l2(p + o);
             }
         }
@@ -289,64 +391,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gs = 0;  // stages issued (producer) or consumed so far
 
     if (warp == kProducerWarp) {
-        // the shared expert's units need no routing: fill the ring with them
-        if (a.shared) {
-            const int n = my_units(upe);
-            const int stages = NC == 1 ? n / ups : n * NC;  // whole stages only
-            for (; (int)gs < min(stages, kStages); ++gs) issue_gate_up(gs, (int)gs, n, false);
-        }
+        // whole stages of the shared expert's units need no routing (once the router's own
+        // loads are through: before them they would hold those up)
+        asm volatile("bar.sync 3, %0;" ::"n"(kConsumers + 32) : "memory");
+        const int stages = NC == 1 ? nsh / ups : nsh * NC;
+        for (; (int)gs < min(stages, kEarlyStages); ++gs) issue_gate_up(gs, (int)gs, false);
     } else if (warp < kConsumerWarps) {
         // ------------------------------------------------------- router
-        // rows b, b + G, ... of [Wr; gate], each split over k so that all warps work; the
-        // same split in every CTA, so that equal rows give equal logits
-        const int rows = a.E + (a.gate ? 1 : 0);
-        const int nrows = rows > b ? (rows - b + G - 1) / G : 0;
-        const int Q = max(1, kConsumerWarps / ((rows + G - 1) / G));
-        float* red = reinterpret_cast<float*>(smem + L::kRed);
-        const int units = H / 8;
-        for (int task = warp; task < nrows * Q; task += kConsumerWarps) {
-            const int e = b + (task / Q) * G, q = task % Q;
-            const uint4* w4 = reinterpret_cast<const uint4*>(e < a.E ? a.wr + (size_t)e * H : a.gate);
-            float acc[8 * NT];
+        // each CTA multiplies a few rows of [Wr; gate], spread over the warps 32 k at a
+        // time.  Equal rows give equal logits: every row's sums have one order.
+        const int r = lane >> 2, c = lane & 3;
+        const int row0 = b * a.router_rows, rows = min(a.router_rows, a.E + (a.gate ? 1 : 0) - row0);
+        if (rows > 0) {
+            // (rows and tokens that do not exist are read as the first one, unconditionally
+            // so that the loads of four steps go out together, and not used)
+            auto row_of = [&](int i) {
+                const int row = row0 + (i < rows ? i : 0);
+                return reinterpret_cast<const uint4*>(row < a.E ? a.wr + (size_t)row * H : a.gate) + c;
+            };
+            const uint4* wa = row_of(r);
+            const uint4* wb = row_of(r + 8);
+            const uint4* x0 = reinterpret_cast<const uint4*>(a.x + (size_t)(r < T ? r : 0) * H) + c;
+            const uint4* x1 = reinterpret_cast<const uint4*>(a.x + (size_t)(8 + r < T ? 8 + r : 0) * H) + c;
+            const bool two_rows = rows > 8, two_tokens = T > 8;
+            float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+            for (int g0 = warp; g0 < KGH; g0 += 4 * kConsumerWarps) {
+                uint4 va[4], vb[4], vx[2][4];
 #pragma unroll
-            for (int t = 0; t < 8 * NT; ++t) acc[t] = 0.0f;
-            const int u1 = units * (q + 1) / Q;
-            for (int u = units * q / Q + lane; u < u1; u += 32) {
-                const uint4 wv = __ldg(w4 + u);
-                const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+                for (int q = 0; q < 4; ++q) {
+                    const int o = 4 * min(g0 + q * kConsumerWarps, KGH - 1);
+                    va[q] = __ldg(wa + o);
+                    vx[0][q] = __ldg(x0 + o);
+                    vb[q] = two_rows ? __ldg(wb + o) : va[q];
+                    vx[1][q] = two_tokens ? __ldg(x1 + o) : vx[0][q];
+                }
 #pragma unroll
-                for (int t = 0; t < 8 * NT; ++t) {
-                    if (t < T) {
-                        const uint4 xv = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * H) + u);
-                        const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+                for (int q = 0; q < 4; ++q) {
+                    if (g0 + q * kConsumerWarps >= KGH) break;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            acc[t] = fmaf(bf16f(ww[i] & 0xFFFFu), bf16f(xx[i] & 0xFFFFu), acc[t]);
-                            acc[t] = fmaf(__uint_as_float(ww[i] & 0xFFFF0000u),
-                                          __uint_as_float(xx[i] & 0xFFFF0000u), acc[t]);
-                        }
+                    for (int n = 0; n < 2; ++n) {
+                        if (n && !two_tokens) break;
+                        float t4[4];
+                        mma_bf16_32(t4, va[q], vb[q], vx[n][q]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[n][i] += t4[i];
                     }
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 8 * NT; ++t) {
-                if (t >= T) break;
+            for (int n = 0; n < 2; ++n)
+                part[(n * kConsumerWarps + warp) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            consumers_sync();
+            if (tid < 256) {  // one (row, token) each
+                const float* p = reinterpret_cast<const float*>(part) + (tid >> 7) * kConsumerWarps * 128 + (tid & 127);
+                float v = 0.0f;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
-                if (lane == t) red[task * 16 + t] = acc[t];
+                for (int w = 0; w < kConsumerWarps; ++w) v += p[w * 128];
+                const int l = (tid & 127) >> 2, q = tid & 3;
+                const int row = (l >> 2) + (q & 2 ? 8 : 0), t = 8 * (tid >> 7) + 2 * (l & 3) + (q & 1);
+                if (row < rows && t < T) a.logits[(size_t)t * (a.E + 1) + row0 + row] = v;
             }
         }
-        consumers_sync();
-        for (int i = tid; i < nrows * T; i += kConsumers) {
-            const int r = i / T, t = i - r * T;
-            float v = 0.0f;
-            for (int q = 0; q < Q; ++q) v += red[(r * Q + q) * 16 + t];
-            a.logits[(size_t)t * (a.E + 1) + b + r * G] = v;
-        }
-        // what later phases add to starts at zero
+        asm volatile("bar.arrive 3, %0;" ::"n"(kConsumers + 32) : "memory");
+        // what gate_up raises starts at zero
         for (int i = b * kConsumers + tid; i < T * Kt; i += G * kConsumers) a.hmax[i] = 0u;
-        for (int i = b * kConsumers + tid; i < H / 16; i += G * kConsumers) a.joined[i] = 0u;
-        __threadfence();
         consumers_sync();
         if (tid == 0) add_release(&a.sync[0]);
 
@@ -354,20 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp < T) {
             uint32_t mx = 0;
             const uint4* xr = reinterpret_cast<const uint4*>(a.x + (size_t)warp * H);
-            for (int u = lane; u < units; u += 32) {
+#pragma unroll 8
+            for (int u = lane; u < H / 8; u += 32) {
                 const uint4 v = __ldg(xr + u);
                 const uint32_t xx[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mx = max(mx, max(xx[i] & 0x7FFFu, (xx[i] >> 16) & 0x7FFFu));
             }
             mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-            // (the MMA's group factor is 2^(s-126): the rest of it goes in here)
-            if (lane == 0) rscale[warp] = __uint_as_float((uint32_t)(127 - row_f16_shift(mx)) << 23) * 0.5f;
+            if (lane == 0) rscale[warp] = __uint_as_float((uint32_t)(127 - row_f16_shift(mx)) << 23);
         }
-        uint32_t* mask = reinterpret_cast<uint32_t*>(smem + L::kMask);
-        uint16_t* first = reinterpret_cast<uint16_t*>(smem + L::kFirst);
-        int32_t* ids_s = reinterpret_cast<int32_t*>(smem + L::kIds);
-        float* w_s = reinterpret_cast<float*>(smem + L::kW);
+        uint32_t* mask = reinterpret_cast<uint32_t*>(smem + kMask);
+        uint16_t* first = reinterpret_cast<uint16_t*>(smem + kFirst);
+        int32_t* ids_s = reinterpret_cast<int32_t*>(smem + kIds);
+        float* logit_s = reinterpret_cast<float*>(smem + kEarlyStages * kStageBytes);  // [T][E]
         for (int e = tid; e < Et; e += kConsumers) mask[e] = 0u;
         if (tid == 0) info[1] = grid_wait(&a.sync[0], (uint32_t)G) ? 1 : 0;
         consumers_sync();
@@ -375,17 +483,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------ routing
         // every CTA routes all tokens, one warp each, and builds the same list
         if (info[1]) {
+            // (loads are kept few in the code: a call runs every line of it once or twice,
+            // and fetching straight-line code costs more than running it)
+            const uint32_t e_m = div_magic((uint32_t)a.E);
+#pragma unroll 4
+            for (int q = tid; q < T * a.E; q += kConsumers) {
+                const int t = (int)div_by((uint32_t)q, e_m);
+                logit_s[q] = __ldcg(a.logits + q + t);  // written by this kernel: read from L2
+            }
+            consumers_sync();
             if (warp < T) {
-                const float* l = a.logits + (size_t)warp * (a.E + 1);
-                const float sw = a.gate ? 1.0f / (1.0f + expf(-__ldcg(l + a.E))) : 1.0f;
+                const float* l = logit_s + warp * a.E;
+                auto load = [l](int e) { return l[e]; };
+                const float sw = a.gate ? 1.0f / (1.0f + expf(-__ldcg(a.logits + (size_t)warp * (a.E + 1) + a.E))) : 1.0f;
                 int32_t* wi = ids_s + warp * 33;
-                float* ww = w_s + warp * 33;
+                float* ww = w_s + warp * Kt;
                 if (a.E <= 128)
-                    route_token<4, true>(l, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
+                    route_loaded<4>(load, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
                 else if (a.E <= 512)
-                    route_token<16, true>(l, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
+                    route_loaded<16>(load, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
                 else
-                    route_token<32, true>(l, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
+                    route_loaded<32>(load, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
                 __syncwarp();
                 for (int j = lane; j < Kt; j += 32) {
                     // a slot without an expert (only where every logit left is a NaN of the
@@ -399,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             consumers_sync();
             // list: the shared expert first, then the touched routed ones by id;
             // warp w orders experts 64 w .. 64 w + 63
-            int32_t* sums = reinterpret_cast<int32_t*>(smem + L::kRed);  // [16][2] experts, pairs
+            int32_t* sums = reinterpret_cast<int32_t*>(smem + kSums);  // entries, pairs by warp
             int ne[2], np[2];
             uint32_t mk[2];
             int ce = 0, cp = 0;
@@ -407,26 +525,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 const int e = 64 * warp + 32 * i + lane;
                 mk[i] = e < a.E ? mask[e] : 0u;
-                const uint32_t hot = __ballot_sync(0xFFFFFFFFu, mk[i] != 0);
-                int c = __popc(mk[i]);
-                const int own = c;
+                int n = __popc(mk[i]);
+                const uint32_t one = __ballot_sync(0xFFFFFFFFu, n > 0), two = __ballot_sync(0xFFFFFFFFu, n > 8);
+                const int own = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xFFFFFFFFu, c, o);
-                    if (lane >= o) c += v;
+                    const int v = __shfl_up_sync(0xFFFFFFFFu, n, o);
+                    if (lane >= o) n += v;
                 }
-                ne[i] = ce + __popc(hot & lanemask_lt());
-                np[i] = cp + c - own;
-                ce += __popc(hot);
-                cp += __shfl_sync(0xFFFFFFFFu, c, 31);
+                ne[i] = ce + __popc(one & lanemask_lt()) + __popc(two & lanemask_lt());
+                np[i] = cp + n - own;
+                ce += __popc(one) + __popc(two);
+                cp += __shfl_sync(0xFFFFFFFFu, n, 31);
             }
             if (lane == 0) {
                 sums[2 * warp] = ce;
                 sums[2 * warp + 1] = cp;
             }
             consumers_sync();
-            int be = a.shared, bp = a.shared ? T : 0;
-            int te = be;
+            int be = a.shared ? (T + 7) / 8 : 0, bp = a.shared ? T : 0, te = be;
             for (int i = 0; i < kConsumerWarps; ++i) {
                 if (i < warp) {
                     be += sums[2 * i];
@@ -434,42 +551,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 te += sums[2 * i];
             }
+            // entries of expert e from `at` on, its pairs from p on
+            auto enter = [&](int e, int at, int p, int n) {
+                list_e[at] = (uint16_t)e;
+                list_p[at] = (uint16_t)(p << 4 | min(n, 8));
+                if (n > 8) {
+                    list_e[at + 1] = (uint16_t)e;
+                    list_p[at + 1] = (uint16_t)((p + 8) << 4 | (n - 8));
+                }
+                first[e] = (uint16_t)p;
+            };
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!mk[i]) continue;
-                const int e = 64 * warp + 32 * i + lane;
-                list_e[be + ne[i]] = e;
-                list_m[be + ne[i]] = (uint32_t)(bp + np[i]) << 16 | mk[i];
-                first[e] = (uint16_t)(bp + np[i]);
-            }
+            for (int i = 0; i < 2; ++i)
+                if (mk[i]) enter(64 * warp + 32 * i + lane, be + ne[i], bp + np[i], __popc(mk[i]));
             if (tid == 0) {
                 info[0] = te;
-                if (a.shared) {
-                    list_e[0] = a.E;
-                    list_m[0] = (1u << T) - 1u;
-                    first[a.E] = 0;
-                }
+                if (a.shared) enter(a.E, 0, 0, T);
             }
             consumers_sync();
             for (int i = tid; i < T * Kt; i += kConsumers) {
                 const int t = i / Kt, e = ids_s[t * 33 + i - t * Kt];
-                pair_w[first[e] + __popc(mask[e] & ((1u << t) - 1u))] = w_s[t * 33 + i - t * Kt];
+                const int p = first[e] + __popc(mask[e] & ((1u << t) - 1u));
+                pair_of[i] = (uint16_t)p;
+                pair_t[p] = (uint8_t)t;
             }
+            // the logits' place in shared memory goes back to the TMA
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
     }
     __syncthreads();  // the list is there (or the barrier gave up)
 
     const bool routed = info[1] != 0;
-    const int nlist = routed ? info[0] : 0;
-    const int nunits = my_units(nlist * upe);
-    const int gstages = gate_up_stages(nunits);
-    const int sd = (I + 255) / 256;
-    const int Q = nlist * sd;                        // down: slots per 16 output rows
-    const long long slots = (long long)(H / 16) * Q;
-    const long long lo = cut(slots, b, G), hi = cut(slots, b + 1, G);
-    const int dstages = (int)((hi - lo + kConsumerWarps - 1) / kConsumerWarps);
-    const int ru0 = Q > 0 ? (int)(lo / Q) : 0;                       // first rows of this CTA
-    const int pieces = hi > lo ? (int)((hi - 1) / Q) - ru0 + 1 : 0;  // groups of 16 output rows
+    const int nent = routed ? info[0] : 0;
+    const int others = max(nent * upe - shared_units, 0);
+    other0 = cut(others, b, G);
+    nunits = routed ? nsh + cut(others, b + 1, G) - other0 : 0;
+    const int gstages = NC == 1 ? (nunits + ups - 1) / ups : nunits * NC;
+    // down: items (entry, 16 output rows) in that order, cut into one range per CTA
+    const int items = RU * nent;
+    const int lo = cut(items, b, G), hi = cut(items, b + 1, G);
+    const int dstages = (hi - lo + ips - 1) / ips * spi;
+    // the stages of a phase are consumed in pairs (a unit's or item's two stages, or two
+    // independent ones), each handing one buffer of sums over to the epilogue
+    const int ghands = (gstages + 1) / 2, dhands = (dstages + 1) / 2;
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------- producer
@@ -479,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
-            issue_gate_up(gs, (int)gs, nunits, true);
+            issue_gate_up(gs, (int)gs, true);
         }
         for (int st = 0; st < dstages && ok; ++st, ++gs) {
             const int s = gs % kStages;
@@ -487,19 +611,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
-            const long long slot = lo + (long long)st * kConsumerWarps + lane;
-            const bool on = lane < kConsumerWarps && slot < hi;
-            const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, on));
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], n * kSlotBytes);
+            const int it0 = lo + (spi > 1 ? st / spi : st * ips), sl0 = (st % spi) * kConsumerWarps;
+            const int n = min(ips, hi - it0);
+            const int whole = min(max(sd_whole - sl0, 0), kConsumerWarps);
+            const bool tail = sd_whole < sd && sd_whole - sl0 < kConsumerWarps;
+            const uint32_t bytes =
+                (uint32_t)(whole + (tail ? 1 : 0)) * kSlotBytes + (SF ? 16u * (uint32_t)sfp2 : 0u);
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)n * bytes);
             __syncwarp();
-            if (on) {
-                const int ru = (int)(slot / Q), q = (int)(slot - (long long)ru * Q);
-                const int i = q / sd, slice = q - i * sd;
-                const int row = list_e[i] * H + ru * 16;
-                tma_load_2d(smem_u32(smem + s * kStageBytes + lane * kSlotBytes), &w2_map, slice * 128, row,
-                            &full[s]);
-                for (int r = slice; r < 16; r += sd) {
-                    const uint8_t* p = a.s2 + (size_t)(row + r) * KGI;
+            if (lane < n) {
+                const int i = (int)div_by((uint32_t)(it0 + lane), ru_m);
+                const int row = (int)list_e[i] * H + (it0 + lane - i * RU) * 16;
+                const uint32_t base = smem_u32(smem + s * kStageBytes);
+                const uint32_t dst = base + (spi > 1 ? 0 : lane * sd) * kSlotBytes;
+                if (whole) tma_load_3d(dst, sl0 > 0 ? &maps.w2_rest : &maps.w2, 0, row, sl0, &full[s]);
+                if (tail) tma_load_2d(dst + whole * kSlotBytes, &maps.w2_tail, sd_whole * 128, row, &full[s]);
+                if (SF) tma_load_2d(base + kCodeBytes + lane * 16 * sfp2, &maps.s2, sl0 * 8, row, &full[s]);
+            }
+            if (!SF && sl0 == 0) {
+                for (int q = lane; q < n * 16; q += 32) {
+                    const int it = it0 + q / 16, i = (int)div_by((uint32_t)it, ru_m);
+                    const uint8_t* p = a.s2 + ((size_t)list_e[i] * H + (it - i * RU) * 16 + q % 16) * KGI;
                     for (int o = 0; o < KGI; o += 128) prefetch_l2(p + o);
                 }
             }
@@ -510,6 +642,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t u = gs - 1 - d;
             if (!mbar_wait_warp(&full[u % kStages], (u / kStages) & 1)) break;
         }
+    } else if (warp == kScaleWarp) {
+        // ------------------------------------------------- scale factors
+        // of stage after stage: this lane's slot, rows lane / 16, + 2, ...
+        const int slot = lane & 15, row0 = lane >> 4;
+        bool ok = routed;
+        // Without SF: the slot's first scale byte in row 0 at byte `at` of src, rows `pitch`
+        // bytes apart and those from 8 on `up` bytes further, n bytes counting (none: no
+        // such slot).  With it: at byte `raw` of the stage's, rows raw_pitch apart.
+        auto convert = [&](int st, const uint8_t* src, size_t words, size_t at, size_t pitch, size_t up, int n,
+                           uint32_t raw, int raw_pitch) {
+            const int s = st % kStages;
+            uint2 w[8];
+            if (!SF) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = row0 + 2 * i;
+                    w[i] = load_scales(src, n > 0 ? at + row * pitch + (row < 8 ? 0 : up) : 0, n, words);
+                    if (n <= 0) w[i] = make_uint2(0, 0);
+                }
+            }
+            if (!mbar_wait_warp(&full[s], (st / kStages) & 1)) return false;
+            const uint32_t stage = smem_u32(smem + s * kStageBytes);
+            const uint32_t f = stage + kCodeBytes + kScaleBytes + row0 * kFactorRow + slot * 32;
+            if (SF) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = lds64(stage + kCodeBytes + raw + (row0 + 2 * i) * raw_pitch);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sts_f4(f + 2 * i * kFactorRow, factors(w[i].x));
+                sts_f4(f + 2 * i * kFactorRow + 16, factors(w[i].y));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sf_full[s]);
+            return true;
+        };
+        {
+            const int j = NC == 1 ? slot / sg : 0, sl = NC == 1 ? slot - j * sg : slot;
+            const uint32_t raw = j < ups ? (uint32_t)(j * 16 * sfp + sl * 8) : 0u;
+            for (int st = 0; st < gstages && ok; ++st) {
+                const int slice = sl + (NC == 1 ? 0 : (st % NC) * kConsumerWarps), k = NC == 1 ? st * ups + j : st / NC;
+                size_t at = 0;
+                int n = 0;
+                if (!SF && j < ups && k < nunits) {
+                    int e, blk;
+                    unit_at(k, e, blk);
+                    at = ((size_t)list_e[e] * 2 * I + blk * 8) * KGH + 8 * slice;
+                    n = min(8, KGH - 8 * slice);
+                }
+                ok = convert(st, a.s13, (size_t)Et * 2 * I * KGH / 4, at, KGH, (size_t)(I - 8) * KGH, n, raw, sfp);
+            }
+        }
+        {
+            const int j = spi == 1 ? slot / sd : 0, sl = spi == 1 ? slot - j * sd : slot;
+            const uint32_t raw = j < ips ? (uint32_t)(j * 16 * sfp2 + sl * 8) : 0u;
+            for (int st = 0; st < dstages && ok; ++st) {
+                const int slice = sl + (spi == 1 ? 0 : (st % spi) * kConsumerWarps);
+                const int item = lo + (spi == 1 ? st * ips + j : st / spi);
+                size_t at = 0;
+                int n = 0;
+                if (!SF && j < ips && item < hi) {
+                    const int e = (int)div_by((uint32_t)item, ru_m);
+                    at = ((size_t)list_e[e] * H + (item - e * RU) * 16) * KGI + 8 * slice;
+                    n = min(8, KGI - 8 * slice);
+                }
+                ok = convert(gstages + st, a.s2, (size_t)Et * H * KGI / 4, at, KGI, 0, n, raw, sfp2);
+            }
+        }
     } else if (warp < kConsumerWarps) {
         // ------------------------------------------------------ consumers
         const int r = lane >> 2, c = lane & 3, mj = lane >> 3, mi = lane & 7;
@@ -517,200 +717,148 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int gp = 0; gp < 4; ++gp)
             lm[gp] = (uint32_t)((mj & 1) * 1024 + mi * 128 + (((2 * gp + (mj >> 1)) ^ mi) << 4));
-        const uint32_t slot_base = smem_u32(smem) + warp * kSlotBytes;
+        const uint32_t ring = smem_u32(smem);
         bool failed = !routed;
-        uint32_t pc = 0;  // partial-sum buffers handed to the epilogue
 
-        auto hand_over = [&](const float (&acc)[NT][4]) {
-            const int buf = pc & 1;
-            if (!failed && pc >= 2 && !mbar_wait_warp(&part_free[buf], ((pc >> 1) - 1) & 1)) failed = true;
+        // the pair's sums to the epilogue: hand-over h, acc[i] of its i-th stage (or, if
+        // `one`, acc[0] of both)
+        auto hand_over = [&](int h, const float (&acc)[2][4], bool one) {
+            const int buf = h & 1;
+            if (!failed && h >= 2 && !mbar_wait_warp(&part_free[buf], ((h >> 1) - 1) & 1)) failed = true;
             if (!failed) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    part[((buf * NT + n) * kConsumerWarps + warp) * 32 + lane] =
-                        make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                float4* p = part + (buf * 2 * kConsumerWarps + warp) * 32 + lane;
+                p[0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+                if (!one)
+                    p[kConsumerWarps * 32] = make_float4(acc[1][0], acc[1][1], acc[1][2], acc[1][3]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&part_full[buf]);
-            ++pc;
+        };
+        // stage st's slot of this warp, slot `at` of the stage, times b
+        auto multiply = [&](int st, int at, bool on, const uint4 (&b)[8], float (&acc)[4]) {
+            const uint32_t stage = ring + (st % kStages) * kStageBytes;
+            if (!failed && on)
+                slot_mma(stage + at * kSlotBytes, lm, stage + kCodeBytes + kScaleBytes + r * kFactorRow + at * 32, b, acc);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st % kStages]);
+        };
+        auto wait_stage = [&](int st) {
+            if (!failed && !mbar_wait_warp(&sf_full[st % kStages], (st / kStages) & 1)) failed = true;
         };
 
         // -------------------------------------------------------- gate_up
         {
-            uint4 xb[NC][NT][8];
-            const int sl0 = NC == 1 ? warp % sg : warp;
+            const int j = NC == 1 ? warp / sg : 0;          // this warp's unit within a stage
+            const int q0 = NC == 1 ? warp - j * sg : warp;  // and its (first) slice
+            uint4 xb[NC][8];
+            int have = -1;  // the entry whose x fragment is in xb
+            auto load_x = [&](int i) {
+                const int n = list_p[i] & 15, p = list_p[i] >> 4;
+                const int t = r < n ? (int)pair_t[p + r] : 0;
+                const float up = 1.0f / rscale[t];  // 2^sigma, exact
+                const uint16_t* xr = a.x + (size_t)t * H;
 #pragma unroll
-            for (int ch = 0; ch < NC; ++ch)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int t = 8 * n + r;
-                    // 2^sigma from the factor 2^-sigma / 2
-                    const float up = t < T ? 0.5f / rscale[t] : 0.0f;
+                for (int f = 0; f < NC; ++f)
 #pragma unroll
                     for (int gl = 0; gl < 8; ++gl) {
-                        const int k = (sl0 + ch * kConsumerWarps) * 256 + 32 * gl + 8 * c;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (t < T && k < H) {
-                            const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * H + k));
-                            v = make_uint4(bf16x2_to_f16x2_scaled(q.x, up), bf16x2_to_f16x2_scaled(q.y, up),
-                                           bf16x2_to_f16x2_scaled(q.z, up), bf16x2_to_f16x2_scaled(q.w, up));
-                        }
-                        xb[ch][n][gl] = v;
+                        const int k = (q0 + f * kConsumerWarps) * 256 + 32 * gl + 8 * c;
+                        xb[f][gl] = r < n && k < H ? __ldg(reinterpret_cast<const uint4*>(xr + k)) : make_uint4(0, 0, 0, 0);
                     }
-                }
-            const bool vec = KGH % 8 == 0 && ((uintptr_t)a.s13 & 7) == 0;
-            auto scales_of = [&](int st, uint2& s0, uint2& s1) {
-                int k, slice;
-                s0 = s1 = make_uint2(0, 0);
-                if (!gate_up_slot(st, warp, k, slice) || k >= nunits) return;
-                const int u = b + k * G, i = u / upe;
-                const uint8_t* p = a.s13 + ((size_t)list_e[i] * 2 * I + (u - i * upe) * 8 + r) * KGH;
-                s0 = load_scales(p, slice, KGH, vec);
-                s1 = load_scales(p + (size_t)I * KGH, slice, KGH, vec);
+#pragma unroll
+                for (int f = 0; f < NC; ++f)
+#pragma unroll
+                    for (int gl = 0; gl < 8; ++gl) {
+                        const uint4 q = xb[f][gl];
+                        xb[f][gl] = make_uint4(bf16x2_to_f16x2_scaled(q.x, up), bf16x2_to_f16x2_scaled(q.y, up),
+                                               bf16x2_to_f16x2_scaled(q.z, up), bf16x2_to_f16x2_scaled(q.w, up));
+                    }
+                have = i;
             };
-            uint2 n0 = make_uint2(0, 0), n1 = n0;
-            if (gstages > 0) scales_of(0, n0, n1);
-            for (int st = 0; st < gstages; st += NC) {
-                float acc[NT][4];
+            for (int h = 0; h < ghands; ++h) {
+                float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-#pragma unroll
-                for (int ch = 0; ch < NC; ++ch, ++gs) {
-                    const int s = gs % kStages;
-                    const uint2 s0 = n0, s1 = n1;
-                    if (st + ch + 1 < gstages) scales_of(st + ch + 1, n0, n1);
-                    if (!failed && !mbar_wait_warp(&full[s], (gs / kStages) & 1)) failed = true;
-                    int k, slice;
-                    if (!failed && gate_up_slot(st + ch, warp, k, slice) && k < nunits) {
-                        const uint32_t m = list_m[(b + k * G) / upe];
-                        slot_mma<NT>(slot_base + s * kStageBytes, lm, s0, s1, xb[ch],
-                                     ((m & 0xFFu) ? 1u : 0u) | ((m & 0xFF00u) ? 2u : 0u), a, acc);
+                for (int i = 0; i < 2; ++i) {
+                    const int st = 2 * h + i, k = NC == 1 ? st * ups + j : h;
+                    if (st >= gstages) break;
+                    const bool on = j < ups && k < nunits && q0 + (NC == 1 ? 0 : i * kConsumerWarps) < sg;
+                    if (on && !failed) {
+                        int e, blk;
+                        unit_at(k, e, blk);
+                        if (e != have) load_x(e);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[s]);
+                    wait_stage(st);
+                    multiply(st, warp, on, xb[NC == 1 ? 0 : i], acc[NC == 1 ? i : 0]);
                 }
-                hand_over(acc);
+                hand_over(h, acc, NC > 1);
             }
         }
         // ----------------------------------------------------------- down
         {
+            const int j = spi > 1 ? 0 : warp / sd;          // this warp's item within a stage
+            const int q0 = spi > 1 ? warp : warp - j * sd;  // and its (first) slice
+            const int hpitch = shift_pitch(I);
+            uint4 hb[8];
+            int have = -1;  // entry (times stages per item, plus the chunk) whose h fragment is in hb
+            // h as f16 with one power of two for the row: each 8 values' own shift
+            // comes down to the row's
+            auto load_h = [&](int i, int slice, int key) {
+                const int n = list_p[i] & 15, p = (list_p[i] >> 4) + r;
+                have = key;
+#pragma unroll
+                for (int gl = 0; gl < 8; ++gl) hb[gl] = make_uint4(0, 0, 0, 0);
+                if (r >= n) return;
+                const uint16_t* hp = a.h + (size_t)p * I + 256 * slice + 8 * c;
+#pragma unroll
+                for (int gl = 0; gl < 8; ++gl)
+                    if (256 * slice + 32 * gl < I) hb[gl] = __ldcg(reinterpret_cast<const uint4*>(hp + 32 * gl));
+                const uint2 us = __ldcg(reinterpret_cast<const uint2*>(a.hshift + (size_t)p * hpitch + 32 * slice + 8 * c));
+                const int sh = f32_f16_shift(__ldcg(a.hmax + p));
+#pragma unroll
+                for (int gl = 0; gl < 8; ++gl) {
+                    if (256 * slice + 32 * gl >= I) break;
+                    const int u = (int)(int8_t)((gl < 4 ? us.x : us.y) >> (8 * (gl & 3)));
+                    const __half2 g = __float2half2_rn(__uint_as_float((uint32_t)max(127 + sh - u, 0) << 23));
+                    __half2* w = reinterpret_cast<__half2*>(&hb[gl]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[q] = __hmul2(w[q], g);
+                }
+            };
             if (!failed && !mbar_wait_warp(h_ready, 0)) failed = true;
             if (!failed && !info[2]) failed = true;
-            const bool vec = KGI % 8 == 0 && ((uintptr_t)a.s2 & 7) == 0;
-            float acc[NT][4];
-            int piece = 0;
-            auto clear = [&]() {
+            for (int h = 0; h < dhands; ++h) {
+                float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-            };
-            clear();
-            auto place = [&](long long slot, int& ru, int& i, int& slice) {
-                ru = (int)(slot / Q);
-                const int q = (int)(slot - (long long)ru * Q);
-                i = q / sd;
-                slice = q - i * sd;
-            };
-            auto scales_of = [&](long long slot, uint2& s0, uint2& s1) {
-                s0 = s1 = make_uint2(0, 0);
-                if (slot >= hi) return;
-                int ru, i, slice;
-                place(slot, ru, i, slice);
-                const uint8_t* p = a.s2 + ((size_t)list_e[i] * H + ru * 16 + r) * KGI;
-                s0 = load_scales(p, slice, KGI, vec);
-                s1 = load_scales(p + (size_t)8 * KGI, slice, KGI, vec);
-            };
-            uint2 n0, n1;
-            scales_of(lo + warp, n0, n1);
-            for (int st = 0; st < dstages; ++st, ++gs) {
-                const int s = gs % kStages;
-                const long long slot = lo + (long long)st * kConsumerWarps + warp;
-                const uint2 s0 = n0, s1 = n1;
-                scales_of(slot + kConsumerWarps, n0, n1);
-                int ru = 0, i = 0, slice = 0;
-                if (slot < hi) {
-                    place(slot, ru, i, slice);
-                    while (piece < ru - ru0) {  // this warp's part of the earlier rows is complete
-                        hand_over(acc);
-                        clear();
-                        ++piece;
+                for (int i = 0; i < 2; ++i) {
+                    const int st = 2 * h + i;
+                    if (st >= dstages) break;
+                    const int slice = q0 + (spi > 1 ? i * kConsumerWarps : 0);
+                    const int item = lo + (spi > 1 ? h : st * ips + j);
+                    const bool on = j < ips && item < hi && slice < sd;
+                    if (on && !failed) {
+                        const int e = (int)div_by((uint32_t)item, ru_m), key = e * spi + (spi > 1 ? i : 0);
+                        if (key != have) load_h(e, slice, key);
                     }
+                    wait_stage(gstages + st);
+                    if (spi == 1)
+                        multiply(gstages + st, warp, on, hb, acc[i]);
+                    else
+                        multiply(gstages + st, warp, on, hb, acc[0]);
                 }
-                uint4 hb[NT][8];
-                float f[NT];  // routing weight and 2^-sigma of this lane's token
-                uint32_t need = 0;
-                if (slot < hi && !failed) {
-                    const uint32_t m = list_m[i];
-                    need = ((m & 0xFFu) ? 1u : 0u) | ((m & 0xFF00u) ? 2u : 0u);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const int t = 8 * n + r;
-                        f[n] = 0.0f;
-#pragma unroll
-                        for (int gl = 0; gl < 8; ++gl) hb[n][gl] = make_uint4(0, 0, 0, 0);
-                        if ((m >> t) & 1u) {
-                            const int p = (int)(m >> 16) + __popc(m & ((1u << t) - 1u));
-                            const int sh = f32_f16_shift(__ldcg(a.hmax + p));
-                            const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
-                            f[n] = pair_w[p] * __uint_as_float((uint32_t)(127 - sh) << 23) * 0.5f;
-                            const float* hp = a.h + (size_t)p * I + 256 * slice + 8 * c;
-#pragma unroll
-                            for (int gl = 0; gl < 8; ++gl) {
-                                if (256 * slice + 32 * gl < I) {
-                                    const float4 u = __ldcg(reinterpret_cast<const float4*>(hp + 32 * gl));
-                                    const float4 v = __ldcg(reinterpret_cast<const float4*>(hp + 32 * gl) + 1);
-                                    const __half2 h0 = __floats2half2_rn(u.x * up, u.y * up);
-                                    const __half2 h1 = __floats2half2_rn(u.z * up, u.w * up);
-                                    const __half2 h2 = __floats2half2_rn(v.x * up, v.y * up);
-                                    const __half2 h3 = __floats2half2_rn(v.z * up, v.w * up);
-                                    hb[n][gl] = make_uint4(*reinterpret_cast<const uint32_t*>(&h0),
-                                                           *reinterpret_cast<const uint32_t*>(&h1),
-                                                           *reinterpret_cast<const uint32_t*>(&h2),
-                                                           *reinterpret_cast<const uint32_t*>(&h3));
-                                }
-                            }
-                        }
-                    }
-                }
-                if (!failed && !mbar_wait_warp(&full[s], (gs / kStages) & 1)) failed = true;
-                if (!failed && slot < hi) {
-                    float d[NT][4];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.0f;
-                    slot_mma<NT>(slot_base + s * kStageBytes, lm, s0, s1, hb, need, a, d);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        // columns 2c and 2c + 1: the factors of lanes with that r.  A token
-                        // that did not choose the expert adds nothing, whatever its column is
-                        const float g0 = __shfl_sync(0xFFFFFFFFu, f[n], 8 * c);
-                        const float g1 = __shfl_sync(0xFFFFFFFFu, f[n], 8 * c + 4);
-                        const uint32_t m2 = list_m[i] >> (8 * n + 2 * c);
-                        if (m2 & 1u) {
-                            acc[n][0] = fmaf(d[n][0], g0, acc[n][0]);
-                            acc[n][2] = fmaf(d[n][2], g0, acc[n][2]);
-                        }
-                        if (m2 & 2u) {
-                            acc[n][1] = fmaf(d[n][1], g1, acc[n][1]);
-                            acc[n][3] = fmaf(d[n][3], g1, acc[n][3]);
-                        }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-            }
-            for (; piece < pieces; ++piece) {
-                hand_over(acc);
-                clear();
+                hand_over(ghands + h, acc, spi > 1);
             }
         }
     } else {
         // ------------------------------------------------------- epilogue
-        const int r = lane >> 2, c = lane & 3;
-        uint32_t pc = 0;
+        // warp `me` takes the sums of a pair's stage `me` (the first one has those of
+        // units and items of two stages)
+        const int me = warp - kEpiWarp0, r = lane >> 2, c = lane & 3;
+        const int hpitch = shift_pitch(I);
         bool ok = routed;
-        // the sum of one n-tile's partial sums over warps w0 .. w0 + n - 1
-        auto sum_of = [&](int buf, int nt, int w0, int n) {
+        // the sum of warps w0 .. w0 + n - 1: this lane's rows r and r + 8 (x, z for column
+        // 2c, y, w for 2c + 1)
+        auto sum_of = [&](int buf, int w0, int n) {
             float4 v = make_float4(0, 0, 0, 0);
-            const float4* p = part + ((buf * NT + nt) * kConsumerWarps + w0) * 32 + lane;
+            const float4* p = part + ((buf * 2 + me) * kConsumerWarps + w0) * 32 + lane;
 #pragma unroll 4
             for (int w = 0; w < n; ++w) {
                 const float4 q = p[w * 32];
@@ -718,37 +866,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return v;
         };
-        for (int st = 0; st < gstages && ok; st += NC, ++pc) {
-            const int buf = pc & 1;
-            if (!mbar_wait_warp(&part_full[buf], (pc >> 1) & 1)) {
-                ok = false;
-                break;
-            }
+        for (int h = 0; h < ghands; ++h) {
+            const int buf = h & 1;
+            if (ok && !mbar_wait_warp(&part_full[buf], (h >> 1) & 1)) ok = false;
+            if (!ok) break;
             for (int j = 0; j < ups; ++j) {
-                const int k = NC == 1 ? st * ups + j : st / NC;
+                const int k = NC == 1 ? (2 * h + me) * ups + j : (me ? nunits : h);
                 if (k >= nunits) break;
-                const int u = b + k * G, i = u / upe;
-                const uint32_t m = list_m[i];
-                const int col = (u - i * upe) * 8 + r;  // of I
+                int i, blk;
+                unit_at(k, i, blk);
+                const int n = list_p[i] & 15, p0 = list_p[i] >> 4;
+                const float4 v = NC == 1 ? sum_of(buf, j * sg, sg) : sum_of(buf, 0, kConsumerWarps);
+                const float g[2] = {v.x, v.y}, up[2] = {v.z, v.w};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float4 v = sum_of(buf, nt, NC == 1 ? j * sg : 0, NC == 1 ? sg : kConsumerWarps);
-                    const float g[2] = {v.x, v.y}, up[2] = {v.z, v.w};
+                for (int q = 0; q < 2; ++q) {
+                    // this lane: row r of the unit's 8, pair p0 + 2c + q
+                    const int p = p0 + 2 * c + q;
+                    const bool on = 2 * c + q < n;
+                    const float rs = on ? rscale[pair_t[p]] : 0.0f;
+                    const float hv = on ? silu(g[q] * rs) * (up[q] * rs) : 0.0f;
+                    uint32_t mx = __float_as_uint(hv) & 0x7FFFFFFFu;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int t = 8 * nt + 2 * c + q;
-                        const bool on = (m >> t) & 1u;
-                        float hv = 0.0f;
-                        const int p = (int)(m >> 16) + __popc(m & ((1u << t) - 1u));
-                        if (on) {
-                            const float rs = rscale[t];
-                            hv = silu(g[q] * rs) * (up[q] * rs);
-                            a.h[(size_t)p * I + col] = hv;
+                    for (int o = 4; o < 32; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                    if (on) {
+                        const int sh = f32_f16_shift(mx);
+                        a.h[(size_t)p * I + blk * 8 + r] =
+                            __half_as_ushort(__float2half_rn(hv * __uint_as_float((uint32_t)(127 + sh) << 23)));
+                        if (r == 0) {
+                            // (eight zeros: a shift so high that they come down to zero)
+                            a.hshift[(size_t)p * hpitch + shift_at(blk)] = (int8_t)(mx ? sh : 127);
+                            atomicMax(a.hmax + p, mx);
                         }
-                        uint32_t mx = __float_as_uint(hv) & 0x7FFFFFFFu;
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-                        if (on && r == 0) atomicMax(a.hmax + p, mx);
                     }
                 }
             }
@@ -756,84 +904,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&part_free[buf]);
         }
         // h of this CTA is complete; wait for everybody's
-        __threadfence();
-        __syncwarp();
-        if (lane == 0 && ok) {
-            add_release(&a.sync[1]);
-            ok = grid_wait(&a.sync[1], (uint32_t)G);
+        ok = all_at_barrier(ok, 2, 64);
+        if (me == 0 && lane == 0) {
             if (ok) {
-                info[2] = 1;
-                // the last CTA past the second barrier leaves the counters at zero
-                if (add_release(&a.sync[2]) == (uint32_t)G - 1) {
-                    a.sync[0] = 0u;
-                    a.sync[1] = 0u;
-                    a.sync[2] = 0u;
+                add_release(&a.sync[1]);
+                if (grid_wait(&a.sync[1], (uint32_t)G)) info[2] = 1;
+            }
+            mbar_arrive(h_ready);
+        }
+        if (ok && !mbar_wait_warp(h_ready, 0)) ok = false;
+        ok = ok && info[2];
+
+        int have = -1;
+        float f[2] = {0, 0};  // 2^-sigma of the pairs in columns 2c and 2c + 1
+        for (int h = 0; h < dhands; ++h) {
+            const int buf = (ghands + h) & 1;
+            if (ok && !mbar_wait_warp(&part_full[buf], ((ghands + h) >> 1) & 1)) ok = false;
+            if (!ok) break;
+            for (int j = 0; j < ips; ++j) {
+                const int item = spi == 1 ? lo + (2 * h + me) * ips + j : (me ? hi : lo + h);
+                if (item >= hi) break;
+                const int i = (int)div_by((uint32_t)item, ru_m);
+                const int n = list_p[i] & 15, p = (list_p[i] >> 4) + 2 * c;
+                if (i != have) {
+                    have = i;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (2 * c + q < n)
+                            f[q] = __uint_as_float((uint32_t)(127 - f32_f16_shift(__ldcg(a.hmax + p + q))) << 23);
+                }
+                const float4 v = spi == 1 ? sum_of(buf, j * sd, sd) : sum_of(buf, 0, kConsumerWarps);
+                float* y = a.y + (size_t)p * H + (item - i * RU) * 16 + r;
+                if (2 * c < n) {
+                    __stcg(y, v.x * f[0]);
+                    __stcg(y + 8, v.z * f[0]);
+                }
+                if (2 * c + 1 < n) {
+                    __stcg(y + H, v.y * f[1]);
+                    __stcg(y + H + 8, v.w * f[1]);
                 }
             }
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-        if (lane == 0) mbar_arrive(h_ready);
-
-        for (int piece = 0; piece < pieces && ok; ++piece, ++pc) {
-            const int buf = pc & 1;
-            if (!mbar_wait_warp(&part_full[buf], (pc >> 1) & 1)) {
-                ok = false;
-                break;
-            }
-            const int ru = ru0 + piece;
-            float4 v[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) v[nt] = sum_of(buf, nt, 0, kConsumerWarps);
             __syncwarp();
             if (lane == 0) mbar_arrive(&part_free[buf]);
-            const long long s0 = (long long)ru * Q, s1 = s0 + Q;
-            bool write = true;
-            if (s0 < lo || s1 > hi) {
-                // rows cut between CTAs: the one that comes last adds the partial
-                // sums in CTA order
-                float4* mine = a.partial + ((size_t)b * 2 + (piece ? 1 : 0)) * NT * 32;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) __stcg(mine + nt * 32 + lane, v[nt]);
-                const int b0 = (int)(((s0 + 1) * G - 1) / slots), b1 = (int)((s1 * G - 1) / slots);
-                // (fewer slots than CTAs: some CTAs have none)
-                const uint32_t parts = slots >= G ? (uint32_t)(b1 - b0 + 1) : (uint32_t)Q;
-                __threadfence();
-                __syncwarp();
-                uint32_t old = 0;
-                if (lane == 0) old = add_release(&a.joined[ru]);
-                old = __shfl_sync(0xFFFFFFFFu, old, 0);
-                write = old == parts - 1;
-                if (write) {
-                    __threadfence();
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) v[nt] = make_float4(0, 0, 0, 0);
-                    for (int bb = b0; bb <= b1; ++bb) {
-                        const long long l0 = cut(slots, bb, G);
-                        if (l0 == cut(slots, bb + 1, G)) continue;
-                        const float4* p = a.partial + ((size_t)bb * 2 + (l0 / Q == ru ? 0 : 1)) * NT * 32 + lane;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float4 q = __ldcg(p + nt * 32);
-                            v[nt].x += q.x, v[nt].y += q.y, v[nt].z += q.z, v[nt].w += q.w;
-                        }
-                    }
-                }
-            }
-            if (write) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int t = 8 * nt + 2 * c;
-                    uint16_t* o = a.out + (size_t)t * H + ru * 16 + r;
-                    if (t < T) {
-                        o[0] = f32_to_bf16_bits(v[nt].x);
-                        o[8] = f32_to_bf16_bits(v[nt].z);
-                    }
-                    if (t + 1 < T) {
-                        o[H] = f32_to_bf16_bits(v[nt].y);
-                        o[H + 8] = f32_to_bf16_bits(v[nt].w);
-                    }
-                }
-            }
+        }
+        if (!ok && lane == 0) info[2] = 0;
+    }
+
+    // ------------------------------------------------------------ weighted sum
+    // once every CTA's y is there, each CTA adds up its share of the outputs
+    __syncthreads();
+    if (tid == 0 && info[2]) {
+        add_release(&a.sync[2]);
+        info[3] = grid_wait(&a.sync[2], (uint32_t)G) ? 1 : 0;
+        // the last CTA past this barrier leaves the counters at zero
+        if (info[3] && add_release(&a.sync[3]) == (uint32_t)G - 1)
+            a.sync[0] = a.sync[1] = a.sync[2] = a.sync[3] = 0u;
+    }
+    __syncthreads();
+    if (info[3]) {
+        const int n = T * H, q1 = cut(n, b + 1, G);
+        for (int q = cut(n, b, G) + tid; q < q1; q += kThreads) {
+            const int t = q / H, row = q - t * H;
+            float v = 0.0f;
+#pragma unroll 4
+            for (int j = 0; j < Kt; ++j)
+                v = fmaf(w_s[t * Kt + j], __ldcg(a.y + (size_t)pair_of[t * Kt + j] * H + row), v);
+            a.out[q] = f32_to_bf16_bits(v);
         }
     }
     pdl_end();
@@ -842,39 +978,75 @@ __global__ void __launch_bounds__(kThreads, 1)
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct FewWorkspace {
-    size_t sync, logits, hmax, joined, h, partial, total;
+    size_t sync, logits, hmax, h, hshift, y, total;
 };
 
 FewWorkspace few_workspace(int T, int H, int I, int E, int Kt) {
+    const size_t pairs = (size_t)T * Kt;
     FewWorkspace w;
     w.sync = 0;
     w.logits = 256;
     w.hmax = w.logits + align256((size_t)T * (E + 1) * 4);
-    w.joined = w.hmax + align256((size_t)T * Kt * 4);
-    w.h = w.joined + align256((size_t)(H / 16) * 4);
-    w.partial = w.h + align256((size_t)T * Kt * I * 4);
-    w.total = w.partial + (size_t)kMaxGrid * 2 * 2 * 512;
+    w.h = w.hmax + align256(pairs * 4);
+    w.hshift = w.h + align256(pairs * I * 2);
+    w.y = w.hshift + align256(pairs * shift_pitch(I));
+    w.total = w.y + align256(pairs * H * 4);
     return w;
 }
 
-template <int NT, int NC>
-cudaError_t launch_few(const FewArgs& a, const CUtensorMap& w13, const CUtensorMap& w2, int grid,
-                       cudaStream_t s) {
-    const size_t smem = FewLayout<NT>::kTotal;
-    cudaError_t err = ensure_dynamic_smem((const void*)layer_few_kernel<NT, NC>, smem);
+// The maps of FewMaps; those that no load uses stay empty.
+cudaError_t few_maps(const LayerFew& p, bool scales, FewMaps* m) {
+    const uint64_t Et = (uint64_t)p.E + p.shared, H = p.H, I = p.I;
+    const uint32_t sg = (uint32_t)p.H / 256, sd = (uint32_t)p.I / 256, most = kConsumerWarps;
+    cudaError_t err = cudaSuccess;
+    memset(m, 0, sizeof(*m));
+    {  // {128 bytes, row, gate or up, slice}
+        const uint64_t dims[4] = {128, Et * 2 * I - I, 2, sg}, strides[3] = {H / 2, I * (H / 2), 128};
+        const uint32_t box[4] = {128, 8, 2, std::min(sg, most)}, rest[4] = {128, 8, 2, sg - most};
+        if (sg > 0) err = encode_nd_map(&m->w13, p.w13, 4, dims, strides, box, true);
+        if (err == cudaSuccess && sg > most) err = encode_nd_map(&m->w13_rest, p.w13, 4, dims, strides, rest, true);
+    }
+    if (err == cudaSuccess && p.H % 256) {  // {byte of the row, row, gate or up}
+        const uint64_t dims[3] = {H / 2, Et * 2 * I - I, 2}, strides[2] = {H / 2, I * (H / 2)};
+        const uint32_t box[3] = {128, 8, 2};
+        err = encode_nd_map(&m->w13_tail, p.w13, 3, dims, strides, box, true);
+    }
+    if (err == cudaSuccess && scales) {  // {scale byte, row, gate or up}
+        const uint64_t dims[3] = {H / 32, Et * 2 * I - I, 2}, strides[2] = {H / 32, I * (H / 32)};
+        const uint32_t box[3] = {(uint32_t)std::min<uint64_t>(H / 32, 128), 8, 2};
+        err = encode_nd_map(&m->s13, p.s13, 3, dims, strides, box, false);
+    }
+    {  // {128 bytes, row, slice}
+        const uint64_t dims[3] = {128, Et * H, sd}, strides[2] = {I / 2, 128};
+        const uint32_t box[3] = {128, 16, std::min(sd, most)}, rest[3] = {128, 16, sd - most};
+        if (err == cudaSuccess && sd > 0) err = encode_nd_map(&m->w2, p.w2, 3, dims, strides, box, true);
+        if (err == cudaSuccess && sd > most) err = encode_nd_map(&m->w2_rest, p.w2, 3, dims, strides, rest, true);
+    }
+    if (err == cudaSuccess && p.I % 256) err = encode_codes_map(&m->w2_tail, p.w2, p.I / 2, Et * H, 128, 16);
+    if (err == cudaSuccess && scales) {
+        const uint64_t dims[2] = {I / 32, Et * H}, strides[1] = {I / 32};
+        const uint32_t box[2] = {(uint32_t)std::min<uint64_t>(I / 32, 128), 16};
+        err = encode_nd_map(&m->s2, p.s2, 2, dims, strides, box, false);
+    }
+    return err;
+}
+
+template <int NC, bool SF>
+cudaError_t launch_few(const FewArgs& a, const FewMaps& maps, int grid, cudaStream_t s) {
+    cudaError_t err = ensure_dynamic_smem((const void*)layer_few_kernel<NC, SF>, kSmemBytes);
     if (err != cudaSuccess) return err;
     // cooperative: the grid's CTAs wait for one another, so all must be resident
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layer_few_kernel<NT, NC>, a, w13, w2);
+    return cudaLaunchKernelEx(&cfg, layer_few_kernel<NC, SF>, a, maps);
 }
 
 }  // namespace
@@ -882,7 +1054,7 @@ cudaError_t launch_few(const FewArgs& a, const CUtensorMap& w13, const CUtensorM
 size_t layer_few_workspace(int T, int H, int I, int E, int Kt) { return few_workspace(T, H, I, E, Kt).total; }
 
 cudaError_t launch_layer_few(const LayerFew& p, void* workspace, cudaStream_t s) {
-    const int Kt = p.K + p.shared, Et = p.E + p.shared;
+    const int Kt = p.K + p.shared;
     const FewWorkspace L = few_workspace(p.T, p.H, p.I, p.E, Kt);
     char* ws = reinterpret_cast<char*>(workspace);
     FewArgs a;
@@ -897,9 +1069,9 @@ cudaError_t launch_layer_few(const LayerFew& p, void* workspace, cudaStream_t s)
     a.sync = reinterpret_cast<uint32_t*>(ws + L.sync);
     a.logits = reinterpret_cast<float*>(ws + L.logits);
     a.hmax = reinterpret_cast<uint32_t*>(ws + L.hmax);
-    a.joined = reinterpret_cast<uint32_t*>(ws + L.joined);
-    a.h = reinterpret_cast<float*>(ws + L.h);
-    a.partial = reinterpret_cast<float4*>(ws + L.partial);
+    a.h = reinterpret_cast<uint16_t*>(ws + L.h);
+    a.hshift = reinterpret_cast<int8_t*>(ws + L.hshift);
+    a.y = reinterpret_cast<float*>(ws + L.y);
     a.T = p.T;
     a.H = p.H;
     a.I = p.I;
@@ -907,22 +1079,21 @@ cudaError_t launch_layer_few(const LayerFew& p, void* workspace, cudaStream_t s)
     a.K = p.K;
     a.shared = p.shared;
     a.renorm = p.renormalize;
-    a.exp_one = a.exp_bias = 1u << 23;
-    CUtensorMap w13, w2;
-    cudaError_t err = encode_codes_map(&w13, p.w13, p.H / 2, (uint64_t)Et * 2 * p.I, 128, 8);
-    if (err != cudaSuccess) return err;
-    err = encode_codes_map(&w2, p.w2, p.I / 2, (uint64_t)Et * p.H, 128, 16);
+    // scale rows that the TMA can read: whole 16-byte units
+    const bool sf = p.H % 512 == 0 && p.I % 512 == 0 && ((uintptr_t)p.s13 | (uintptr_t)p.s2) % 16 == 0;
+    FewMaps maps;
+    cudaError_t err = few_maps(p, sf, &maps);
     if (err != cudaSuccess) return err;
     // no more CTAs than the widest phase has pieces of work for (a barrier of
     // fewer CTAs is shorter)
     const long long touched = std::min<long long>((long long)p.T * p.K, p.E) + p.shared;
-    const long long work = std::max({(long long)p.E + 1, touched * (p.I / 8),
-                                     (long long)(p.H / 16) * touched * ((p.I + 255) / 256)});
+    const int rows = p.E + (p.w_shared_gate ? 1 : 0);
+    const long long work = std::max({(long long)rows, touched * (p.I / 8), (long long)(p.H / 16) * touched});
     const int grid = (int)std::min<long long>({work, (long long)num_sms(), (long long)kMaxGrid});
-    if ((p.E + 1 + grid - 1) / grid > kMaxTasks) return cudaErrorNotSupported;
-    if (p.T > 8) return launch_few<2, 1>(a, w13, w2, grid, s);
-    if (p.H > 4096) return launch_few<1, 2>(a, w13, w2, grid, s);
-    return launch_few<1, 1>(a, w13, w2, grid, s);
+    a.router_rows = (rows + grid - 1) / grid;
+    if (a.router_rows > 16) return cudaErrorNotSupported;  // fewer than 65 SMs
+    if (p.H > 4096) return sf ? launch_few<2, true>(a, maps, grid, s) : launch_few<2, false>(a, maps, grid, s);
+    return sf ? launch_few<1, true>(a, maps, grid, s) : launch_few<1, false>(a, maps, grid, s);
 }
 
 cudaError_t read_device_error_few(int* flag, int clear) {

@@ -79,6 +79,25 @@ cudaError_t encode_codes_map(CUtensorMap* map, const void* base, int row_bytes, 
                          (uint64_t)row_bytes, box_bytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+cudaError_t encode_nd_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                          const uint64_t* strides, const uint32_t* box, bool swizzle) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rank < 1 || rank > 5) return cudaErrorNotSupported;
+    cuuint64_t d[5], st[4] = {0, 0, 0, 0};
+    cuuint32_t bx[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i] > 0 ? dims[i] : 1;
+        bx[i] = box[i];
+        estr[i] = 1;
+        if (i > 0) st[i - 1] = strides[i - 1];
+    }
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx,
+                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int num_sms() {
     static std::mutex mu;
     static int cached[64] = {0};
@@ -983,7 +1002,7 @@ moe_status_t moe_linear_mxfp4act(const void* x, moe_dtype_t x_type, int64_t ldx,
 
 static moe_status_t check_few(int T, int H, int I, int E, int K) {
     if (T < 0 || H < 1 || I < 1 || E < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-    if (T > kFewMaxT || H % 32 || I % 32 || H > few_max_h(T) || I > kFewMaxI || E > 1024 || K > 32 || K > E)
+    if (T > kFewMaxT || H % 32 || I % 32 || H > kFewMaxH || I > kFewMaxI || E > 1024 || K > 32 || K > E)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }

@@ -25,6 +25,12 @@ cudaError_t encode_2d_map(CUtensorMap* map, const void* base, CUtensorMapDataTyp
                           uint64_t rows, uint64_t row_stride, int box_inner, int box_rows,
                           CUtensorMapSwizzle swizzle);
 
+// TMA descriptor of a uint8 tensor of `rank` (2 .. 5) dimensions, innermost
+// first: dims, strides in bytes of dimensions 1 .. rank - 1, box; 128-byte
+// swizzle or none, zero fill out of bounds.
+cudaError_t encode_nd_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                          const uint64_t* strides, const uint32_t* box, bool swizzle);
+
 cudaError_t launch_route(const float* logits, const float* shared_w, int T, int E, int K,
                          int with_shared, int renormalize, int32_t* ids, float* w, cudaStream_t s);
 // Routing and permutation in one single-block launch (small batches).
@@ -307,9 +313,7 @@ cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStrea
 cudaError_t read_device_error_linear(int* flag, int clear);
 
 // The whole layer for a few tokens in one cooperative launch (layer_few.cu).
-constexpr int kFewMaxT = 16, kFewMaxI = 8192;
-// widest H for this many tokens (the x fragments stay in registers)
-inline int few_max_h(int T) { return T > 8 ? 4096 : 8192; }
+constexpr int kFewMaxT = 16, kFewMaxH = 8192, kFewMaxI = 8192;
 struct LayerFew {
     const uint16_t* x;              // bf16 [T][H]
     const uint16_t* w_router;       // bf16 [E][H]

@@ -97,6 +97,8 @@ SHAPES = [
     (7, 6144, 512, 16, 4, True, False), (5, 4128, 64, 9, 3, True, True), (4, 128, 8192, 4, 2, True, False),
     (16, 96, 4096, 700, 10, False, False), (5, 1024, 1024, 512, 10, True, True), (1, 4096, 1024, 64, 10, True, False),
     (16, 2048, 1024, 256, 8, True, False), (10, 32, 64, 300, 2, False, False),
+    (3, 8160, 4640, 3, 2, False, False), (8, 4384, 8160, 2, 1, False, False), (12, 4064, 6176, 2, 1, True, False),
+    (16, 8192, 512, 3, 2, True, True), (11, 6688, 160, 12, 3, False, False),
 ]
 
 
