@@ -89,37 +89,83 @@ __device__ __forceinline__ uint32_t quantize8(const float v[8], uint32_t& sbyte)
     return e2m1x8(v, mx_inv_scale(sbyte));
 }
 
-// x [T] rows of K values, ldx elements apart -> codes [T][K/2] and scales, a
-// row of `pitch` bytes per token (K/32 bytes, zeros up to the next multiple of
-// 8).  One warp takes 256 values of a row at a time, eight per lane: every load
-// and store is coalesced.  Bound by HBM for long prompts (2 bytes read and
-// 17/32 written per value), by launch latency for short ones.
+// Where the scale bytes of row r, k groups 4c .. 4c + 3 lie in the layout that the
+// pair kernel copies straight into tensor memory: 512-byte blocks of (128 rows, 128
+// k), within one the four 32-row quarters side by side.
+__device__ __forceinline__ size_t sf_block(int r, int c, int nch) {
+    return ((size_t)(r >> 7) * nch + c) * 512 + (size_t)((r & 31) * 16 + ((r >> 5) & 3) * 4);
+}
+
+struct QuantArgs {
+    const void* x;       // [T] rows of K values, ldx elements apart
+    long long ldx;
+    int T, K;
+    uint8_t* codes;      // [T][K/2]
+    uint8_t* scales;     // [T][pitch] (K/32 bytes, zeros up to the next multiple of 8), or
+    int pitch;           // with nch blocks of sf_block's layout (pitch 0)
+    int nch;
+    const uint8_t* ws;   // nch > 0: the weights' scale bytes [N][K/32], laid out in blocks too
+    uint8_t* wsb;
+    int N;
+    int xblocks;         // thread blocks that encode x; the others lay ws out
+};
+
+// One warp takes 256 values of a row at a time, eight per lane: every load and store is
+// coalesced.  Bound by HBM for long prompts (2 bytes read and 17/32 written per
+// value), by launch latency for short ones.  The weights' scales (1/16 of their codes'
+// bytes) are laid out by further blocks of the same launch: 16 groups of a row per
+// thread, neighbouring rows in neighbouring threads.
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(256)
-    quantize_rows_kernel(const void* __restrict__ x, long long ldx, int T, int K,
-                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int pitch) {
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
     pdl_begin();
+    if ((int)blockIdx.x >= a.xblocks) {
+        const int KG = a.K / 32, c4s = (a.nch + 3) / 4;
+        const bool vec = KG % 16 == 0 && ((uintptr_t)a.ws & 15) == 0;
+        const long long items = (long long)a.N * c4s;
+        for (long long it = (long long)((int)blockIdx.x - a.xblocks) * blockDim.x + threadIdx.x; it < items;
+             it += (long long)((int)gridDim.x - a.xblocks) * blockDim.x) {
+            const int c4 = (int)(it / a.N), r = (int)(it - (long long)c4 * a.N);
+            const uint8_t* p = a.ws + (size_t)r * KG + 16 * c4;
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (vec) {
+                if (16 * c4 < KG) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (16 * c4 + j < KG) w[j >> 2] |= (uint32_t)__ldg(p + j) << (8 * (j & 3));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * c4 + i < a.nch) *reinterpret_cast<uint32_t*>(a.wsb + sf_block(r, 4 * c4 + i, a.nch)) = w[i];
+        }
+        pdl_end();
+        return;
+    }
     const int lane = threadIdx.x & 31;
-    const int segs = (K + kBK - 1) / kBK;
-    const long long items = (long long)T * segs;
+    const int segs = (a.K + kBK - 1) / kBK;
+    const long long items = (long long)a.T * segs;
     const int esize = F32 ? 4 : 2;
     for (long long it = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items;
-         it += (long long)gridDim.x * (blockDim.x >> 5)) {
+         it += (long long)a.xblocks * (blockDim.x >> 5)) {
         const int t = (int)(it / segs), seg = (int)(it - (long long)t * segs);
         const int k = seg * kBK + lane * 8;
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (k < K)
-            load8<F32, VEC>(reinterpret_cast<const char*>(x) + ((size_t)t * ldx + k) * esize, v);
+        if (k < a.K)
+            load8<F32, VEC>(reinterpret_cast<const char*>(a.x) + ((size_t)t * a.ldx + k) * esize, v);
         uint32_t sb;
         const uint32_t c = quantize8(v, sb);
-        if (k < K) *reinterpret_cast<uint32_t*>(codes + (size_t)t * (K / 2) + k / 2) = c;
+        if (k < a.K) *reinterpret_cast<uint32_t*>(a.codes + (size_t)t * (a.K / 2) + k / 2) = c;
         // lanes 0 and 16: the four scale bytes of their 128 values
         uint32_t w = sb;
         w |= __shfl_down_sync(0xFFFFFFFFu, sb, 4) << 8;
         w |= __shfl_down_sync(0xFFFFFFFFu, sb, 8) << 16;
         w |= __shfl_down_sync(0xFFFFFFFFu, sb, 12) << 24;
         if ((lane & 15) == 0)
-            *reinterpret_cast<uint32_t*>(scales + (size_t)t * pitch + seg * 8 + (lane >> 4) * 4) = w;
+            *reinterpret_cast<uint32_t*>(a.scales + (a.pitch ? (size_t)t * a.pitch + seg * 8 + (lane >> 4) * 4
+                                                             : sf_block(t, 2 * seg + (lane >> 4), a.nch))) = w;
     }
     pdl_end();
 }
@@ -147,6 +193,65 @@ __device__ __forceinline__ void store_out(const StreamArgs& a, int t, int n, flo
             v += __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.residual)[(size_t)t * a.ldr + n] << 16);
         reinterpret_cast<uint16_t*>(a.out)[(size_t)t * a.ldo + n] = f32_to_bf16_bits(v);
     }
+}
+
+// 32 rows (tokens t0 ..) x 32 columns (n0 ..) of fp32 staged in shared memory, row pitch
+// `pitch`, to the output: 16 bytes a lane in rows of 64 (bf16) or 128 bytes, or, where
+// rows or the right edge do not allow it, element by element.  All 32 lanes call it.
+__device__ __forceinline__ void store_block(const StreamArgs& a, bool vec, const float* stg, int pitch, int t0, int n0,
+                                            int lane) {
+    if (!vec || n0 + 32 > a.N) {
+        for (int r = 0; r < 32 && t0 + r < a.T; ++r)
+            if (n0 + lane < a.N) store_out(a, t0 + r, n0 + lane, stg[r * pitch + lane]);
+        return;
+    }
+    if (a.out_f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7), t = t0 + r;
+            if (t >= a.T) break;
+            float4 v = *reinterpret_cast<const float4*>(stg + r * pitch + c);
+            if (a.residual) {
+                const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.residual) + (size_t)t * a.ldr + n0 + c);
+                v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+            }
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + (size_t)t * a.ldo + n0 + c) = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2), c = 8 * (lane & 3), t = t0 + r;
+            if (t >= a.T) break;
+            const float4 u = *reinterpret_cast<const float4*>(stg + r * pitch + c);
+            const float4 w = *reinterpret_cast<const float4*>(stg + r * pitch + c + 4);
+            float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+            if (a.residual) {
+                const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.residual) + (size_t)t * a.ldr + n0 + c);
+                const uint32_t qq[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[2 * k] += bf16_lo(qq[k]), v[2 * k + 1] += bf16_hi(qq[k]);
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = (uint32_t)f32_to_bf16_bits(v[2 * k]) | (uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16;
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (size_t)t * a.ldo + n0 + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+StreamArgs stream_args(const LinearMxfp4& p) {
+    StreamArgs a = {};
+    a.scales = p.scales;
+    a.residual = p.residual;
+    a.out = p.out;
+    a.ldr = p.ldr;
+    a.ldo = p.ldo;
+    a.T = p.T;
+    a.N = p.N;
+    a.K = p.K;
+    a.out_f32 = p.out_f32;
+    return a;
 }
 
 constexpr int kStreamThreads = 192;
@@ -379,6 +484,274 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     pdl_end();
 }
 
+// ------------------------------------------------------ product, large batches
+
+// Long prompts are bound by the tensor cores (and by what feeds them), so tokens are
+// the MMA's M side in pairs of CTAs (cta_group::2: 256 tokens x TN weight rows,
+// each CTA loading its 128 tokens and half of the weight rows), persistent, in
+// an order that keeps a weight tile on neighbouring pairs.  A stage (256 k) also brings
+// its scale bytes, already in tensor memory's layout (sf_block): the MMA thread copies
+// them there itself (tcgen05.cp, in order before the MMAs that read them), so no warp
+// handles scales.  Eight epilogue warps read the accumulator into registers,
+// free it, and store through shared memory in full rows of 64 or 128 bytes.
+// TN = 256 halves what crosses L2 -> shared memory per product (the bound of
+// this shape: 8 KB a CTA per 256 x 256 x 64 MMA, 64 bytes a clock) but has room for one
+// accumulator only; TN = 128 has two, and twice the tiles.
+struct PairArgs {
+    const uint8_t* sfa;   // x's scale blocks, ceil(T / 256) * 2 of nch
+    const uint8_t* sfb;   // the weights', ceil(N / 256) * 2 of nch
+    int nch;
+    StreamArgs o;         // output, residual, sizes
+    int vec;              // 16-byte stores (and residual loads)
+};
+
+constexpr int kPairThreads = 384;
+constexpr int kPairEpiWarp0 = 4;
+
+template <int TN>
+struct PairLayout {
+    static constexpr int kBRows = TN / 2;                     // weight rows per CTA
+    static constexpr int kBBytes = kBRows * kRowBytes;
+    static constexpr int kSfaBytes = 1024;                    // 128 tokens x 256 k
+    static constexpr int kSfbBytes = TN / 128 * 1024;         // all TN weight rows
+    static constexpr int kSf = kABytes + kBBytes;
+    static constexpr int kStage = kSf + kSfaBytes + kSfbBytes;
+    static_assert(kStage % 1024 == 0, "alignment");
+    static constexpr int kStgRow = 36;                        // fp32 per staged row, padded
+    static constexpr int kStgWarp = 32 * kStgRow * 4;
+    static constexpr int kFit = (232448 - 1024 - 256 - 8 * kStgWarp) / kStage;
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kStg = kStages * kStage;
+    static constexpr int kBar = kStg + 8 * kStgWarp;
+    static constexpr int kTotal = kBar + 256 + 1024;
+    static_assert(kStages >= 4 && kTotal <= 232448, "shared memory");
+    // tensor memory: accumulators, then 32 columns of scale factors per stage (tokens at
+    // +0 and +8 for the two 128-k chunks, weights at +16 and +24)
+    static constexpr int kAccBufs = TN == 128 ? 2 : 1;
+    static constexpr int kSfCol0 = kAccBufs * TN;
+    static_assert(kSfCol0 + kStages * 32 <= 512, "tensor memory");
+};
+
+// 32 rows of 16 bytes (512 contiguous bytes) from shared memory to 4 columns of tensor
+// memory, the same in every lane quadrant, in both CTAs of the pair from their own
+// shared memory.  In order with this thread's MMAs.
+__device__ __forceinline__ void copy_sf_pair(uint32_t taddr, uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;             // leading byte offset (unused)
+    d |= (uint64_t)(128u >> 4) << 32;    // next 8 rows
+    d |= (uint64_t)1u << 46;             // descriptor version; no swizzle
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+template <int TN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const PairArgs a, const __grid_constant__ CUtensorMap x_map,
+                       const __grid_constant__ CUtensorMap w_map) {
+    using L = PairLayout<TN>;
+    constexpr int kStages = L::kStages, kAccBufs = L::kAccBufs;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* tma_full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // this CTA's loads
+    uint64_t* peer_full = tma_full + kStages;   // even CTA: the odd one's loads
+    uint64_t* stage_free = peer_full + kStages;
+    uint64_t* acc_full = stage_free + kStages;  // [2]
+    uint64_t* acc_free = acc_full + 2;          // [2], even CTA: drained by both
+    uint64_t* drain = acc_free + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)(blockIdx.x & 1u), pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int T = a.o.T, N = a.o.N;
+    const int mts = (T + 255) / 256, nts = (N + TN - 1) / TN, tiles = mts * nts;
+    const int nk = (a.o.K + kBK - 1) / kBK;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&tma_full[s], 1);
+            mbar_init(&peer_full[s], 1);
+            mbar_init(&stage_free[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_free[b], 16);
+        }
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<true>(tmem_slot, 512);
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_begin();
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer
+        if (lane == 0) {
+            uint32_t gs = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                const int nt = tile / mts, mt = tile - nt * mts;
+                const int arow = mt * 256 + rank * 128, brow = nt * TN + rank * L::kBRows;
+                const uint8_t* sfa = a.sfa + (size_t)(mt * 2 + rank) * a.nch * 512;
+                const uint8_t* sfb = a.sfb + (size_t)nt * (TN / 128) * a.nch * 512;
+                for (int st = 0; st < nk; ++st, ++gs) {
+                    const int s = gs % kStages;
+                    if (gs >= (uint32_t)kStages && !mbar_wait(&stage_free[s], ((gs / kStages) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t base = smem_u32(smem + s * L::kStage);
+                    mbar_arrive_expect_tx(&tma_full[s], (uint32_t)L::kStage);
+                    tma_load_2d(base, &x_map, st * kRowBytes, arow, &tma_full[s]);
+                    tma_load_2d(base + kABytes, &w_map, st * kRowBytes, brow, &tma_full[s]);
+                    bulk_copy_g2s(base + L::kSf, sfa + (size_t)st * 1024, 1024, &tma_full[s]);
+#pragma unroll
+                    for (int j = 0; j < TN / 128; ++j)
+                        bulk_copy_g2s(base + L::kSf + L::kSfaBytes + j * 1024,
+                                      sfb + ((size_t)j * a.nch + 2 * st) * 512, 1024, &tma_full[s]);
+                }
+            }
+            // wait (bounded) until the last loads landed before the CTA can exit
+            for (int d = 0; d < kStages && d < (int)gs; ++d) {
+                const uint32_t u = gs - 1 - d;
+                if (!mbar_wait(&tma_full[u % kStages], (u / kStages) & 1)) break;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // -------------------------------------------------------- MMA
+            constexpr uint32_t id0 = idesc_mxf4(256, TN, 0), id2 = idesc_mxf4(256, TN, 2);
+            uint32_t gs = 0, it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs, ++it) {
+                const uint32_t b = it % kAccBufs;
+                if (it >= (uint32_t)kAccBufs && !mbar_wait(&acc_free[b], ((it / kAccBufs) - 1) & 1)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem + b * TN;
+                for (int st = 0; st < nk; ++st, ++gs) {
+                    const int s = gs % kStages;
+                    const uint32_t par = (gs / kStages) & 1;
+                    if (!mbar_wait(&tma_full[s], par) || !mbar_wait(&peer_full[s], par)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t base = smem_u32(smem + s * L::kStage);
+                    const uint32_t sf = tmem + (uint32_t)(L::kSfCol0 + s * 32);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        copy_sf_pair(sf + 8u * c, base + L::kSf + c * 512);
+#pragma unroll
+                        for (int j = 0; j < TN / 128; ++j)
+                            copy_sf_pair(sf + 16u + 8u * c + 4u * j, base + L::kSf + L::kSfaBytes + j * 1024 + c * 512);
+                    }
+                    const uint64_t ad = sdesc_sw128(base), bd = sdesc_sw128(base + kABytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // K = 64 each: +32 bytes in the swizzle atom
+                        mma_mxf4_pair(d_tmem, ad + 2u * kk, bd + 2u * kk, (kk & 1) ? id2 : id0, sf + 8u * (kk >> 1),
+                                      sf + 16u + 8u * (kk >> 1), (st | kk) != 0 ? 1u : 0u);
+                    mma_commit_pair(&stage_free[s]);
+                }
+                if (ok) mma_commit_pair(&acc_full[b]);
+            }
+            mma_commit_pair(drain);  // every MMA issued has completed when this arrives
+            mbar_wait(drain, 0);
+        } else if (lane == 0) {
+            // the odd CTA: tell the even one when this CTA's stages have landed
+            uint32_t gs = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs)
+                for (int st = 0; st < nk; ++st, ++gs) {
+                    const int s = gs % kStages;
+                    if (!mbar_wait(&tma_full[s], (gs / kStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_remote(&peer_full[s], 0);
+                }
+            mbar_wait(drain, 0);  // the pair's MMAs and their commits to this CTA are done
+        }
+    } else if (warp >= kPairEpiWarp0) {
+        // -------------------------------------------------------- epilogue
+        constexpr int kCols = TN / 2;  // columns per warp
+        const int quad = warp & 3, half = (warp - kPairEpiWarp0) >> 2;
+        float* stg = reinterpret_cast<float*>(smem + L::kStg + (warp - kPairEpiWarp0) * L::kStgWarp);
+        uint32_t it = 0;
+        for (int tile = pair; tile < tiles; tile += pairs, ++it) {
+            const int nt = tile / mts, mt = tile - nt * mts;
+            const uint32_t b = it % kAccBufs;
+            if (!mbar_wait_warp(&acc_full[b], (it / kAccBufs) & 1)) break;
+            tc_fence_after();
+            uint32_t v[kCols];
+            const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16) + b * TN + (uint32_t)(half * kCols);
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) tmem_ld16_nowait(taddr + c, v + c);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {  // drained: the next tile may use it
+                if (rank == 0)
+                    mbar_arrive(&acc_free[b]);
+                else
+                    mbar_arrive_remote(&acc_free[b], 0);
+            }
+            const int t0 = mt * 256 + rank * 128 + quad * 32, n0 = nt * TN + half * kCols;
+            if (t0 >= T) continue;
+#pragma unroll
+            for (int ch = 0; ch < kCols / 32; ++ch) {
+                if (n0 + ch * 32 >= N) break;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<uint4*>(stg + lane * L::kStgRow + 4 * q) =
+                        make_uint4(v[ch * 32 + 4 * q], v[ch * 32 + 4 * q + 1], v[ch * 32 + 4 * q + 2], v[ch * 32 + 4 * q + 3]);
+                __syncwarp();
+                store_block(a.o, a.vec != 0, stg, L::kStgRow, t0, n0 + ch * 32, lane);
+                __syncwarp();
+            }
+        }
+    }
+
+    tc_fence_before();
+    // neither CTA releases its memory while the other may still arrive there or the
+    // pair's MMAs may still run
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<true>(tmem, 512);
+    }
+    pdl_end();
+}
+
+template <int TN>
+cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* sfa, const uint8_t* sfb, int nch,
+                        cudaStream_t s) {
+    const size_t smem = PairLayout<TN>::kTotal;
+    cudaError_t err = ensure_dynamic_smem((const void*)linear_pair_kernel<TN>, smem);
+    if (err != cudaSuccess) return err;
+    CUtensorMap w_map, x_map;
+    err = encode_codes_map(&w_map, p.codes, p.K / 2, (uint64_t)p.N, kRowBytes, TN / 2);
+    if (err != cudaSuccess) return err;
+    err = encode_codes_map(&x_map, xcodes, p.K / 2, (uint64_t)p.T, kRowBytes, kMRows);
+    if (err != cudaSuccess) return err;
+    int pairs = 0;
+    err = max_active_pairs((const void*)linear_pair_kernel<TN>, kPairThreads, smem, &pairs);
+    if (err != cudaSuccess) return err;
+    if (pairs < 1) return cudaErrorNotSupported;
+    PairArgs a;
+    a.sfa = sfa;
+    a.sfb = sfb;
+    a.nch = nch;
+    a.o = stream_args(p);
+    const size_t es = p.out_f32 ? 4 : 2;
+    a.vec = (uintptr_t)p.out % 16 == 0 && p.ldo * es % 16 == 0 &&
+            (!p.residual || ((uintptr_t)p.residual % 16 == 0 && p.ldr * es % 16 == 0));
+    const long long tiles = (long long)((p.T + 255) / 256) * ((p.N + TN - 1) / TN);
+    const int grid = 2 * (int)std::min<long long>(tiles, pairs);
+    return launch_pdl_cluster(linear_pair_kernel<TN>, dim3((unsigned)grid), dim3(kPairThreads), smem, s, 2u, a, x_map, w_map);
+}
+
 template <int NT>
 cudaError_t launch_stream(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* xscales, int xpitch,
                           cudaStream_t s) {
@@ -390,18 +763,9 @@ cudaError_t launch_stream(const LinearMxfp4& p, const uint8_t* xcodes, const uin
     if (err != cudaSuccess) return err;
     err = encode_codes_map(&x_map, xcodes, p.K / 2, (uint64_t)p.T, kRowBytes, NT);
     if (err != cudaSuccess) return err;
-    StreamArgs a;
-    a.scales = p.scales;
+    StreamArgs a = stream_args(p);
     a.xscales = xscales;
     a.xpitch = xpitch;
-    a.residual = p.residual;
-    a.out = p.out;
-    a.ldr = p.ldr;
-    a.ldo = p.ldo;
-    a.T = p.T;
-    a.N = p.N;
-    a.K = p.K;
-    a.out_f32 = p.out_f32;
     const int row_tiles = (p.N + kMRows - 1) / kMRows, tok_tiles = (p.T + NT - 1) / NT;
     const int nk = (p.K + kBK - 1) / kBK;
     // split K while the CTAs do not fill two per SM and every split has a stage
@@ -413,42 +777,58 @@ cudaError_t launch_stream(const LinearMxfp4& p, const uint8_t* xcodes, const uin
 }
 
 template <bool F32>
-cudaError_t launch_quantize_rows(const LinearMxfp4& p, uint8_t* codes, uint8_t* scales, int pitch,
-                                 cudaStream_t s) {
-    const long long items = (long long)p.T * ((p.K + kBK - 1) / kBK);
-    const int blocks = (int)std::min<long long>((items + 7) / 8, (long long)num_sms() * 8);
+cudaError_t launch_quantize_rows(QuantArgs a, cudaStream_t s) {
+    const long long items = (long long)a.T * ((a.K + kBK - 1) / kBK);
+    a.xblocks = (int)std::min<long long>((items + 7) / 8, (long long)num_sms() * 8);
+    const int wblocks = a.nch ? (int)std::min<long long>(((long long)a.N * ((a.nch + 3) / 4) + 255) / 256, (long long)num_sms() * 4) : 0;
     // 16-byte loads where every row starts on a 16-byte boundary
-    const bool vec = ((uintptr_t)p.x % 16) == 0 && (p.ldx * (F32 ? 4 : 2)) % 16 == 0;
-    return vec ? launch_pdl(quantize_rows_kernel<F32, true>, dim3(blocks), dim3(256), 0, s, p.x, p.ldx, p.T, p.K,
-                            codes, scales, pitch)
-               : launch_pdl(quantize_rows_kernel<F32, false>, dim3(blocks), dim3(256), 0, s, p.x, p.ldx, p.T, p.K,
-                            codes, scales, pitch);
+    const bool vec = ((uintptr_t)a.x % 16) == 0 && (a.ldx * (F32 ? 4 : 2)) % 16 == 0;
+    return launch_pdl(vec ? quantize_rows_kernel<F32, true> : quantize_rows_kernel<F32, false>, dim3(a.xblocks + wblocks),
+                      dim3(256), 0, s, a);
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // bytes of a token's scale row: whole stages
 int xscale_pitch(int K) { return (K + kBK - 1) / kBK * 8; }
+// bytes of `rows` rows' scale blocks, whole tiles of 256 rows
+size_t sf_bytes(int rows, int K) { return (size_t)((rows + 255) / 256) * 2 * (size_t)((K + kBK - 1) / kBK) * 1024; }
+
+// Batches from here on go to the CTA pairs.
+bool use_pairs(int T, int N) { return T >= 256 && N >= 128; }
 
 }  // namespace
 
 size_t linear_mxfp4_workspace(int T, int N, int K) {
-    (void)N;
-    return align256((size_t)T * (K / 2)) + align256((size_t)T * xscale_pitch(K));
+    const size_t codes = align256((size_t)T * (K / 2));
+    return use_pairs(T, N) ? codes + sf_bytes(T, K) + sf_bytes(N, K) : codes + align256((size_t)T * xscale_pitch(K));
 }
 
 cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStream_t s) {
-    uint8_t* codes = reinterpret_cast<uint8_t*>(workspace);
-    uint8_t* scales = codes + align256((size_t)p.T * (p.K / 2));
-    const int pitch = xscale_pitch(p.K);
-    cudaError_t err = p.x_f32 ? launch_quantize_rows<true>(p, codes, scales, pitch, s)
-                              : launch_quantize_rows<false>(p, codes, scales, pitch, s);
+    QuantArgs q = {};
+    q.x = p.x;
+    q.ldx = p.ldx;
+    q.T = p.T;
+    q.K = p.K;
+    q.codes = reinterpret_cast<uint8_t*>(workspace);
+    q.scales = q.codes + align256((size_t)p.T * (p.K / 2));
+    const bool pairs = use_pairs(p.T, p.N);
+    if (pairs) {
+        q.nch = (p.K + kBK - 1) / kBK * 2;
+        q.ws = p.scales;
+        q.wsb = q.scales + sf_bytes(p.T, p.K);
+        q.N = p.N;
+    } else {
+        q.pitch = xscale_pitch(p.K);
+    }
+    cudaError_t err = p.x_f32 ? launch_quantize_rows<true>(q, s) : launch_quantize_rows<false>(q, s);
     if (err != cudaSuccess) return err;
+    if (pairs) return launch_pair<256>(p, q.codes, q.scales, q.wsb, q.nch, s);
     // the narrowest token tile that holds the batch
-    if (p.T <= 16) return launch_stream<16>(p, codes, scales, pitch, s);
-    if (p.T <= 32) return launch_stream<32>(p, codes, scales, pitch, s);
-    if (p.T <= 64) return launch_stream<64>(p, codes, scales, pitch, s);
-    return launch_stream<128>(p, codes, scales, pitch, s);
+    if (p.T <= 16) return launch_stream<16>(p, q.codes, q.scales, q.pitch, s);
+    if (p.T <= 32) return launch_stream<32>(p, q.codes, q.scales, q.pitch, s);
+    if (p.T <= 64) return launch_stream<64>(p, q.codes, q.scales, q.pitch, s);
+    return launch_stream<128>(p, q.codes, q.scales, q.pitch, s);
 }
 
 cudaError_t read_device_error_linear(int* flag, int clear) {
