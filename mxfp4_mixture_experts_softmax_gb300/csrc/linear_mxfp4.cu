@@ -4,7 +4,8 @@
 //   out[t, n] = residual[t, n] + sum_k decode(W)[n, k] * xq[t, k]
 // with fp32 sums and one rounding to the output type.
 //
-// quantize_rows_kernel encodes x; linear_stream_kernel multiplies, on the
+// quantize_rows_kernel encodes x; linear_stream_kernel (linear_pair_kernel for large
+// batches) multiplies, on the
 // block-scaled tensor cores (tcgen05.mma kind::mxf4, both scales applied by the
 // MMA, K = 64 an instruction).
 //
@@ -24,7 +25,8 @@
 //   * MMA warp: one thread;
 //   * 4 warps, one per tensor-memory lane quadrant: write each stage's scale
 //     factors into tensor memory (layout as in ffn_mxfp4act.cu), then drain the
-//     accumulator.
+//     accumulator.  For up to 16 tokens whose CTAs all run at once they also encode
+//     the stage's part of x themselves (FUSED): one launch, 3 us less than two.
 // Every wait is bounded (see mbar_wait).
 #include <algorithm>
 
@@ -89,11 +91,10 @@ __device__ __forceinline__ uint32_t quantize8(const float v[8], uint32_t& sbyte)
     return e2m1x8(v, mx_inv_scale(sbyte));
 }
 
-// Where the scale bytes of row r, k groups 4c .. 4c + 3 lie in the layout that the
-// pair kernel copies straight into tensor memory: 512-byte blocks of (128 rows, 128
-// k), within one the four 32-row quarters side by side.
-__device__ __forceinline__ size_t sf_block(int r, int c, int nch) {
-    return ((size_t)(r >> 7) * nch + c) * 512 + (size_t)((r & 31) * 16 + ((r >> 5) & 3) * 4);
+// Where the eight scale bytes of row r, stage st (256 k) lie for the pair kernel:
+// blocks of (128 rows, one stage), a kilobyte each.
+__device__ __forceinline__ size_t sf_block(int r, int st, int nk) {
+    return ((size_t)(r >> 7) * nk + st) * 1024 + (size_t)(r & 127) * 8;
 }
 
 struct QuantArgs {
@@ -102,70 +103,81 @@ struct QuantArgs {
     int T, K;
     uint8_t* codes;      // [T][K/2]
     uint8_t* scales;     // [T][pitch] (K/32 bytes, zeros up to the next multiple of 8), or
-    int pitch;           // with nch blocks of sf_block's layout (pitch 0)
-    int nch;
-    const uint8_t* ws;   // nch > 0: the weights' scale bytes [N][K/32], laid out in blocks too
+    int pitch;           // 0: in sf_block's layout, and
+    const uint8_t* ws;   // the weights' scale bytes [N][K/32] in it too
     uint8_t* wsb;
     int N;
     int xblocks;         // thread blocks that encode x; the others lay ws out
+    int parts;           // warps that share a row of x
 };
 
 // One warp takes 256 values of a row at a time, eight per lane: every load and store is
-// coalesced.  Bound by HBM for long prompts (2 bytes read and 17/32 written per
-// value), by launch latency for short ones.  The weights' scales (1/16 of their codes'
-// bytes) are laid out by further blocks of the same launch: 16 groups of a row per
+// coalesced; kQuantAhead such loads are in flight per lane.  Bound by HBM for long
+// prompts (2 bytes read and 17/32 written per value), by launch latency for short
+// ones.  The weights' scales (1/16 of their codes'
+// bytes) are laid out by further blocks of the same launch: two stages of a row per
 // thread, neighbouring rows in neighbouring threads.
+constexpr int kQuantAhead = 4;
+
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
     pdl_begin();
     if ((int)blockIdx.x >= a.xblocks) {
-        const int KG = a.K / 32, c4s = (a.nch + 3) / 4;
+        const int KG = a.K / 32, nk = (a.K + kBK - 1) / kBK, pairs = (nk + 1) / 2;
         const bool vec = KG % 16 == 0 && ((uintptr_t)a.ws & 15) == 0;
-        const long long items = (long long)a.N * c4s;
-        for (long long it = (long long)((int)blockIdx.x - a.xblocks) * blockDim.x + threadIdx.x; it < items;
-             it += (long long)((int)gridDim.x - a.xblocks) * blockDim.x) {
-            const int c4 = (int)(it / a.N), r = (int)(it - (long long)c4 * a.N);
-            const uint8_t* p = a.ws + (size_t)r * KG + 16 * c4;
+        const uint32_t items = (uint32_t)a.N * (uint32_t)pairs;  // (at most 2^24 x 2^7)
+        for (uint32_t it = ((uint32_t)blockIdx.x - (uint32_t)a.xblocks) * blockDim.x + threadIdx.x; it < items;
+             it += (gridDim.x - (uint32_t)a.xblocks) * blockDim.x) {
+            const int p2 = (int)(it / (uint32_t)a.N), r = (int)(it - (uint32_t)p2 * (uint32_t)a.N);
+            const uint8_t* p = a.ws + (size_t)r * KG + 16 * p2;
             uint32_t w[4] = {0, 0, 0, 0};
-            if (vec) {
-                if (16 * c4 < KG) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                }
+            if (vec) {  // K is a multiple of 512: whole pairs
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (16 * c4 + j < KG) w[j >> 2] |= (uint32_t)__ldg(p + j) << (8 * (j & 3));
+                    if (16 * p2 + j < KG) w[j >> 2] |= (uint32_t)__ldg(p + j) << (8 * (j & 3));
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (4 * c4 + i < a.nch) *reinterpret_cast<uint32_t*>(a.wsb + sf_block(r, 4 * c4 + i, a.nch)) = w[i];
+            *reinterpret_cast<uint2*>(a.wsb + sf_block(r, 2 * p2, nk)) = make_uint2(w[0], w[1]);
+            if (2 * p2 + 1 < nk) *reinterpret_cast<uint2*>(a.wsb + sf_block(r, 2 * p2 + 1, nk)) = make_uint2(w[2], w[3]);
         }
         pdl_end();
         return;
     }
     const int lane = threadIdx.x & 31;
-    const int segs = (a.K + kBK - 1) / kBK;
-    const long long items = (long long)a.T * segs;
+    const int segs = (a.K + kBK - 1) / kBK, chunk = (segs + a.parts - 1) / a.parts;
     const int esize = F32 ? 4 : 2;
-    for (long long it = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items;
-         it += (long long)a.xblocks * (blockDim.x >> 5)) {
-        const int t = (int)(it / segs), seg = (int)(it - (long long)t * segs);
-        const int k = seg * kBK + lane * 8;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (k < a.K)
-            load8<F32, VEC>(reinterpret_cast<const char*>(a.x) + ((size_t)t * a.ldx + k) * esize, v);
-        uint32_t sb;
-        const uint32_t c = quantize8(v, sb);
-        if (k < a.K) *reinterpret_cast<uint32_t*>(a.codes + (size_t)t * (a.K / 2) + k / 2) = c;
-        // lanes 0 and 16: the four scale bytes of their 128 values
-        uint32_t w = sb;
-        w |= __shfl_down_sync(0xFFFFFFFFu, sb, 4) << 8;
-        w |= __shfl_down_sync(0xFFFFFFFFu, sb, 8) << 16;
-        w |= __shfl_down_sync(0xFFFFFFFFu, sb, 12) << 24;
-        if ((lane & 15) == 0)
-            *reinterpret_cast<uint32_t*>(a.scales + (a.pitch ? (size_t)t * a.pitch + seg * 8 + (lane >> 4) * 4
-                                                             : sf_block(t, 2 * seg + (lane >> 4), a.nch))) = w;
+    const int items = a.T * a.parts;  // (the launcher keeps this within 2^21)
+    for (int it = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5); it < items; it += a.xblocks * 8) {
+        const int t = it / a.parts, s0 = (it - t * a.parts) * chunk, s1 = min(s0 + chunk, segs);
+        const char* row = reinterpret_cast<const char*>(a.x) + (size_t)t * a.ldx * esize;
+        for (int sg = s0; sg < s1; sg += kQuantAhead) {
+            float v[kQuantAhead][8];
+#pragma unroll
+            for (int u = 0; u < kQuantAhead; ++u) {
+                const int k = (sg + u) * kBK + lane * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+                if (sg + u < s1 && k < a.K) load8<F32, VEC>(row + (size_t)k * esize, v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kQuantAhead; ++u) {
+                const int seg = sg + u, k = seg * kBK + lane * 8;
+                if (seg >= s1) break;
+                uint32_t sb;
+                const uint32_t c = quantize8(v[u], sb);
+                if (k < a.K) *reinterpret_cast<uint32_t*>(a.codes + (size_t)t * (a.K / 2) + k / 2) = c;
+                // lanes 0 and 16: the four scale bytes of their 128 values
+                uint32_t w = sb;
+                w |= __shfl_down_sync(0xFFFFFFFFu, sb, 4) << 8;
+                w |= __shfl_down_sync(0xFFFFFFFFu, sb, 8) << 16;
+                w |= __shfl_down_sync(0xFFFFFFFFu, sb, 12) << 24;
+                if ((lane & 15) == 0)
+                    *reinterpret_cast<uint32_t*>(a.scales + (a.pitch ? (size_t)t * a.pitch + seg * 8 + (lane >> 4) * 4
+                                                                     : sf_block(t, seg, segs) + (lane >> 4) * 4)) = w;
+            }
+        }
     }
     pdl_end();
 }
@@ -173,6 +185,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
 // ----------------------------------------------------------------- product
 
 struct StreamArgs {
+    const void* x;           // FUSED: [T] rows, ldx elements apart
+    long long ldx;
+    int x_f32, x_vec;
     const uint8_t* scales;   // [N][K/32]
     const uint8_t* xscales;  // [T][xpitch]
     int xpitch;
@@ -264,7 +279,8 @@ struct StreamLayout {
     static constexpr int kFit = (110 * 1024) / kStage;
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kBar = kStages * kStage;
-    static constexpr int kTotal = kBar + 256 + 1024;  // + barriers, alignment slack
+    static constexpr int kXsf = kBar + 256;           // FUSED: a stage's scale bytes of 16 tokens, two stages
+    static constexpr int kTotal = kXsf + 256 + 1024;  // + barriers, alignment slack
     static_assert(kStages >= 3, "ring depth");
     static_assert(NT * kMRows * 4 <= kBar, "the partial tile takes the ring's place");
     static constexpr int kNJ = (NT + 31) / 32;        // scale columns of the tokens
@@ -277,7 +293,7 @@ struct StreamLayout {
     static_assert(kSfCol0 + kStages * kSfCols <= kCols, "tensor memory, half an SM's");
 };
 
-template <int NT>
+template <int NT, bool FUSED>
 __global__ void __launch_bounds__(kStreamThreads, 2)
     linear_stream_kernel(const StreamArgs a, const int splits,
                          const __grid_constant__ CUtensorMap w_map,
@@ -313,14 +329,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    bool done = false;  // this thread's warp saw the finished accumulator
+    // (FUSED: the kernel before this one may have written anything that is read here)
+    if (FUSED) pdl_begin();
 
     if (warp == 0) {
         // ------------------------------------------------------- producer
         if (lane == 0) {
             auto load_w = [&](int i) {
                 const int s = i % kStages;
-                mbar_arrive_expect_tx(&tma_full[s], (uint32_t)L::kStage);
+                mbar_arrive_expect_tx(&tma_full[s], (uint32_t)(FUSED ? kABytes : L::kStage));
                 tma_load_2d(smem_u32(smem + s * L::kStage), &w_map, (st0 + i) * kRowBytes, n0, &tma_full[s]);
             };
             auto load_x = [&](int i) {
@@ -330,13 +347,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             };
             const int n = st1 - st0, first = min(n, kStages);
             for (int i = 0; i < first; ++i) load_w(i);
-            pdl_begin();
-            for (int i = 0; i < first; ++i) load_x(i);
+            if (!FUSED) {
+                pdl_begin();
+                for (int i = 0; i < first; ++i) load_x(i);
+            }
             int i = first;
             for (; i < n; ++i) {
                 if (!mbar_wait(&stage_free[i % kStages], ((i / kStages) - 1) & 1)) break;
                 load_w(i);
-                load_x(i);
+                if (!FUSED) load_x(i);
             }
             // wait (bounded) until the last loads landed before the CTA can exit
             for (int d = 0; d < kStages && d < i; ++d) {
@@ -386,12 +405,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             return make_uint2(w[0], w[1]);
         };
         uint2 an = load_sa(st0);
-        pdl_begin();
+        if (!FUSED) pdl_begin();
         const uint8_t* sb[kNJ];
 #pragma unroll
         for (int j = 0; j < kNJ; ++j) {
             const int t = t0 + 32 * j + lane;
-            sb[j] = (32 * j + lane < NT && t < a.T) ? a.xscales + (size_t)t * a.xpitch : nullptr;
+            sb[j] = (!FUSED && 32 * j + lane < NT && t < a.T) ? a.xscales + (size_t)t * a.xpitch : nullptr;
         }
         uint2 bn[kNJ];
         auto load_sb = [&](int st) {
@@ -400,6 +419,23 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 bn[j] = sb[j] ? *reinterpret_cast<const uint2*>(sb[j] + 8 * st) : make_uint2(0, 0);
         };
         load_sb(st0);
+        // FUSED: this lane's eight values of tokens quad, quad + 4, ... of stage st
+        float xv[FUSED ? 4 : 1][8];
+        auto load_xv = [&](int st) {
+#pragma unroll
+            for (int u = 0; u < (FUSED ? 4 : 0); ++u) {
+                const int t = quad + 4 * u, k = st * kBK + 8 * lane;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) xv[u][i] = 0.0f;
+                if (t >= a.T || k >= a.K) continue;
+                const char* p = reinterpret_cast<const char*>(a.x) + ((size_t)t * a.ldx + k) * (a.x_f32 ? 4 : 2);
+                if (a.x_f32)
+                    a.x_vec ? load8<true, true>(p, xv[u]) : load8<true, false>(p, xv[u]);
+                else
+                    a.x_vec ? load8<false, true>(p, xv[u]) : load8<false, false>(p, xv[u]);
+            }
+        };
+        if (FUSED) load_xv(st0);
         bool ok = true;
         for (int i = 0; i < st1 - st0 && ok; ++i) {
             const int s = i % kStages;
@@ -411,7 +447,32 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 an = load_sa(st0 + i + 1);
                 load_sb(st0 + i + 1);
             }
-            if (i >= kStages && !mbar_wait_warp(&stage_free[s], ((i / kStages) - 1) & 1)) {
+            bool free = i < kStages || mbar_wait_warp(&stage_free[s], ((i / kStages) - 1) & 1);
+            if (FUSED) {
+                // encode into the stage's rows (128-byte swizzle); the four warps meet
+                // before the scale bytes are read back
+                if (free) {
+                    uint8_t* rows = smem + s * L::kStage + kABytes;
+                    uint8_t* xsf = smem + L::kXsf + (i & 1) * 128;
+#pragma unroll
+                    for (int u = 0; u < (FUSED ? 4 : 0); ++u) {
+                        const int t = quad + 4 * u;
+                        uint32_t sbyte;
+                        const uint32_t c = quantize8(xv[u], sbyte);
+                        *reinterpret_cast<uint32_t*>(rows + t * kRowBytes + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4) = c;
+                        if ((lane & 3) == 0) xsf[t * 8 + (lane >> 2)] = (uint8_t)sbyte;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                free = all_at_barrier(free, 1, 128);
+                if (free) {
+                    const uint2 v = lane < 16 ? *reinterpret_cast<const uint2*>(smem + L::kXsf + (i & 1) * 128 + lane * 8)
+                                              : make_uint2(0, 0);
+                    bv[0][0] = v.x, bv[1][0] = v.y;
+                    if (i + 1 < st1 - st0) load_xv(st0 + i + 1);
+                }
+            }
+            if (!free) {
                 ok = false;
                 break;
             }
@@ -427,8 +488,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sf_full[s]);
         }
-        done = ok && mbar_wait_warp(acc_full, 0);
-        if (done) {
+        if (ok && mbar_wait_warp(acc_full, 0)) {
             tc_fence_after();
             float* part = reinterpret_cast<float*>(smem);  // [NT][128], over the ring: its loads are used
             const int ncol = min(NT, a.T - t0);
@@ -489,24 +549,25 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 // Long prompts are bound by the tensor cores (and by what feeds them), so tokens are
 // the MMA's M side in pairs of CTAs (cta_group::2: 256 tokens x TN weight rows,
 // each CTA loading its 128 tokens and half of the weight rows), persistent, in
-// an order that keeps a weight tile on neighbouring pairs.  A stage (256 k) also brings
-// its scale bytes, already in tensor memory's layout (sf_block): the MMA thread copies
-// them there itself (tcgen05.cp, in order before the MMAs that read them), so no warp
-// handles scales.  Eight epilogue warps read the accumulator into registers,
+// an order that keeps a weight tile on neighbouring pairs (squarer groups of tiles
+// took the same time).  A stage (256 k) also brings
+// the scale bytes of its rows (sf_block), which four warps, one per tensor-memory lane
+// quadrant, write into tensor memory; letting the MMA thread copy them there
+// (tcgen05.cp, six copies a stage) held the products up by a third, also when issued a
+// stage ahead.  Eight epilogue warps read the accumulator into registers,
 // free it, and store through shared memory in full rows of 64 or 128 bytes.
 // TN = 256 halves what crosses L2 -> shared memory per product (the bound of
 // this shape: 8 KB a CTA per 256 x 256 x 64 MMA, 64 bytes a clock) but has room for one
 // accumulator only; TN = 128 has two, and twice the tiles.
 struct PairArgs {
-    const uint8_t* sfa;   // x's scale blocks, ceil(T / 256) * 2 of nch
-    const uint8_t* sfb;   // the weights', ceil(N / 256) * 2 of nch
-    int nch;
+    const uint8_t* sfa;   // x's scale bytes: ceil(T / 256) * 2 rows of blocks
+    const uint8_t* sfb;   // the weights': ceil(N / 256) * 2
     StreamArgs o;         // output, residual, sizes
     int vec;              // 16-byte stores (and residual loads)
 };
 
-constexpr int kPairThreads = 384;
-constexpr int kPairEpiWarp0 = 4;
+constexpr int kPairThreads = 448;
+constexpr int kPairEpiWarp0 = 6;  // after the producer, the MMA and the four scale warps (2..5)
 
 template <int TN>
 struct PairLayout {
@@ -532,18 +593,6 @@ struct PairLayout {
     static_assert(kSfCol0 + kStages * 32 <= 512, "tensor memory");
 };
 
-// 32 rows of 16 bytes (512 contiguous bytes) from shared memory to 4 columns of tensor
-// memory, the same in every lane quadrant, in both CTAs of the pair from their own
-// shared memory.  In order with this thread's MMAs.
-__device__ __forceinline__ void copy_sf_pair(uint32_t taddr, uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)1u << 16;             // leading byte offset (unused)
-    d |= (uint64_t)(128u >> 4) << 32;    // next 8 rows
-    d |= (uint64_t)1u << 46;             // descriptor version; no swizzle
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-}
-
 template <int TN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const PairArgs a, const __grid_constant__ CUtensorMap x_map,
@@ -553,8 +602,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* tma_full = reinterpret_cast<uint64_t*>(smem + L::kBar);  // this CTA's loads
-    uint64_t* peer_full = tma_full + kStages;   // even CTA: the odd one's loads
-    uint64_t* stage_free = peer_full + kStages;
+    uint64_t* sf_full = tma_full + kStages;     // even CTA: loads and scale factors of both
+    uint64_t* stage_free = sf_full + kStages;
     uint64_t* acc_full = stage_free + kStages;  // [2]
     uint64_t* acc_free = acc_full + 2;          // [2], even CTA: drained by both
     uint64_t* drain = acc_free + 2;
@@ -569,7 +618,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&tma_full[s], 1);
-            mbar_init(&peer_full[s], 1);
+            mbar_init(&sf_full[s], 8);
             mbar_init(&stage_free[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -594,8 +643,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int tile = pair; tile < tiles && ok; tile += pairs) {
                 const int nt = tile / mts, mt = tile - nt * mts;
                 const int arow = mt * 256 + rank * 128, brow = nt * TN + rank * L::kBRows;
-                const uint8_t* sfa = a.sfa + (size_t)(mt * 2 + rank) * a.nch * 512;
-                const uint8_t* sfb = a.sfb + (size_t)nt * (TN / 128) * a.nch * 512;
+                const uint8_t* sfa = a.sfa + (size_t)(mt * 2 + rank) * nk * 1024;
+                const uint8_t* sfb = a.sfb + (size_t)nt * (TN / 128) * nk * 1024;
                 for (int st = 0; st < nk; ++st, ++gs) {
                     const int s = gs % kStages;
                     if (gs >= (uint32_t)kStages && !mbar_wait(&stage_free[s], ((gs / kStages) - 1) & 1)) {
@@ -610,7 +659,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int j = 0; j < TN / 128; ++j)
                         bulk_copy_g2s(base + L::kSf + L::kSfaBytes + j * 1024,
-                                      sfb + ((size_t)j * a.nch + 2 * st) * 512, 1024, &tma_full[s]);
+                                      sfb + ((size_t)j * nk + st) * 1024, 1024, &tma_full[s]);
                 }
             }
             // wait (bounded) until the last loads landed before the CTA can exit
@@ -632,21 +681,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const uint32_t d_tmem = tmem + b * TN;
                 for (int st = 0; st < nk; ++st, ++gs) {
                     const int s = gs % kStages;
-                    const uint32_t par = (gs / kStages) & 1;
-                    if (!mbar_wait(&tma_full[s], par) || !mbar_wait(&peer_full[s], par)) {
+                    // (arrived at once the stage's loads and scale factors are there, by both CTAs)
+                    if (!mbar_wait(&sf_full[s], (gs / kStages) & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t base = smem_u32(smem + s * L::kStage);
                     const uint32_t sf = tmem + (uint32_t)(L::kSfCol0 + s * 32);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        copy_sf_pair(sf + 8u * c, base + L::kSf + c * 512);
-#pragma unroll
-                        for (int j = 0; j < TN / 128; ++j)
-                            copy_sf_pair(sf + 16u + 8u * c + 4u * j, base + L::kSf + L::kSfaBytes + j * 1024 + c * 512);
-                    }
                     const uint64_t ad = sdesc_sw128(base), bd = sdesc_sw128(base + kABytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)  // K = 64 each: +32 bytes in the swizzle atom
@@ -659,21 +701,51 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mma_commit_pair(drain);  // every MMA issued has completed when this arrives
             mbar_wait(drain, 0);
         } else if (lane == 0) {
-            // the odd CTA: tell the even one when this CTA's stages have landed
-            uint32_t gs = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs)
-                for (int st = 0; st < nk; ++st, ++gs) {
-                    const int s = gs % kStages;
-                    if (!mbar_wait(&tma_full[s], (gs / kStages) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_remote(&peer_full[s], 0);
-                }
-            mbar_wait(drain, 0);  // the pair's MMAs and their commits to this CTA are done
+            mbar_wait(drain, 0);  // odd CTA: the pair's MMAs and their commits to it are done
         }
-    } else if (warp >= kPairEpiWarp0) {
+    } else if (warp < kPairEpiWarp0) {
+        // -------------------------------------------------- scale factors
+        // token r's at lane r, column base + r / 32; weight row n's at lane 32 q + n % 32,
+        // column base + n / 32, in every quadrant q
+        constexpr int NJ = TN / 32;
+        const int quad = warp & 3;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)L::kSfCol0;
+        uint32_t gs = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            for (int st = 0; st < nk; ++st, ++gs) {
+                const int s = gs % kStages;
+                // the stage is filled again only after the MMAs that read these columns
+                if (!mbar_wait_warp(&tma_full[s], (gs / kStages) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sf = smem_u32(smem + s * L::kStage + L::kSf) + 8 * lane;
+                const uint2 av = lds64(sf + 256 * quad);
+                uint32_t b0[NJ], b1[NJ];
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const uint2 v = lds64(sf + L::kSfaBytes + 256 * j);
+                    b0[j] = v.x, b1[j] = v.y;
+                }
+                tc_fence_after();
+                const uint32_t col = lane_base + (uint32_t)(s * 32);
+                tmem_st_cols<1>(col + (uint32_t)quad, &av.x);
+                tmem_st_cols<1>(col + 8u + (uint32_t)quad, &av.y);
+                tmem_st_cols<NJ>(col + 16u, b0);
+                tmem_st_cols<NJ>(col + 24u, b1);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0)
+                        mbar_arrive(&sf_full[s]);
+                    else
+                        mbar_arrive_remote(&sf_full[s], 0);
+                }
+            }
+        }
+    } else {
         // -------------------------------------------------------- epilogue
         constexpr int kCols = TN / 2;  // columns per warp
         const int quad = warp & 3, half = (warp - kPairEpiWarp0) >> 2;
@@ -725,7 +797,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 template <int TN>
-cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* sfa, const uint8_t* sfb, int nch,
+cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* sfa, const uint8_t* sfb,
                         cudaStream_t s) {
     const size_t smem = PairLayout<TN>::kTotal;
     cudaError_t err = ensure_dynamic_smem((const void*)linear_pair_kernel<TN>, smem);
@@ -742,7 +814,6 @@ cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8
     PairArgs a;
     a.sfa = sfa;
     a.sfb = sfb;
-    a.nch = nch;
     a.o = stream_args(p);
     const size_t es = p.out_f32 ? 4 : 2;
     a.vec = (uintptr_t)p.out % 16 == 0 && p.ldo * es % 16 == 0 &&
@@ -752,35 +823,52 @@ cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8
     return launch_pdl_cluster(linear_pair_kernel<TN>, dim3((unsigned)grid), dim3(kPairThreads), smem, s, 2u, a, x_map, w_map);
 }
 
-template <int NT>
+int row_tiles(int N) { return (N + kMRows - 1) / kMRows; }
+
+// Split K while the CTAs do not fill two per SM and every split has a stage.
+int stream_splits(const LinearMxfp4& p, int NT) {
+    const long long tiles = (long long)row_tiles(p.N) * ((p.T + NT - 1) / NT);
+    const int nk = (p.K + kBK - 1) / kBK;
+    int splits = 1;
+    while (splits < 8 && 2 * splits <= nk && tiles * 2 * splits <= 2LL * num_sms()) splits *= 2;
+    return splits;
+}
+
+template <int NT, bool FUSED>
 cudaError_t launch_stream(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* xscales, int xpitch,
                           cudaStream_t s) {
     const size_t smem = StreamLayout<NT>::kTotal;
-    cudaError_t err = ensure_dynamic_smem((const void*)linear_stream_kernel<NT>, smem);
+    cudaError_t err = ensure_dynamic_smem((const void*)linear_stream_kernel<NT, FUSED>, smem);
     if (err != cudaSuccess) return err;
     CUtensorMap w_map, x_map;
     err = encode_codes_map(&w_map, p.codes, p.K / 2, (uint64_t)p.N, kRowBytes, kMRows);
     if (err != cudaSuccess) return err;
-    err = encode_codes_map(&x_map, xcodes, p.K / 2, (uint64_t)p.T, kRowBytes, NT);
-    if (err != cudaSuccess) return err;
+    if (FUSED) {
+        x_map = w_map;  // not read
+    } else {
+        err = encode_codes_map(&x_map, xcodes, p.K / 2, (uint64_t)p.T, kRowBytes, NT);
+        if (err != cudaSuccess) return err;
+    }
     StreamArgs a = stream_args(p);
     a.xscales = xscales;
     a.xpitch = xpitch;
-    const int row_tiles = (p.N + kMRows - 1) / kMRows, tok_tiles = (p.T + NT - 1) / NT;
-    const int nk = (p.K + kBK - 1) / kBK;
-    // split K while the CTAs do not fill two per SM and every split has a stage
-    int splits = 1;
-    while (splits < 8 && 2 * splits <= nk && (long long)row_tiles * tok_tiles * 2 * splits <= 2LL * num_sms())
-        splits *= 2;
-    return launch_pdl_cluster(linear_stream_kernel<NT>, dim3((unsigned)row_tiles * splits, (unsigned)tok_tiles),
+    a.x = p.x;
+    a.ldx = p.ldx;
+    a.x_f32 = p.x_f32;
+    a.x_vec = (uintptr_t)p.x % 16 == 0 && p.ldx * (p.x_f32 ? 4 : 2) % 16 == 0;
+    const int tok_tiles = (p.T + NT - 1) / NT, splits = stream_splits(p, NT);
+    return launch_pdl_cluster(linear_stream_kernel<NT, FUSED>, dim3((unsigned)row_tiles(p.N) * splits, (unsigned)tok_tiles),
                               dim3(kStreamThreads), smem, s, (unsigned)splits, a, splits, w_map, x_map);
 }
 
 template <bool F32>
 cudaError_t launch_quantize_rows(QuantArgs a, cudaStream_t s) {
-    const long long items = (long long)a.T * ((a.K + kBK - 1) / kBK);
-    a.xblocks = (int)std::min<long long>((items + 7) / 8, (long long)num_sms() * 8);
-    const int wblocks = a.nch ? (int)std::min<long long>(((long long)a.N * ((a.nch + 3) / 4) + 255) / 256, (long long)num_sms() * 4) : 0;
+    // a warp per row where the rows fill the GPU, else rows split into 256-value parts
+    const int warps = num_sms() * 4 * 8, segs = (a.K + kBK - 1) / kBK;
+    a.parts = std::max(1, std::min(segs, warps / std::max(a.T, 1)));
+    a.xblocks = (int)std::min<long long>(((long long)a.T * a.parts + 7) / 8, (long long)num_sms() * 4);
+    const long long witems = (long long)a.N * (((a.K + kBK - 1) / kBK + 1) / 2);
+    const int wblocks = a.wsb ? (int)std::min<long long>((witems + 255) / 256, (long long)num_sms()) : 0;
     // 16-byte loads where every row starts on a 16-byte boundary
     const bool vec = ((uintptr_t)a.x % 16) == 0 && (a.ldx * (F32 ? 4 : 2)) % 16 == 0;
     return launch_pdl(vec ? quantize_rows_kernel<F32, true> : quantize_rows_kernel<F32, false>, dim3(a.xblocks + wblocks),
@@ -805,6 +893,9 @@ size_t linear_mxfp4_workspace(int T, int N, int K) {
 }
 
 cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStream_t s) {
+    // few tokens and one wave of CTAs: they encode x themselves
+    if (p.T <= 16 && (long long)row_tiles(p.N) * stream_splits(p, 16) <= 2LL * num_sms())
+        return launch_stream<16, true>(p, nullptr, nullptr, 0, s);
     QuantArgs q = {};
     q.x = p.x;
     q.ldx = p.ldx;
@@ -814,7 +905,6 @@ cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStrea
     q.scales = q.codes + align256((size_t)p.T * (p.K / 2));
     const bool pairs = use_pairs(p.T, p.N);
     if (pairs) {
-        q.nch = (p.K + kBK - 1) / kBK * 2;
         q.ws = p.scales;
         q.wsb = q.scales + sf_bytes(p.T, p.K);
         q.N = p.N;
@@ -823,12 +913,12 @@ cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStrea
     }
     cudaError_t err = p.x_f32 ? launch_quantize_rows<true>(q, s) : launch_quantize_rows<false>(q, s);
     if (err != cudaSuccess) return err;
-    if (pairs) return launch_pair<256>(p, q.codes, q.scales, q.wsb, q.nch, s);
+    if (pairs) return launch_pair<256>(p, q.codes, q.scales, q.wsb, s);
     // the narrowest token tile that holds the batch
-    if (p.T <= 16) return launch_stream<16>(p, q.codes, q.scales, q.pitch, s);
-    if (p.T <= 32) return launch_stream<32>(p, q.codes, q.scales, q.pitch, s);
-    if (p.T <= 64) return launch_stream<64>(p, q.codes, q.scales, q.pitch, s);
-    return launch_stream<128>(p, q.codes, q.scales, q.pitch, s);
+    if (p.T <= 16) return launch_stream<16, false>(p, q.codes, q.scales, q.pitch, s);
+    if (p.T <= 32) return launch_stream<32, false>(p, q.codes, q.scales, q.pitch, s);
+    if (p.T <= 64) return launch_stream<64, false>(p, q.codes, q.scales, q.pitch, s);
+    return launch_stream<128, false>(p, q.codes, q.scales, q.pitch, s);
 }
 
 cudaError_t read_device_error_linear(int* flag, int clear) {

@@ -601,30 +601,39 @@ def moe_layer_few(x, w_router, w13, s13, w2, s2, K: int, with_shared: bool = Tru
     sigmoid(w_shared_gate . x).  workspace: from alloc_workspace_few (include/moe.h)."""
     import torch
     T, H = x.shape
-    E, I = w_router.shape[0], w13.shape[1] // 2
-    Kt, Et = K + (1 if with_shared else 0), E + (1 if with_shared else 0)
+    E = w_router.shape[0]
+    Et, twoI, _ = w13.shape
+    I, shared = twoI // 2, 1 if with_shared else 0
+    bf16, u8 = torch.bfloat16, torch.uint8
+    if Et != E + shared or w2.shape != (Et, H, I // 2) or w13.shape[2] != H // 2:
+        raise ValueError("weights must hold E experts plus the shared one when with_shared")
+    assert x.dtype == bf16 and w_router.dtype == bf16 and w_router.shape[1] == H, "x and w_router are bfloat16"
+    assert w13.dtype == s13.dtype == w2.dtype == s2.dtype == u8, "weights are uint8"
+    assert s13.shape == (Et, twoI, H // 32) and s2.shape == (Et, H, I // 32), "scales do not match the weights"
     for t in (x, w_router, w13, s13, w2, s2):
         _dev(t, "layer input")
-    bf16 = torch.bfloat16
-    assert x.dtype == bf16 and w_router.dtype == bf16 and w_router.shape[1] == H
-    if w13.shape != (Et, 2 * I, H // 2) or w2.shape != (Et, H, I // 2):
-        raise ValueError("weights must hold E experts plus the shared one when with_shared")
-    assert s13.shape == (Et, 2 * I, H // 32) and s2.shape == (Et, H, I // 32)
     if w_shared_gate is not None:
         _dev(w_shared_gate, "w_shared_gate")
         assert w_shared_gate.dtype == bf16 and w_shared_gate.shape == (H,)
     if out is None:
-        out = torch.empty((T, H), dtype=bf16, device=x.device)
+        out = torch.empty_like(x)
+    elif not (out.is_cuda and out.is_contiguous() and out.dtype == bf16 and out.shape == x.shape):
+        raise ValueError("out must be a contiguous CUDA bfloat16 tensor like x")
     if topk_ids is None:
-        topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=x.device)
+        topk_ids = torch.empty((T, K + shared), dtype=torch.int32, device=x.device)
     if topk_w is None:
-        topk_w = torch.empty((T, Kt), dtype=torch.float32, device=x.device)
+        topk_w = torch.empty((T, K + shared), dtype=torch.float32, device=x.device)
     if workspace is None:
         workspace = alloc_workspace_few(T, H, I, E, K, with_shared, x.device)
-    _check(load().moe_layer_few(_ptr(x), _ptr(w_router), _ptr(w_shared_gate), _ptr(w13), _ptr(s13),
-                                _ptr(w2), _ptr(s2), T, H, I, E, K, int(with_shared), int(renormalize),
-                                _ptr(out), _ptr(topk_ids), _ptr(topk_w), _ptr(workspace),
-                                workspace.numel(), _stream(stream)), "moe_layer_few")
+    for t, dt in ((topk_ids, torch.int32), (topk_w, torch.float32)):
+        assert t.is_cuda and t.is_contiguous() and t.dtype == dt and t.numel() == T * (K + shared)
+    status = (_lib or load()).moe_layer_few(
+        x.data_ptr(), w_router.data_ptr(), None if w_shared_gate is None else w_shared_gate.data_ptr(),
+        w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), T, H, I, E, K, shared,
+        1 if renormalize else 0, out.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _raw_stream(stream, x))
+    if status:
+        raise MoeError(status, "moe_layer_few")
     return out, topk_ids, topk_w
 
 
@@ -640,15 +649,21 @@ def alloc_workspace_linear(T: int, N: int, K: int, device="cuda"):
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
-def _rows(t, what: str):
-    """(element type, row stride) of a 2D CUDA tensor whose rows are contiguous."""
+def _raw_stream(stream, t):
+    """The handle of `stream`, or of the current stream of t's device (without the Stream object
+    that torch.cuda.current_stream makes: 3 us of a call that takes 10)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    types = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
-    assert t.is_cuda and t.dim() == 2, f"{what} must be a 2D CUDA tensor"
-    assert t.dtype in types, f"{what} must be bfloat16 or float32"
-    assert t.shape[1] <= 1 or t.stride(1) == 1, f"{what}'s rows must be contiguous"
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _row_stride(t, rows: int, width: int, what: str) -> int:
+    """The row stride of a 2D CUDA tensor whose rows are contiguous."""
+    ld, inner = t.stride()
+    assert t.is_cuda and (inner == 1 or width <= 1), f"{what} must be a CUDA tensor with contiguous rows"
     # a single row has no neighbour: its stride means nothing
-    return types[t.dtype], max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    return ld if rows > 1 else width
 
 
 def moe_linear_mxfp4act(x, codes, scales, residual=None, out=None, out_dtype=None, workspace=None,
@@ -657,23 +672,35 @@ def moe_linear_mxfp4act(x, codes, scales, residual=None, out=None, out_dtype=Non
     to MXFP4 inside the call, plus residual [T, N] (include/moe.h).  x, residual and out may be
     row slices of wider tensors; out_dtype: torch.bfloat16 (default) or torch.float32."""
     import torch
+    f32, bf16 = torch.float32, torch.bfloat16
     T, K = x.shape
     N = codes.shape[0]
     _dev(codes, "codes")
     _dev(scales, "scales")
     assert codes.shape == (N, K // 2) and scales.shape == (N, K // 32), "weights do not match x"
+    assert codes.dtype == torch.uint8 and scales.dtype == torch.uint8, "weights are uint8"
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
-    assert out.shape == (T, N) and out_dtype in (None, out.dtype)
-    x_type, ldx = _rows(x, "x")
-    out_type, ldo = _rows(out, "out")
-    ldr = 0
+        out_dtype = out_dtype or bf16
+        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+        ldo = N
+    else:
+        assert out.shape == (T, N) and out_dtype in (None, out.dtype), "out must be [T, N]"
+        out_dtype = out.dtype
+        ldo = _row_stride(out, T, N, "out")
+    xt = x.dtype
+    assert (xt == bf16 or xt == f32) and (out_dtype == bf16 or out_dtype == f32), \
+        "x and out must be bfloat16 or float32"
+    res, ldr = None, 0
     if residual is not None:
-        assert residual.shape == (T, N) and residual.dtype == out.dtype, "residual must match out"
-        _, ldr = _rows(residual, "residual")
+        assert residual.shape == (T, N) and residual.dtype == out_dtype, "residual must match out"
+        res, ldr = residual.data_ptr(), _row_stride(residual, T, N, "residual")
     if workspace is None:
         workspace = alloc_workspace_linear(T, N, K, x.device)
-    _check(load().moe_linear_mxfp4act(_ptr(x), x_type, ldx, _ptr(codes), _ptr(scales), _ptr(residual), ldr,
-                                      _ptr(out), out_type, ldo, T, N, K, _ptr(workspace),
-                                      workspace.numel(), _stream(stream)), "moe_linear_mxfp4act")
+    status = (_lib or load()).moe_linear_mxfp4act(
+        x.data_ptr(), MOE_DTYPE_F32 if xt == f32 else MOE_DTYPE_BF16, _row_stride(x, T, K, "x"),
+        codes.data_ptr(), scales.data_ptr(), res, ldr, out.data_ptr(),
+        MOE_DTYPE_F32 if out_dtype == f32 else MOE_DTYPE_BF16, ldo, T, N, K, workspace.data_ptr(),
+        workspace.numel(), _raw_stream(stream, x))
+    if status:
+        raise MoeError(status, "moe_linear_mxfp4act")
     return out
