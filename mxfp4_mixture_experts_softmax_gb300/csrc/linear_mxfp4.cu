@@ -48,7 +48,7 @@ constexpr int kABytes = kMRows * kRowBytes;
 // Eight values of a row from `p`: one or two 16-byte loads, or element by
 // element where the row's start is not 16-byte aligned.
 template <bool F32, bool VEC>
-__device__ __forceinline__ void load8(const void* p, float v[8]) {
+__device__ __forceinline__ void load8(const void* p, float* v) {
     if (F32) {
         const float* f = reinterpret_cast<const float*>(p);
         if (VEC) {
@@ -271,12 +271,14 @@ StreamArgs stream_args(const LinearMxfp4& p) {
 
 constexpr int kStreamThreads = 192;
 
-template <int NT>
+template <int NT, bool FUSED>
 struct StreamLayout {
     static constexpr int kBBytes = NT * kRowBytes;
     static constexpr int kStage = kABytes + kBBytes;  // a multiple of 1024
-    // two CTAs per SM: at most 110 KB each
-    static constexpr int kFit = (110 * 1024) / kStage;
+    // CTAs per SM: four short ones for the fewest tokens, whose CTAs only pass weights on
+    // (16 x 100003 x 4096: 42 us against 46 with two)
+    static constexpr int kPerSm = NT == 16 && !FUSED ? 4 : 2;
+    static constexpr int kFit = (kPerSm == 4 ? 54 : 110) * 1024 / kStage;
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kBar = kStages * kStage;
     static constexpr int kXsf = kBar + 256;           // FUSED: a stage's scale bytes of 16 tokens, two stages
@@ -289,16 +291,16 @@ struct StreamLayout {
     // +0 and +8, tokens at +16 and +24)
     static constexpr int kSfCols = 32;
     static constexpr int kSfCol0 = NT < 32 ? 32 : NT;
-    static constexpr int kCols = 256;
-    static_assert(kSfCol0 + kStages * kSfCols <= kCols, "tensor memory, half an SM's");
+    static constexpr int kCols = 512 / kPerSm;
+    static_assert(kSfCol0 + kStages * kSfCols <= kCols, "tensor memory, a CTA's share");
 };
 
 template <int NT, bool FUSED>
-__global__ void __launch_bounds__(kStreamThreads, 2)
+__global__ void __launch_bounds__(kStreamThreads, (StreamLayout<NT, FUSED>::kPerSm))
     linear_stream_kernel(const StreamArgs a, const int splits,
                          const __grid_constant__ CUtensorMap w_map,
                          const __grid_constant__ CUtensorMap x_map) {
-    using L = StreamLayout<NT>;
+    using L = StreamLayout<NT, FUSED>;
     constexpr int kStages = L::kStages, kNJ = L::kNJ;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -419,20 +421,29 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
                 bn[j] = sb[j] ? *reinterpret_cast<const uint2*>(sb[j] + 8 * st) : make_uint2(0, 0);
         };
         load_sb(st0);
-        // FUSED: this lane's eight values of tokens quad, quad + 4, ... of stage st
+        // FUSED: this lane's eight values of tokens quad, quad + 4, ... of stage st, the
+        // four loads together
         float xv[FUSED ? 4 : 1][8];
         auto load_xv = [&](int st) {
+            const int k = st * kBK + 8 * lane, esize = a.x_f32 ? 4 : 2;
+            auto each = [&](auto load) {
 #pragma unroll
-            for (int u = 0; u < (FUSED ? 4 : 0); ++u) {
-                const int t = quad + 4 * u, k = st * kBK + 8 * lane;
+                for (int u = 0; u < (FUSED ? 4 : 0); ++u) {
+                    const int t = quad + 4 * u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xv[u][i] = 0.0f;
-                if (t >= a.T || k >= a.K) continue;
-                const char* p = reinterpret_cast<const char*>(a.x) + ((size_t)t * a.ldx + k) * (a.x_f32 ? 4 : 2);
-                if (a.x_f32)
-                    a.x_vec ? load8<true, true>(p, xv[u]) : load8<true, false>(p, xv[u]);
+                    for (int i = 0; i < 8; ++i) xv[u][i] = 0.0f;
+                    if (t < a.T && k < a.K) load(reinterpret_cast<const char*>(a.x) + ((size_t)t * a.ldx + k) * esize, xv[u]);
+                }
+            };
+            if (a.x_f32) {
+                if (a.x_vec)
+                    each([](const void* p, float* v) { load8<true, true>(p, v); });
                 else
-                    a.x_vec ? load8<false, true>(p, xv[u]) : load8<false, false>(p, xv[u]);
+                    each([](const void* p, float* v) { load8<true, false>(p, v); });
+            } else if (a.x_vec) {
+                each([](const void* p, float* v) { load8<false, true>(p, v); });
+            } else {
+                each([](const void* p, float* v) { load8<false, false>(p, v); });
             }
         };
         if (FUSED) load_xv(st0);
@@ -837,7 +848,7 @@ int stream_splits(const LinearMxfp4& p, int NT) {
 template <int NT, bool FUSED>
 cudaError_t launch_stream(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* xscales, int xpitch,
                           cudaStream_t s) {
-    const size_t smem = StreamLayout<NT>::kTotal;
+    const size_t smem = StreamLayout<NT, FUSED>::kTotal;
     cudaError_t err = ensure_dynamic_smem((const void*)linear_stream_kernel<NT, FUSED>, smem);
     if (err != cudaSuccess) return err;
     CUtensorMap w_map, x_map;
@@ -882,8 +893,13 @@ int xscale_pitch(int K) { return (K + kBK - 1) / kBK * 8; }
 // bytes of `rows` rows' scale blocks, whole tiles of 256 rows
 size_t sf_bytes(int rows, int K) { return (size_t)((rows + 255) / 256) * 2 * (size_t)((K + kBK - 1) / kBK) * 1024; }
 
+// Most stages of a CTA that encodes x itself: a stage's encoding takes about 1 us, which only
+// the first loads hide (16 x 4096 x 4096, 2 stages: 8.4 us against 9.1 in two launches; 16 x
+// 8192 x 4096, 4 stages: 12.8 against 10.6; 16 x 32000 x 4096, 16 stages: 39 against 17).
+constexpr int kFusedStages = 2;
+
 // Batches from here on go to the CTA pairs.
-bool use_pairs(int T, int N) { return T >= 256 && N >= 128; }
+bool use_pairs(int T, int N) { return T > 64 && N >= 128; }
 
 }  // namespace
 
@@ -893,9 +909,12 @@ size_t linear_mxfp4_workspace(int T, int N, int K) {
 }
 
 cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStream_t s) {
-    // few tokens and one wave of CTAs: they encode x themselves
-    if (p.T <= 16 && (long long)row_tiles(p.N) * stream_splits(p, 16) <= 2LL * num_sms())
-        return launch_stream<16, true>(p, nullptr, nullptr, 0, s);
+    // few tokens, one wave of CTAs and a few stages each: they encode x themselves
+    if (p.T <= 16) {
+        const int splits = stream_splits(p, 16), nk = (p.K + kBK - 1) / kBK;
+        if ((long long)row_tiles(p.N) * splits <= 2LL * num_sms() && (nk + splits - 1) / splits <= kFusedStages)
+            return launch_stream<16, true>(p, nullptr, nullptr, 0, s);
+    }
     QuantArgs q = {};
     q.x = p.x;
     q.ldx = p.ldx;
@@ -913,7 +932,15 @@ cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStrea
     }
     cudaError_t err = p.x_f32 ? launch_quantize_rows<true>(q, s) : launch_quantize_rows<false>(q, s);
     if (err != cudaSuccess) return err;
-    if (pairs) return launch_pair<256>(p, q.codes, q.scales, q.wsb, s);
+    if (pairs) {
+        // half-width tiles where the full ones would leave pairs idle: they take 0.6 of the time
+        // (512 x 4096 x 4096, 32 or 64 tiles: 16.8 and 13.7 us; 1024 x 16384 x 4096, 256 or
+        // 512 tiles: 37.7 and 42.7)
+        const long long mts = (p.T + 255) / 256, most = num_sms() / 2;
+        const long long w256 = (mts * ((p.N + 255) / 256) + most - 1) / most, w128 = (mts * ((p.N + 127) / 128) + most - 1) / most;
+        return 3 * w128 < 5 * w256 ? launch_pair<128>(p, q.codes, q.scales, q.wsb, s)
+                                   : launch_pair<256>(p, q.codes, q.scales, q.wsb, s);
+    }
     // the narrowest token tile that holds the batch
     if (p.T <= 16) return launch_stream<16, false>(p, q.codes, q.scales, q.pitch, s);
     if (p.T <= 32) return launch_stream<32, false>(p, q.codes, q.scales, q.pitch, s);
