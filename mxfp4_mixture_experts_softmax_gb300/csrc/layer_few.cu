@@ -35,16 +35,15 @@
 //            order, times routing weight.
 // What a warp does for a stage beside its products (waits, arrivals, handing its sums
 // over) takes longer than one slot's products, so the consumers take the stages two
-// at a time, and one warp turns the scale bytes into fp32 factors for all of them
-// (each of the four lanes that share a row would otherwise do it again: 130 of the
-// 330 cycles that 16 warps take per slot and scheduler).
+// at a time.  A warp turns its slot's scale bytes into fp32 factors once, through shared
+// memory (each of the four lanes that share a row would otherwise do it again: 130
+// of the 330 cycles that 16 warps take per slot and scheduler).
 // h passes between the phases as f16 with a power of two per 8 values (11
 // significant bits); the down product brings a pair's row to one power of two
 // (elements below 2^-14 of the row's largest keep fewer bits, those below 2^-25 of
 // it are dropped).  No result depends on timing.
-// Warps: 16 consumers, one producer (TMA), one for the scale factors, two epilogue
-// warps, one per stage of a pair (adding the consumers' partial sums over k, SwiGLU,
-// stores).  Every wait
+// Warps: 16 consumers, one producer (TMA), two epilogue warps, one per stage of a pair
+// (adding the consumers' partial sums over k, SwiGLU, stores).  Every wait
 // is bounded (mbar_wait, grid_wait).
 #include <string.h>
 
@@ -60,15 +59,12 @@ namespace {
 constexpr int kConsumerWarps = 16;
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kProducerWarp = kConsumerWarps;
-constexpr int kScaleWarp = kConsumerWarps + 1;
-constexpr int kEpiWarp0 = kConsumerWarps + 2;
-constexpr int kThreads = kConsumers + 4 * 32;
+constexpr int kEpiWarp0 = kConsumerWarps + 1;
+constexpr int kThreads = kConsumers + 3 * 32;
 constexpr int kSlotBytes = 16 * 128;
-constexpr int kCodeBytes = kConsumerWarps * kSlotBytes;    // a stage's codes,
-constexpr int kScaleBytes = kConsumerWarps * 16 * 8;       // its scale bytes
-constexpr int kFactorRow = kConsumerWarps * 32 + 16;       // and the factors made of them: 8 floats a slot,
-constexpr int kFactorBytes = 16 * kFactorRow;              // rows 4 banks apart
-constexpr int kStageBytes = (kCodeBytes + kScaleBytes + kFactorBytes + 1023) / 1024 * 1024;
+constexpr int kCodeBytes = kConsumerWarps * kSlotBytes;    // a stage's codes
+constexpr int kScaleBytes = kConsumerWarps * 16 * 8;       // and scale bytes
+constexpr int kStageBytes = kCodeBytes + kScaleBytes;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxPairs = 528;  // (token, slot) pairs: 16 * 33; also the most list entries
 constexpr int kMaxGrid = 256;
@@ -90,6 +86,10 @@ struct FewArgs {
     float* y;                // [T * Kt][H] expert outputs by pair
     int T, H, I, E, K, shared, renorm;
     int router_rows;         // rows of [Wr; gate] per CTA, at most 16
+    int router_k;            // k of them and of x that fit shared memory at once
+    // units of a stage, items of a stage; division by I / 8, H / 16 and E (div_by)
+    int ups, ips;
+    uint32_t upe_m, ru_m, e_m;
 };
 
 // The weights as the TMA reads them: whole 256-k slices (w13 [slice][gate, up][row],
@@ -101,22 +101,24 @@ struct FewMaps {
 
 // shared memory
 constexpr int kPartBytes = 2 * kConsumerWarps * 32 * 16;  // one buffer: the sums of a pair of stages
+constexpr int kFactorBytes = 2 * kConsumerWarps * 16 * 32;  // a slot's 16 x 8 factors per warp, two stages
 constexpr int kListBytes = kMaxPairs * (2 + 2 + 2 + 4 + 1) + 64 + 32;
 constexpr int kBarBytes = 192;
-constexpr int kStages = (kSmemLimit - 1024 - kBarBytes - kListBytes - 2 * kPartBytes) / kStageBytes;
+constexpr int kStages = (kSmemLimit - 1024 - kBarBytes - kListBytes - 2 * kPartBytes - kFactorBytes) / kStageBytes;
 static_assert(kStages >= 4, "ring depth");
 constexpr int kPart = kStages * kStageBytes;
-constexpr int kList = kPart + 2 * kPartBytes;
+constexpr int kFactors = kPart + 2 * kPartBytes;
+constexpr int kList = kFactors + kFactorBytes;
 constexpr int kBar = (kList + kListBytes + 7) / 8 * 8;
 constexpr int kSmemBytes = kBar + kBarBytes + 1024;  // + alignment slack
 static_assert(kSmemBytes <= kSmemLimit, "shared memory");
-static_assert((3 * kStages + 5) * 8 <= kBarBytes, "barriers");
+static_assert((2 * kStages + 6) * 8 <= kBarBytes, "barriers");
 // scratch of the routing phase: over the partial sums, and the logits over the last stages
 constexpr int kMask = kPart;                 // [1025] token masks by expert
 constexpr int kFirst = kMask + 1028 * 4;     // [1025] first pair by expert (16 bits)
 constexpr int kIds = kFirst + 1028 * 2;      // [16][33]
 constexpr int kSums = kIds + 16 * 33 * 4;    // [16][2]
-static_assert(kSums + 16 * 2 * 4 <= kList, "routing scratch");
+static_assert(kSums + 16 * 2 * 4 <= kFactors, "routing scratch");
 constexpr int kLogitStages = 2;              // 64 KB: 16 tokens x 1024 experts
 constexpr int kEarlyStages = kStages - kLogitStages;  // loads before the routing is known
 
@@ -155,7 +157,7 @@ __device__ __forceinline__ void consumers_sync() {
 }
 
 // v / d for v < 2^20 and d < 2^12, m = div_magic(d)
-__device__ __forceinline__ uint32_t div_magic(uint32_t d) { return d > 1 ? 0xFFFFFFFFu / d + 1u : 0u; }
+__host__ __device__ __forceinline__ uint32_t div_magic(uint32_t d) { return d > 1 ? 0xFFFFFFFFu / d + 1u : 0u; }
 __device__ __forceinline__ uint32_t div_by(uint32_t v, uint32_t m) { return m ? __umulhi(v, m) : v; }
 
 // Eight codes (two per byte, the even k in the low nibble) -> four f16x2.
@@ -198,9 +200,15 @@ __device__ __forceinline__ void mma_bf16_32(float d[4], uint4 wa, uint4 wb, uint
           "r"(x.y), "r"(x.z), "r"(x.w), "f"(0.0f));
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
 
@@ -216,12 +224,13 @@ __device__ __forceinline__ void sts_f4(uint32_t addr, float4 v) {
 
 // acc += one slot (16 rows x 256 k) times the token fragment b: per 32-k scale
 // group two MMAs into a fresh partial sum, added times the group's factor.  lm:
-// this lane's four ldmatrix offsets within a slot; fr: the factors of its row r.
+// this lane's four ldmatrix offsets within a slot; fr: the factors of its row r (8
+// floats; row r + 8 lies 256 bytes on).
 __device__ __forceinline__ void slot_mma(uint32_t slot, const uint32_t lm[4], uint32_t fr, const uint4 (&b)[8],
                                          float (&acc)[4]) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const float4 fa = lds_f4(fr + 16 * half), fb = lds_f4(fr + 8 * kFactorRow + 16 * half);
+        const float4 fa = lds_f4(fr + 16 * half), fb = lds_f4(fr + 256 + 16 * half);
         const float f0[4] = {fa.x, fa.y, fa.z, fa.w}, f1[4] = {fb.x, fb.y, fb.z, fb.w};
         uint32_t w[2][4];
         ldmatrix_x4(slot + lm[2 * half], w[0]);
@@ -243,18 +252,73 @@ __device__ __forceinline__ void slot_mma(uint32_t slot, const uint32_t lm[4], ui
     }
 }
 
-// Eight bytes from byte `at` of a matrix of `words` 32-bit words on, of which the
-// first n count (zeros for the others): three aligned words and a shift, whatever
-// the row's alignment, and no word past the matrix.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* base, size_t at, int n, size_t words) {
+// Four bytes from byte `at` of a matrix of `words` 32-bit words on, of which the
+// first n count (zeros for the others): two aligned words and a shift, whatever the
+// row's alignment, and no word past the matrix.
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* base, size_t at, int n, size_t words) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(base);
     const size_t w = at >> 2;
-    const uint32_t sh = (uint32_t)(at & 3) * 8u;
-    const uint32_t w0 = __ldg(p + w), w1 = __ldg(p + min(w + 1, words - 1)), w2 = __ldg(p + min(w + 2, words - 1));
-    uint2 v = make_uint2(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh));
-    if (n < 8) v.y = n > 4 ? v.y & ((1u << (8 * (n - 4))) - 1u) : 0u;
-    if (n < 4) v.x &= (1u << (8 * n)) - 1u;
-    return v;
+    const uint32_t v = __funnelshift_r(__ldg(p + w), __ldg(p + min(w + 1, words - 1)), (uint32_t)(at & 3) * 8u);
+    return n >= 4 ? v : (n > 0 ? v & ((1u << (8 * n)) - 1u) : 0u);
+}
+
+// Softmax top-K routing of one token by one warp, as route_loaded does it (the same
+// rounds, the same results), written for a warp that has its scheduler to itself: what
+// counts is the length of a round's chain of dependent steps.
+template <int VPL>
+__device__ __forceinline__ void route_few(const float* l, int E, int K, int with_shared, int renormalize,
+                                          float shared_weight, int32_t* ids, float* w, int lane) {
+    uint32_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = lane + 32 * i < E ? order_key(l[lane + 32 * i]) : 0u;
+    int my_id = 0;
+    uint32_t my_key = 0u, top = 0u;
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+        uint32_t t[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) t[i] = key[i];
+#pragma unroll
+        for (int o = VPL / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < o; ++i) t[i] = max(t[i], t[i + o]);
+        const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, t[0]);
+        // the lowest expert that holds it
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) t[i] = key[i] == best ? 1u << i : 0u;
+#pragma unroll
+        for (int o = VPL / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < o; ++i) t[i] |= t[i + o];
+        const uint32_t le = t[0] && best ? (uint32_t)(lane + 32 * (__ffs((int)t[0]) - 1)) : 0xFFFFFFFFu;
+        const int e = (int)__reduce_min_sync(0xFFFFFFFFu, le);  // -1 if none is left
+        const int own = e >= 0 && (e & 31) == lane ? e >> 5 : -1;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = i == own ? 0u : key[i];
+        if (lane == k) {
+            my_id = e;
+            my_key = best;
+        }
+        if (k == 0) top = best;
+    }
+    const float m = key_to_float(top);
+    float z = 0.0f;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) z += expf(l[e] - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+    const float p = lane < K ? expf(key_to_float(my_key) - m) / z : 0.0f;
+    float s = p;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane < K) {
+        ids[lane] = my_id;
+        w[lane] = renormalize ? p / s : p;
+    }
+    if (with_shared && lane == 0) {
+        ids[K] = E;
+        w[K] = shared_weight;
+    }
 }
 
 // 2^(s - 127) of four scale bytes (0 for byte 0)
@@ -277,8 +341,8 @@ __device__ __forceinline__ int shift_at(int blk) { return (blk & ~31) | ((blk & 
 __device__ __forceinline__ int cut(int n, int b, int G) { return (int)((uint32_t)n * (uint32_t)b / (uint32_t)G); }
 
 // NC: stages of a gate_up unit (H <= NC * 4096).  SF: the scale bytes come with the
-// codes (rows of whole 16-byte units, which the TMA can read); else the scale warp
-// loads them.
+// codes (rows of whole 16-byte units, which the TMA can read); else each warp loads
+// its own, a pair of stages ahead.
 template <int NC, bool SF>
 __global__ void __launch_bounds__(kThreads, 1)
     layer_few_kernel(const FewArgs a, const __grid_constant__ FewMaps maps) {
@@ -297,10 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* pair_t = reinterpret_cast<uint8_t*>(pair_of + kMaxPairs);  // a pair's token
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBar);
     uint64_t* empty = full + kStages;
-    uint64_t* sf_full = empty + kStages;      // codes and factors
-    uint64_t* part_full = sf_full + kStages;  // [2]
+    uint64_t* part_full = empty + kStages;    // [2]
     uint64_t* part_free = part_full + 2;      // [2]
     uint64_t* h_ready = part_free + 2;
+    uint64_t* router_full = h_ready + 1;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = (int)blockIdx.x, G = (int)gridDim.x;
@@ -309,31 +373,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int KGH = H / 32, KGI = I / 32;
     // gate_up: slots per unit, units per stage (NC == 1), units per entry
     const int sg = (H + 255) / 256, sg_whole = H / 256;
-    const int ups = NC == 1 ? kConsumerWarps / sg : 1;
-    const int upe = I / 8;
-    const uint32_t upe_m = div_magic((uint32_t)upe);
+    const int ups = a.ups, upe = I / 8;
+    const uint32_t upe_m = a.upe_m;
     const int sfp = NC == 1 ? KGH : 128;  // bytes between a unit's scale rows in a stage
     // down: items per entry, slots per item, items per stage or stages per item
     const int RU = H / 16;
-    const uint32_t ru_m = div_magic((uint32_t)RU);
+    const uint32_t ru_m = a.ru_m;
     const int sd = (I + 255) / 256, sd_whole = I / 256;
     const int spi = (sd + kConsumerWarps - 1) / kConsumerWarps;
-    const int ips = spi == 1 ? kConsumerWarps / sd : 1;
+    const int ips = a.ips;
     const int sfp2 = spi == 1 ? KGI : 128;
 
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kConsumerWarps);
-            mbar_init(&sf_full[s], 1);
+    // router rows of this CTA, and what of them and of x lies in the ring: `rows` rows of
+    // Wr (the gate last), then x's T, each 64 bytes past a multiple of 128 from the next
+    const int row0 = b * a.router_rows, rows = max(min(a.router_rows, a.E + (a.gate ? 1 : 0) - row0), 0);
+    const int rpitch = a.router_k * 2 + 64;
+    auto load_router = [&](int k0) {  // the producer: rows' and tokens' k0 .. k0 + router_k
+        const uint32_t bytes = (uint32_t)min(a.router_k, H - k0) * 2u;
+        if (lane == 0) mbar_arrive_expect_tx(router_full, (uint32_t)(rows + T) * bytes);
+        __syncwarp();
+        if (lane < rows + T) {
+            const uint16_t* src = lane >= rows ? a.x + (size_t)(lane - rows) * H
+                                               : (row0 + lane < a.E ? a.wr + (size_t)(row0 + lane) * H : a.gate);
+            bulk_copy_g2s(smem_u32(smem) + lane * rpitch, src + k0, bytes, router_full);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&part_full[i], kConsumerWarps);
-            mbar_init(&part_free[i], 2);
+    };
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            mbar_init(router_full, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        mbar_init(h_ready, 1);
-        info[2] = info[3] = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+        load_router(0);  // ahead of everything else
+        if (lane == 0) {
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], kConsumerWarps);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&part_full[i], kConsumerWarps);
+                mbar_init(&part_free[i], 2);
+            }
+            mbar_init(h_ready, 1);
+            info[2] = info[3] = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
     }
     __syncthreads();
 
@@ -391,8 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gs = 0;  // stages issued (producer) or consumed so far
 
     if (warp == kProducerWarp) {
-        // whole stages of the shared expert's units need no routing (once the router's own
-        // loads are through: before them they would hold those up)
+        // the router's further k, where all of it does not fit at once
+        for (int k0 = a.router_k; k0 < H; k0 += a.router_k) {
+            asm volatile("bar.sync 3, %0;" ::"n"(kConsumers + 32) : "memory");
+            load_router(k0);
+        }
+        // whole stages of the shared expert's units need no routing (the ring is free once
+        // the router has read it)
         asm volatile("bar.sync 3, %0;" ::"n"(kConsumers + 32) : "memory");
         const int stages = NC == 1 ? nsh / ups : nsh * NC;
         for (; (int)gs < min(stages, kEarlyStages); ++gs) issue_gate_up(gs, (int)gs, false);
@@ -401,56 +490,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         // each CTA multiplies a few rows of [Wr; gate], spread over the warps 32 k at a
         // time.  Equal rows give equal logits: every row's sums have one order.
         const int r = lane >> 2, c = lane & 3;
-        const int row0 = b * a.router_rows, rows = min(a.router_rows, a.E + (a.gate ? 1 : 0) - row0);
-        if (rows > 0) {
-            // (rows and tokens that do not exist are read as the first one, unconditionally
-            // so that the loads of four steps go out together, and not used)
-            auto row_of = [&](int i) {
-                const int row = row0 + (i < rows ? i : 0);
-                return reinterpret_cast<const uint4*>(row < a.E ? a.wr + (size_t)row * H : a.gate) + c;
-            };
-            const uint4* wa = row_of(r);
-            const uint4* wb = row_of(r + 8);
-            const uint4* x0 = reinterpret_cast<const uint4*>(a.x + (size_t)(r < T ? r : 0) * H) + c;
-            const uint4* x1 = reinterpret_cast<const uint4*>(a.x + (size_t)(8 + r < T ? 8 + r : 0) * H) + c;
-            const bool two_rows = rows > 8, two_tokens = T > 8;
-            float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-            for (int g0 = warp; g0 < KGH; g0 += 4 * kConsumerWarps) {
-                uint4 va[4], vb[4], vx[2][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int o = 4 * min(g0 + q * kConsumerWarps, KGH - 1);
-                    va[q] = __ldg(wa + o);
-                    vx[0][q] = __ldg(x0 + o);
-                    vb[q] = two_rows ? __ldg(wb + o) : va[q];
-                    vx[1][q] = two_tokens ? __ldg(x1 + o) : vx[0][q];
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (g0 + q * kConsumerWarps >= KGH) break;
+        float racc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        uint32_t xmax = 0;  // the largest |x| of token `warp`
+        bool router_ok = true;
+        for (int k0 = 0, u = 0; k0 < H; k0 += a.router_k, ++u) {
+            const int kg = min(a.router_k, H - k0) / 32;
+            if (u) {  // the last piece has been read: the next may take its place
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                asm volatile("bar.arrive 3, %0;" ::"n"(kConsumers + 32) : "memory");
+            }
+            router_ok = router_ok && mbar_wait_warp(router_full, u & 1);
+            if (!router_ok) continue;
+            const uint32_t base = smem_u32(smem) + 16 * c, xs = base + rows * rpitch;
+            // (rows and tokens that do not exist: the first one, not used)
+            const uint32_t wa = base + (r < rows ? r : 0) * rpitch, wb = base + (r + 8 < rows ? r + 8 : 0) * rpitch;
+            const uint32_t xa = xs + (r < T ? r : 0) * rpitch, xb = xs + (8 + r < T ? 8 + r : 0) * rpitch;
+            if (rows > 0) {
+#pragma unroll 2
+                for (int g = warp; g < kg; g += kConsumerWarps) {
+                    const uint4 va = lds128(wa + 64 * g), vb = lds128(wb + 64 * g);
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        if (n && !two_tokens) break;
+                        if (n && T <= 8) break;
                         float t4[4];
-                        mma_bf16_32(t4, va[q], vb[q], vx[n][q]);
+                        mma_bf16_32(t4, va, vb, lds128((n ? xb : xa) + 64 * g));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][i] += t4[i];
+                        for (int i = 0; i < 4; ++i) racc[n][i] += t4[i];
                     }
                 }
             }
+            if (warp < T) {
+                const uint32_t xr = smem_u32(smem) + (rows + warp) * rpitch;
+#pragma unroll 4
+                for (int q = lane; q < kg * 4; q += 32) {
+                    const uint4 v = lds128(xr + 16 * q);
+                    const uint32_t xx[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-                part[(n * kConsumerWarps + warp) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-            consumers_sync();
-            if (tid < 256) {  // one (row, token) each
-                const float* p = reinterpret_cast<const float*>(part) + (tid >> 7) * kConsumerWarps * 128 + (tid & 127);
-                float v = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kConsumerWarps; ++w) v += p[w * 128];
-                const int l = (tid & 127) >> 2, q = tid & 3;
-                const int row = (l >> 2) + (q & 2 ? 8 : 0), t = 8 * (tid >> 7) + 2 * (l & 3) + (q & 1);
-                if (row < rows && t < T) a.logits[(size_t)t * (a.E + 1) + row0 + row] = v;
+                    for (int i = 0; i < 4; ++i) xmax = max(xmax, max(xx[i] & 0x7FFFu, (xx[i] >> 16) & 0x7FFFu));
+                }
             }
+        }
+        xmax = __reduce_max_sync(0xFFFFFFFFu, xmax);
+        // the power of two that scales token `warp`
+        if (warp < T && lane == 0) rscale[warp] = __uint_as_float((uint32_t)(127 - row_f16_shift(xmax)) << 23);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+            part[(n * kConsumerWarps + warp) * 32 + lane] = make_float4(racc[n][0], racc[n][1], racc[n][2], racc[n][3]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring goes back to the TMA
+        consumers_sync();
+        if (tid < 256) {  // one (row, token) each
+            const float* p = reinterpret_cast<const float*>(part) + (tid >> 7) * kConsumerWarps * 128 + (tid & 127);
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kConsumerWarps; ++w) v += p[w * 128];
+            const int l = (tid & 127) >> 2, q = tid & 3;
+            const int row = (l >> 2) + (q & 2 ? 8 : 0), t = 8 * (tid >> 7) + 2 * (l & 3) + (q & 1);
+            if (row < rows && t < T) a.logits[(size_t)t * (a.E + 1) + row0 + row] = v;
         }
         asm volatile("bar.arrive 3, %0;" ::"n"(kConsumers + 32) : "memory");
         // what gate_up raises starts at zero
@@ -458,26 +553,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         consumers_sync();
         if (tid == 0) add_release(&a.sync[0]);
 
-        // while the others finish: the rows' powers of two, the masks' zeros
-        if (warp < T) {
-            uint32_t mx = 0;
-            const uint4* xr = reinterpret_cast<const uint4*>(a.x + (size_t)warp * H);
-#pragma unroll 8
-            for (int u = lane; u < H / 8; u += 32) {
-                const uint4 v = __ldg(xr + u);
-                const uint32_t xx[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx = max(mx, max(xx[i] & 0x7FFFu, (xx[i] >> 16) & 0x7FFFu));
-            }
-            mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-            if (lane == 0) rscale[warp] = __uint_as_float((uint32_t)(127 - row_f16_shift(mx)) << 23);
-        }
+        // while the others finish: the masks' zeros
         uint32_t* mask = reinterpret_cast<uint32_t*>(smem + kMask);
         uint16_t* first = reinterpret_cast<uint16_t*>(smem + kFirst);
         int32_t* ids_s = reinterpret_cast<int32_t*>(smem + kIds);
         float* logit_s = reinterpret_cast<float*>(smem + kEarlyStages * kStageBytes);  // [T][E]
         for (int e = tid; e < Et; e += kConsumers) mask[e] = 0u;
-        if (tid == 0) info[1] = grid_wait(&a.sync[0], (uint32_t)G) ? 1 : 0;
+        if (tid == 0) info[1] = router_ok && grid_wait(&a.sync[0], (uint32_t)G) ? 1 : 0;
         consumers_sync();
 
         // ------------------------------------------------------ routing
@@ -485,25 +567,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (info[1]) {
             // (loads are kept few in the code: a call runs every line of it once or twice,
             // and fetching straight-line code costs more than running it)
-            const uint32_t e_m = div_magic((uint32_t)a.E);
 #pragma unroll 4
             for (int q = tid; q < T * a.E; q += kConsumers) {
-                const int t = (int)div_by((uint32_t)q, e_m);
+                const int t = (int)div_by((uint32_t)q, a.e_m);
                 logit_s[q] = __ldcg(a.logits + q + t);  // written by this kernel: read from L2
             }
             consumers_sync();
             if (warp < T) {
                 const float* l = logit_s + warp * a.E;
-                auto load = [l](int e) { return l[e]; };
                 const float sw = a.gate ? 1.0f / (1.0f + expf(-__ldcg(a.logits + (size_t)warp * (a.E + 1) + a.E))) : 1.0f;
                 int32_t* wi = ids_s + warp * 33;
                 float* ww = w_s + warp * Kt;
                 if (a.E <= 128)
-                    route_loaded<4>(load, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
+                    route_few<4>(l, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
                 else if (a.E <= 512)
-                    route_loaded<16>(load, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
+                    route_few<16>(l, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
                 else
-                    route_loaded<32>(load, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
+                    route_few<32>(l, a.E, a.K, a.shared, a.renorm, sw, wi, ww, lane);
                 __syncwarp();
                 for (int j = lane; j < Kt; j += 32) {
                     // a slot without an expert (only where every logit left is a NaN of the
@@ -642,74 +722,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t u = gs - 1 - d;
             if (!mbar_wait_warp(&full[u % kStages], (u / kStages) & 1)) break;
         }
-    } else if (warp == kScaleWarp) {
-        // ------------------------------------------------- scale factors
-        // of stage after stage: this lane's slot, rows lane / 16, + 2, ...
-        const int slot = lane & 15, row0 = lane >> 4;
-        bool ok = routed;
-        // Without SF: the slot's first scale byte in row 0 at byte `at` of src, rows `pitch`
-        // bytes apart and those from 8 on `up` bytes further, n bytes counting (none: no
-        // such slot).  With it: at byte `raw` of the stage's, rows raw_pitch apart.
-        auto convert = [&](int st, const uint8_t* src, size_t words, size_t at, size_t pitch, size_t up, int n,
-                           uint32_t raw, int raw_pitch) {
-            const int s = st % kStages;
-            uint2 w[8];
-            if (!SF) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = row0 + 2 * i;
-                    w[i] = load_scales(src, n > 0 ? at + row * pitch + (row < 8 ? 0 : up) : 0, n, words);
-                    if (n <= 0) w[i] = make_uint2(0, 0);
-                }
-            }
-            if (!mbar_wait_warp(&full[s], (st / kStages) & 1)) return false;
-            const uint32_t stage = smem_u32(smem + s * kStageBytes);
-            const uint32_t f = stage + kCodeBytes + kScaleBytes + row0 * kFactorRow + slot * 32;
-            if (SF) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = lds64(stage + kCodeBytes + raw + (row0 + 2 * i) * raw_pitch);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sts_f4(f + 2 * i * kFactorRow, factors(w[i].x));
-                sts_f4(f + 2 * i * kFactorRow + 16, factors(w[i].y));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sf_full[s]);
-            return true;
-        };
-        {
-            const int j = NC == 1 ? slot / sg : 0, sl = NC == 1 ? slot - j * sg : slot;
-            const uint32_t raw = j < ups ? (uint32_t)(j * 16 * sfp + sl * 8) : 0u;
-            for (int st = 0; st < gstages && ok; ++st) {
-                const int slice = sl + (NC == 1 ? 0 : (st % NC) * kConsumerWarps), k = NC == 1 ? st * ups + j : st / NC;
-                size_t at = 0;
-                int n = 0;
-                if (!SF && j < ups && k < nunits) {
-                    int e, blk;
-                    unit_at(k, e, blk);
-                    at = ((size_t)list_e[e] * 2 * I + blk * 8) * KGH + 8 * slice;
-                    n = min(8, KGH - 8 * slice);
-                }
-                ok = convert(st, a.s13, (size_t)Et * 2 * I * KGH / 4, at, KGH, (size_t)(I - 8) * KGH, n, raw, sfp);
-            }
-        }
-        {
-            const int j = spi == 1 ? slot / sd : 0, sl = spi == 1 ? slot - j * sd : slot;
-            const uint32_t raw = j < ips ? (uint32_t)(j * 16 * sfp2 + sl * 8) : 0u;
-            for (int st = 0; st < dstages && ok; ++st) {
-                const int slice = sl + (spi == 1 ? 0 : (st % spi) * kConsumerWarps);
-                const int item = lo + (spi == 1 ? st * ips + j : st / spi);
-                size_t at = 0;
-                int n = 0;
-                if (!SF && j < ips && item < hi) {
-                    const int e = (int)div_by((uint32_t)item, ru_m);
-                    at = ((size_t)list_e[e] * H + (item - e * RU) * 16) * KGI + 8 * slice;
-                    n = min(8, KGI - 8 * slice);
-                }
-                ok = convert(gstages + st, a.s2, (size_t)Et * H * KGI / 4, at, KGI, 0, n, raw, sfp2);
-            }
-        }
     } else if (warp < kConsumerWarps) {
         // ------------------------------------------------------ consumers
         const int r = lane >> 2, c = lane & 3, mj = lane >> 3, mi = lane & 7;
@@ -734,16 +746,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&part_full[buf]);
         };
-        // stage st's slot of this warp, slot `at` of the stage, times b
-        auto multiply = [&](int st, int at, bool on, const uint4 (&b)[8], float (&acc)[4]) {
+        // stage st's slot of this warp times b.  Lane 2 q + z turns the scale bytes 4 z .. of
+        // the slot's row q into factors: from the stage (byte raw on), or from word w
+        const uint32_t fac = smem_u32(smem + kFactors) + warp * 1024;  // two slots' factors
+        auto multiply = [&](int st, bool on, uint32_t raw, uint32_t w, const uint4 (&b)[8], float (&acc)[4]) {
             const uint32_t stage = ring + (st % kStages) * kStageBytes;
-            if (!failed && on)
-                slot_mma(stage + at * kSlotBytes, lm, stage + kCodeBytes + kScaleBytes + r * kFactorRow + at * 32, b, acc);
+            if (!failed && !mbar_wait_warp(&full[st % kStages], (st / kStages) & 1)) failed = true;
+            if (!failed && on) {
+                const uint32_t f = fac + (st & 1) * 512;
+                sts_f4(f + 16 * lane, factors(SF ? lds32(stage + kCodeBytes + raw) : w));
+                __syncwarp();
+                slot_mma(stage + warp * kSlotBytes, lm, f + 32 * r, b, acc);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st % kStages]);
-        };
-        auto wait_stage = [&](int st) {
-            if (!failed && !mbar_wait_warp(&sf_full[st % kStages], (st / kStages) & 1)) failed = true;
         };
 
         // -------------------------------------------------------- gate_up
@@ -774,8 +790,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 have = i;
             };
+            // where this lane's scale word lies: row lane / 2 of the slot, groups 4 (lane % 2) ..
+            const int srow = lane >> 1, sgrp = 4 * (lane & 1);
+            const uint32_t raw = (uint32_t)((j * 16 + srow) * sfp + q0 * 8 + sgrp);
+            const size_t words = (size_t)Et * 2 * I * KGH / 4;
+            uint32_t sw[2] = {0, 0};
+            auto load_sw = [&](int h) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int k = NC == 1 ? (2 * h + i) * ups + j : h, grp = (q0 + (NC == 1 ? 0 : i * kConsumerWarps)) * 8 + sgrp;
+                    sw[i] = 0;
+                    if (SF || j >= ups || k >= nunits || grp >= KGH) continue;
+                    int e, blk;
+                    unit_at(k, e, blk);
+                    const int row = blk * 8 + (srow < 8 ? srow : I + srow - 8);
+                    sw[i] = load_scales(a.s13, ((size_t)list_e[e] * 2 * I + row) * KGH + grp, KGH - grp, words);
+                }
+            };
+            load_sw(0);
             for (int h = 0; h < ghands; ++h) {
                 float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+                const uint32_t w[2] = {sw[0], sw[1]};
+                load_sw(h + 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int st = 2 * h + i, k = NC == 1 ? st * ups + j : h;
@@ -786,8 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         unit_at(k, e, blk);
                         if (e != have) load_x(e);
                     }
-                    wait_stage(st);
-                    multiply(st, warp, on, xb[NC == 1 ? 0 : i], acc[NC == 1 ? i : 0]);
+                    multiply(st, on, raw, w[i], xb[NC == 1 ? 0 : i], acc[NC == 1 ? i : 0]);
                 }
                 hand_over(h, acc, NC > 1);
             }
@@ -823,10 +858,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 4; ++q) w[q] = __hmul2(w[q], g);
                 }
             };
+            const int srow = lane >> 1, sgrp = 4 * (lane & 1);
+            const uint32_t raw = (uint32_t)((j * 16 + srow) * sfp2 + q0 * 8 + sgrp);
+            const size_t words = (size_t)Et * H * KGI / 4;
+            uint32_t sw[2] = {0, 0};
+            auto load_sw = [&](int h) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int item = lo + (spi > 1 ? h : (2 * h + i) * ips + j), grp = (q0 + (spi > 1 ? i * kConsumerWarps : 0)) * 8 + sgrp;
+                    sw[i] = 0;
+                    if (SF || j >= ips || item >= hi || grp >= KGI) continue;
+                    const int e = (int)div_by((uint32_t)item, ru_m);
+                    sw[i] = load_scales(a.s2, ((size_t)list_e[e] * H + (item - e * RU) * 16 + srow) * KGI + grp, KGI - grp, words);
+                }
+            };
+            load_sw(0);
             if (!failed && !mbar_wait_warp(h_ready, 0)) failed = true;
             if (!failed && !info[2]) failed = true;
             for (int h = 0; h < dhands; ++h) {
                 float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+                const uint32_t w[2] = {sw[0], sw[1]};
+                load_sw(h + 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int st = 2 * h + i;
@@ -838,11 +890,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int e = (int)div_by((uint32_t)item, ru_m), key = e * spi + (spi > 1 ? i : 0);
                         if (key != have) load_h(e, slice, key);
                     }
-                    wait_stage(gstages + st);
                     if (spi == 1)
-                        multiply(gstages + st, warp, on, hb, acc[i]);
+                        multiply(gstages + st, on, raw, w[i], hb, acc[i]);
                     else
-                        multiply(gstages + st, warp, on, hb, acc[0]);
+                        multiply(gstages + st, on, raw, w[i], hb, acc[0]);
                 }
                 hand_over(ghands + h, acc, spi > 1);
             }
@@ -966,9 +1017,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = cut(n, b, G) + tid; q < q1; q += kThreads) {
             const int t = q / H, row = q - t * H;
             float v = 0.0f;
-#pragma unroll 4
-            for (int j = 0; j < Kt; ++j)
-                v = fmaf(w_s[t * Kt + j], __ldcg(a.y + (size_t)pair_of[t * Kt + j] * H + row), v);
+            for (int j0 = 0; j0 < Kt; j0 += 12) {  // (the loads of twelve slots together)
+                float y[12];
+#pragma unroll
+                for (int j = 0; j < 12; ++j)
+                    y[j] = __ldcg(a.y + (size_t)pair_of[t * Kt + min(j0 + j, Kt - 1)] * H + row);
+#pragma unroll
+                for (int j = 0; j < 12; ++j)
+                    if (j0 + j < Kt) v = fmaf(w_s[t * Kt + j0 + j], y[j], v);
+            }
             a.out[q] = f32_to_bf16_bits(v);
         }
     }
@@ -1081,6 +1138,12 @@ cudaError_t launch_layer_few(const LayerFew& p, void* workspace, cudaStream_t s)
     a.renorm = p.renormalize;
     // scale rows that the TMA can read: whole 16-byte units
     const bool sf = p.H % 512 == 0 && p.I % 512 == 0 && ((uintptr_t)p.s13 | (uintptr_t)p.s2) % 16 == 0;
+    const int sg = (p.H + 255) / 256, sd = (p.I + 255) / 256;
+    a.ups = sg <= kConsumerWarps ? kConsumerWarps / sg : 1;
+    a.ips = sd <= kConsumerWarps ? kConsumerWarps / sd : 1;
+    a.upe_m = div_magic((uint32_t)p.I / 8);
+    a.ru_m = div_magic((uint32_t)p.H / 16);
+    a.e_m = div_magic((uint32_t)p.E);
     FewMaps maps;
     cudaError_t err = few_maps(p, sf, &maps);
     if (err != cudaSuccess) return err;
@@ -1092,6 +1155,8 @@ cudaError_t launch_layer_few(const LayerFew& p, void* workspace, cudaStream_t s)
     const int grid = (int)std::min<long long>({work, (long long)num_sms(), (long long)kMaxGrid});
     a.router_rows = (rows + grid - 1) / grid;
     if (a.router_rows > 16) return cudaErrorNotSupported;  // fewer than 65 SMs
+    // as many k as the ring holds of the rows and the tokens (whole groups of 32)
+    a.router_k = std::min(p.H, ((kStages * kStageBytes / (a.router_rows + p.T) - 64) / 2) & ~31);
     if (p.H > 4096) return sf ? launch_few<2, true>(a, maps, grid, s) : launch_few<2, false>(a, maps, grid, s);
     return sf ? launch_few<1, true>(a, maps, grid, s) : launch_few<1, false>(a, maps, grid, s);
 }
