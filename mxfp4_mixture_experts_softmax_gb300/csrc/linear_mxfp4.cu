@@ -255,6 +255,27 @@ __device__ __forceinline__ void store_block(const StreamArgs& a, bool vec, const
     }
 }
 
+// 32 rows x 64 columns of bf16 staged in shared memory in rows of 128 bytes, 16-byte part q of
+// row r at q ^ (r & 7), to the output in full lines.  All 32 lanes call it.
+__device__ __forceinline__ void store_rows_bf16(const StreamArgs& a, const uint8_t* stg, int t0, int n0, int lane) {
+    const int q = lane & 7, n = n0 + 8 * q;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3), t = t0 + r;
+        if (t >= a.T) break;
+        const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((q ^ (r & 7)) << 4));
+        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + (size_t)t * a.ldo + n;
+        if (n + 8 <= a.N) {
+            *reinterpret_cast<uint4*>(o) = v;
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (n + k < a.N) o[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+        }
+    }
+}
+
 StreamArgs stream_args(const LinearMxfp4& p) {
     StreamArgs a = {};
     a.scales = p.scales;
@@ -577,8 +598,12 @@ struct PairArgs {
     int vec;              // 16-byte stores (and residual loads)
 };
 
-constexpr int kPairThreads = 448;
-constexpr int kPairEpiWarp0 = 6;  // after the producer, the MMA and the four scale warps (2..5)
+// Four warpgroups: the scale warps; the producer, the MMA and two idle warps; two of epilogue
+// warps, which take registers from the others so that a warp holds its 128 columns.
+constexpr int kPairThreads = 512;
+constexpr int kPairProducer = 4, kPairMma = 5, kPairEpiWarp0 = 8;
+constexpr int kPairRegs = 56, kPairEpiRegs = 192;
+static_assert(256 * (kPairRegs + kPairEpiRegs) <= kPairThreads * 128, "registers of the launch");
 
 template <int TN>
 struct PairLayout {
@@ -639,124 +664,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<true>(tmem_slot, 512);
+    if (warp == kPairMma) tmem_alloc<true>(tmem_slot, 512);
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_begin();
 
-    if (warp == 0) {
-        // ------------------------------------------------------- producer
-        if (lane == 0) {
-            uint32_t gs = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs) {
-                const int nt = tile / mts, mt = tile - nt * mts;
-                const int arow = mt * 256 + rank * 128, brow = nt * TN + rank * L::kBRows;
-                const uint8_t* sfa = a.sfa + (size_t)(mt * 2 + rank) * nk * 1024;
-                const uint8_t* sfb = a.sfb + (size_t)nt * (TN / 128) * nk * 1024;
-                for (int st = 0; st < nk; ++st, ++gs) {
-                    const int s = gs % kStages;
-                    if (gs >= (uint32_t)kStages && !mbar_wait(&stage_free[s], ((gs / kStages) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t base = smem_u32(smem + s * L::kStage);
-                    mbar_arrive_expect_tx(&tma_full[s], (uint32_t)L::kStage);
-                    tma_load_2d(base, &x_map, st * kRowBytes, arow, &tma_full[s]);
-                    tma_load_2d(base + kABytes, &w_map, st * kRowBytes, brow, &tma_full[s]);
-                    bulk_copy_g2s(base + L::kSf, sfa + (size_t)st * 1024, 1024, &tma_full[s]);
-#pragma unroll
-                    for (int j = 0; j < TN / 128; ++j)
-                        bulk_copy_g2s(base + L::kSf + L::kSfaBytes + j * 1024,
-                                      sfb + ((size_t)j * nk + st) * 1024, 1024, &tma_full[s]);
-                }
-            }
-            // wait (bounded) until the last loads landed before the CTA can exit
-            for (int d = 0; d < kStages && d < (int)gs; ++d) {
-                const uint32_t u = gs - 1 - d;
-                if (!mbar_wait(&tma_full[u % kStages], (u / kStages) & 1)) break;
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // -------------------------------------------------------- MMA
-            constexpr uint32_t id0 = idesc_mxf4(256, TN, 0), id2 = idesc_mxf4(256, TN, 2);
-            uint32_t gs = 0, it = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs, ++it) {
-                const uint32_t b = it % kAccBufs;
-                if (it >= (uint32_t)kAccBufs && !mbar_wait(&acc_free[b], ((it / kAccBufs) - 1) & 1)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem + b * TN;
-                for (int st = 0; st < nk; ++st, ++gs) {
-                    const int s = gs % kStages;
-                    // (arrived at once the stage's loads and scale factors are there, by both CTAs)
-                    if (!mbar_wait(&sf_full[s], (gs / kStages) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t base = smem_u32(smem + s * L::kStage);
-                    const uint32_t sf = tmem + (uint32_t)(L::kSfCol0 + s * 32);
-                    const uint64_t ad = sdesc_sw128(base), bd = sdesc_sw128(base + kABytes);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)  // K = 64 each: +32 bytes in the swizzle atom
-                        mma_mxf4_pair(d_tmem, ad + 2u * kk, bd + 2u * kk, (kk & 1) ? id2 : id0, sf + 8u * (kk >> 1),
-                                      sf + 16u + 8u * (kk >> 1), (st | kk) != 0 ? 1u : 0u);
-                    mma_commit_pair(&stage_free[s]);
-                }
-                if (ok) mma_commit_pair(&acc_full[b]);
-            }
-            mma_commit_pair(drain);  // every MMA issued has completed when this arrives
-            mbar_wait(drain, 0);
-        } else if (lane == 0) {
-            mbar_wait(drain, 0);  // odd CTA: the pair's MMAs and their commits to it are done
-        }
-    } else if (warp < kPairEpiWarp0) {
-        // -------------------------------------------------- scale factors
-        // token r's at lane r, column base + r / 32; weight row n's at lane 32 q + n % 32,
-        // column base + n / 32, in every quadrant q
-        constexpr int NJ = TN / 32;
-        const int quad = warp & 3;
-        const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)L::kSfCol0;
-        uint32_t gs = 0;
-        bool ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += pairs) {
-            for (int st = 0; st < nk; ++st, ++gs) {
-                const int s = gs % kStages;
-                // the stage is filled again only after the MMAs that read these columns
-                if (!mbar_wait_warp(&tma_full[s], (gs / kStages) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t sf = smem_u32(smem + s * L::kStage + L::kSf) + 8 * lane;
-                const uint2 av = lds64(sf + 256 * quad);
-                uint32_t b0[NJ], b1[NJ];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const uint2 v = lds64(sf + L::kSfaBytes + 256 * j);
-                    b0[j] = v.x, b1[j] = v.y;
-                }
-                tc_fence_after();
-                const uint32_t col = lane_base + (uint32_t)(s * 32);
-                tmem_st_cols<1>(col + (uint32_t)quad, &av.x);
-                tmem_st_cols<1>(col + 8u + (uint32_t)quad, &av.y);
-                tmem_st_cols<NJ>(col + 16u, b0);
-                tmem_st_cols<NJ>(col + 24u, b1);
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 0)
-                        mbar_arrive(&sf_full[s]);
-                    else
-                        mbar_arrive_remote(&sf_full[s], 0);
-                }
-            }
-        }
-    } else {
+    if (warp >= kPairEpiWarp0) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
         // -------------------------------------------------------- epilogue
         constexpr int kCols = TN / 2;  // columns per warp
         const int quad = warp & 3, half = (warp - kPairEpiWarp0) >> 2;
@@ -782,6 +698,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             const int t0 = mt * 256 + rank * 128 + quad * 32, n0 = nt * TN + half * kCols;
             if (t0 >= T) continue;
+            if (a.vec && !a.o.out_f32 && !a.o.residual) {
+                // rounded before staging: half the shared-memory traffic, which the MMA's
+                // operands share
+                uint8_t* row = reinterpret_cast<uint8_t*>(stg) + lane * 128;
+#pragma unroll
+                for (int ch = 0; ch < kCols / 64; ++ch) {
+                    if (n0 + ch * 64 >= N) break;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = ch * 64 + 8 * q + 2 * i;
+                            o[i] = f32x2_to_bf16x2_bits(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                        }
+                        *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    __syncwarp();
+                    store_rows_bf16(a.o, reinterpret_cast<const uint8_t*>(stg), t0, n0 + ch * 64, lane);
+                    __syncwarp();
+                }
+                continue;
+            }
 #pragma unroll
             for (int ch = 0; ch < kCols / 32; ++ch) {
                 if (n0 + ch * 32 >= N) break;
@@ -794,13 +733,126 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
             }
         }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegs));
+        if (warp == kPairProducer) {
+            // ------------------------------------------------------- producer
+            if (lane == 0) {
+                uint32_t gs = 0;
+                bool ok = true;
+                for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                    const int nt = tile / mts, mt = tile - nt * mts;
+                    const int arow = mt * 256 + rank * 128, brow = nt * TN + rank * L::kBRows;
+                    const uint8_t* sfa = a.sfa + (size_t)(mt * 2 + rank) * nk * 1024;
+                    const uint8_t* sfb = a.sfb + (size_t)nt * (TN / 128) * nk * 1024;
+                    for (int st = 0; st < nk; ++st, ++gs) {
+                        const int s = gs % kStages;
+                        if (gs >= (uint32_t)kStages && !mbar_wait(&stage_free[s], ((gs / kStages) - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t base = smem_u32(smem + s * L::kStage);
+                        mbar_arrive_expect_tx(&tma_full[s], (uint32_t)L::kStage);
+                        tma_load_2d(base, &x_map, st * kRowBytes, arow, &tma_full[s]);
+                        tma_load_2d(base + kABytes, &w_map, st * kRowBytes, brow, &tma_full[s]);
+                        bulk_copy_g2s(base + L::kSf, sfa + (size_t)st * 1024, 1024, &tma_full[s]);
+#pragma unroll
+                        for (int j = 0; j < TN / 128; ++j)
+                            bulk_copy_g2s(base + L::kSf + L::kSfaBytes + j * 1024,
+                                          sfb + ((size_t)j * nk + st) * 1024, 1024, &tma_full[s]);
+                    }
+                }
+                // wait (bounded) until the last loads landed before the CTA can exit
+                for (int d = 0; d < kStages && d < (int)gs; ++d) {
+                    const uint32_t u = gs - 1 - d;
+                    if (!mbar_wait(&tma_full[u % kStages], (u / kStages) & 1)) break;
+                }
+            }
+        } else if (warp == kPairMma) {
+            if (lane == 0 && rank == 0) {
+                // -------------------------------------------------------- MMA
+                constexpr uint32_t id0 = idesc_mxf4(256, TN, 0), id2 = idesc_mxf4(256, TN, 2);
+                uint32_t gs = 0, it = 0;
+                bool ok = true;
+                for (int tile = pair; tile < tiles && ok; tile += pairs, ++it) {
+                    const uint32_t b = it % kAccBufs;
+                    if (it >= (uint32_t)kAccBufs && !mbar_wait(&acc_free[b], ((it / kAccBufs) - 1) & 1)) break;
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem + b * TN;
+                    for (int st = 0; st < nk; ++st, ++gs) {
+                        const int s = gs % kStages;
+                        // (arrived at once the stage's loads and scale factors are there, by both CTAs)
+                        if (!mbar_wait(&sf_full[s], (gs / kStages) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t base = smem_u32(smem + s * L::kStage);
+                        const uint32_t sf = tmem + (uint32_t)(L::kSfCol0 + s * 32);
+                        const uint64_t ad = sdesc_sw128(base), bd = sdesc_sw128(base + kABytes);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)  // K = 64 each: +32 bytes in the swizzle atom
+                            mma_mxf4_pair(d_tmem, ad + 2u * kk, bd + 2u * kk, (kk & 1) ? id2 : id0, sf + 8u * (kk >> 1),
+                                          sf + 16u + 8u * (kk >> 1), (st | kk) != 0 ? 1u : 0u);
+                        mma_commit_pair(&stage_free[s]);
+                    }
+                    if (ok) mma_commit_pair(&acc_full[b]);
+                }
+                mma_commit_pair(drain);  // every MMA issued has completed when this arrives
+                mbar_wait(drain, 0);
+            } else if (lane == 0) {
+                mbar_wait(drain, 0);  // odd CTA: the pair's MMAs and their commits to it are done
+            }
+        } else if (warp < 4) {
+            // -------------------------------------------------- scale factors
+            // token r's at lane r, column base + r / 32; weight row n's at lane 32 q + n % 32,
+            // column base + n / 32, in every quadrant q
+            constexpr int NJ = TN / 32;
+            const int quad = warp & 3;
+            const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)L::kSfCol0;
+            uint32_t gs = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                for (int st = 0; st < nk; ++st, ++gs) {
+                    const int s = gs % kStages;
+                    // the stage is filled again only after the MMAs that read these columns
+                    if (!mbar_wait_warp(&tma_full[s], (gs / kStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sf = smem_u32(smem + s * L::kStage + L::kSf) + 8 * lane;
+                    const uint2 av = lds64(sf + 256 * quad);
+                    uint32_t b0[NJ], b1[NJ];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const uint2 v = lds64(sf + L::kSfaBytes + 256 * j);
+                        b0[j] = v.x, b1[j] = v.y;
+                    }
+                    tc_fence_after();
+                    const uint32_t col = lane_base + (uint32_t)(s * 32);
+                    tmem_st_cols<1>(col + (uint32_t)quad, &av.x);
+                    tmem_st_cols<1>(col + 8u + (uint32_t)quad, &av.y);
+                    tmem_st_cols<NJ>(col + 16u, b0);
+                    tmem_st_cols<NJ>(col + 24u, b1);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive(&sf_full[s]);
+                        else
+                            mbar_arrive_remote(&sf_full[s], 0);
+                    }
+                }
+            }
+        }
     }
 
     tc_fence_before();
     // neither CTA releases its memory while the other may still arrive there or the
     // pair's MMAs may still run
     cluster_sync_all();
-    if (warp == 1) {
+    if (warp == kPairMma) {
         tc_fence_after();
         tmem_dealloc<true>(tmem, 512);
     }

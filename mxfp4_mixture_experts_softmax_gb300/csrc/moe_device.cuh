@@ -50,6 +50,12 @@ __device__ __forceinline__ uint16_t f32_to_bf16_bits(float f) {
     return *reinterpret_cast<uint16_t*>(&b);
 }
 
+// Two of them, the first in the low half.
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2_bits(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // ------------------------------------------- bf16 rows as scaled f16 rows
 
 // The power-of-two shift sigma that moves a bf16 row's largest magnitude into
