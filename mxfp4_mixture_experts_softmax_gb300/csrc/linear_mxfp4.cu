@@ -120,7 +120,7 @@ struct QuantArgs {
 constexpr int kQuantAhead = 4;
 
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(256, 5) quantize_rows_kernel(const QuantArgs a) {
     pdl_begin();
     if ((int)blockIdx.x >= a.xblocks) {
         const int KG = a.K / 32, nk = (a.K + kBK - 1) / kBK, pairs = (nk + 1) / 2;
@@ -148,35 +148,33 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
     const int lane = threadIdx.x & 31;
     const int segs = (a.K + kBK - 1) / kBK, chunk = (segs + a.parts - 1) / a.parts;
     const int esize = F32 ? 4 : 2;
-    const int items = a.T * a.parts;  // (the launcher keeps this within 2^21)
-    for (int it = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5); it < items; it += a.xblocks * 8) {
-        const int t = it / a.parts, s0 = (it - t * a.parts) * chunk, s1 = min(s0 + chunk, segs);
+    const long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int t = (int)(it / a.parts), s0 = (int)(it % a.parts) * chunk, s1 = min(s0 + chunk, segs);
+    if (t < a.T && s0 < s1) {
         const char* row = reinterpret_cast<const char*>(a.x) + (size_t)t * a.ldx * esize;
-        for (int sg = s0; sg < s1; sg += kQuantAhead) {
-            float v[kQuantAhead][8];
+        float v[kQuantAhead][8];
 #pragma unroll
-            for (int u = 0; u < kQuantAhead; ++u) {
-                const int k = (sg + u) * kBK + lane * 8;
+        for (int u = 0; u < kQuantAhead; ++u) {
+            const int k = (s0 + u) * kBK + lane * 8;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
-                if (sg + u < s1 && k < a.K) load8<F32, VEC>(row + (size_t)k * esize, v[u]);
-            }
+            for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+            if (s0 + u < s1 && k < a.K) load8<F32, VEC>(row + (size_t)k * esize, v[u]);
+        }
 #pragma unroll
-            for (int u = 0; u < kQuantAhead; ++u) {
-                const int seg = sg + u, k = seg * kBK + lane * 8;
-                if (seg >= s1) break;
-                uint32_t sb;
-                const uint32_t c = quantize8(v[u], sb);
-                if (k < a.K) *reinterpret_cast<uint32_t*>(a.codes + (size_t)t * (a.K / 2) + k / 2) = c;
-                // lanes 0 and 16: the four scale bytes of their 128 values
-                uint32_t w = sb;
-                w |= __shfl_down_sync(0xFFFFFFFFu, sb, 4) << 8;
-                w |= __shfl_down_sync(0xFFFFFFFFu, sb, 8) << 16;
-                w |= __shfl_down_sync(0xFFFFFFFFu, sb, 12) << 24;
-                if ((lane & 15) == 0)
-                    *reinterpret_cast<uint32_t*>(a.scales + (a.pitch ? (size_t)t * a.pitch + seg * 8 + (lane >> 4) * 4
-                                                                     : sf_block(t, seg, segs) + (lane >> 4) * 4)) = w;
-            }
+        for (int u = 0; u < kQuantAhead; ++u) {
+            const int seg = s0 + u, k = seg * kBK + lane * 8;
+            if (seg >= s1) break;
+            uint32_t sb;
+            const uint32_t c = quantize8(v[u], sb);
+            if (k < a.K) *reinterpret_cast<uint32_t*>(a.codes + (size_t)t * (a.K / 2) + k / 2) = c;
+            // lanes 0 and 16: the four scale bytes of their 128 values
+            uint32_t w = sb;
+            w |= __shfl_down_sync(0xFFFFFFFFu, sb, 4) << 8;
+            w |= __shfl_down_sync(0xFFFFFFFFu, sb, 8) << 16;
+            w |= __shfl_down_sync(0xFFFFFFFFu, sb, 12) << 24;
+            if ((lane & 15) == 0)
+                *reinterpret_cast<uint32_t*>(a.scales + (a.pitch ? (size_t)t * a.pitch + seg * 8 + (lane >> 4) * 4
+                                                                 : sf_block(t, seg, segs) + (lane >> 4) * 4)) = w;
         }
     }
     pdl_end();
@@ -926,10 +924,10 @@ cudaError_t launch_stream(const LinearMxfp4& p, const uint8_t* xcodes, const uin
 
 template <bool F32>
 cudaError_t launch_quantize_rows(QuantArgs a, cudaStream_t s) {
-    // a warp per row where the rows fill the GPU, else rows split into 256-value parts
+    // a warp takes kQuantAhead stages of a row, or fewer while the GPU has idle warps
     const int warps = num_sms() * 4 * 8, segs = (a.K + kBK - 1) / kBK;
-    a.parts = std::max(1, std::min(segs, warps / std::max(a.T, 1)));
-    a.xblocks = (int)std::min<long long>(((long long)a.T * a.parts + 7) / 8, (long long)num_sms() * 4);
+    a.parts = std::max(std::min(segs, warps / std::max(a.T, 1)), (segs + kQuantAhead - 1) / kQuantAhead);
+    a.xblocks = (int)(((long long)a.T * a.parts + 7) / 8);
     const long long witems = (long long)a.N * (((a.K + kBK - 1) / kBK + 1) / 2);
     const int wblocks = a.wsb ? (int)std::min<long long>((witems + 255) / 256, (long long)num_sms()) : 0;
     // 16-byte loads where every row starts on a 16-byte boundary
