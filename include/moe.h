@@ -553,8 +553,9 @@ moe_status_t moe_ffn_mxfp4act_h_offsets(int T, int H, int I, int Et, int Kt, int
  * (11 significant bits; elements below 2^-25 of the largest |h| of their token and
  * expert are dropped).
  * Sums are fp32, over k in blocks of 32 and then over a token's slots in
- * ascending order; results do not vary from run to run.  Weight scale bytes 1..254.  A token whose x holds an infinity
- * or a NaN gets NaN outputs; other tokens are not touched.
+ * ascending order; results do not vary from run to run.  Weight scale bytes
+ * 1..254.  A token whose x holds an infinity or a NaN gets NaN outputs; other
+ * tokens are not touched.
  * Limits: T <= MOE_LAYER_FEW_MAX_T (0 is a no-op), H % 32 == I % 32 == 0, H <= 8192,
  * I <= 8192, E <= 1024, K <= min(E, 32).  Pointers 16-byte
  * aligned; s13, s2, topk_ids and topk_w 4-byte.

@@ -4,13 +4,12 @@
 //   out[t, n] = residual[t, n] + sum_k decode(W)[n, k] * xq[t, k]
 // with fp32 sums and one rounding to the output type.
 //
-// quantize_rows_kernel encodes x; linear_stream_kernel (linear_pair_kernel for large
-// batches) multiplies, on the
-// block-scaled tensor cores (tcgen05.mma kind::mxf4, both scales applied by the
-// MMA, K = 64 an instruction).
+// quantize_rows_kernel encodes x; linear_stream_kernel (up to 64 tokens) or
+// linear_pair_kernel multiplies, on the block-scaled tensor cores (tcgen05.mma
+// kind::mxf4, both scales applied by the MMA, K = 64 an instruction).
 //
-// The weights are the MMA's M side (128 rows a CTA) and the tokens its N side
-// (NT = 16 .. 128 columns), so one token costs no more tensor work than
+// linear_stream_kernel: the weights are the MMA's M side (128 rows a CTA) and the tokens
+// its N side (NT = 16 .. 128 columns), so one token costs no more tensor work than
 // sixteen and the weight stream, which bounds small batches, is read once per
 // token tile.  A stage is 256 k: one 128-byte row of packed codes per weight row and
 // token, two TMA boxes in the 128-byte swizzle.  Few weight tiles do not fill the
@@ -18,8 +17,8 @@
 // leaves its fp32 partial tile in shared memory, and the CTAs of the cluster
 // each add a share of the tile over the S partials (distributed shared
 // memory, in rank order: the result does not depend on timing).
-// 192 threads, two CTAs per SM, so that one CTA's start and end overlap the
-// other's stream:
+// 192 threads, two to four CTAs per SM, so that one CTA's start and end overlap the
+// others' stream:
 //   * producer warp: the TMA loads.  The weights of the first stages are asked for
 //     before the quantisation kernel has finished (programmatic launch);
 //   * MMA warp: one thread;
@@ -27,6 +26,9 @@
 //     factors into tensor memory (layout as in ffn_mxfp4act.cu), then drain the
 //     accumulator.  For up to 16 tokens whose CTAs all run at once they also encode
 //     the stage's part of x themselves (FUSED): one launch, 3 us less than two.
+// Bound by HBM for wide outputs (16 x 100003 x 4096: 42 us with the encoding, 224 MB, 5.3
+// TB/s), by its chain of latencies below (16 x 4096 x 4096: 8.4 us; 64 x 4096 x 4096: 10.8
+// with the encoding).
 // Every wait is bounded (see mbar_wait).
 #include <algorithm>
 #include <type_traits>
@@ -130,11 +132,12 @@ struct QuantArgs {
     int parts;           // warps that share a row of x
 };
 
-// One warp takes 256 values of a row at a time, eight per lane: every load and store is
-// coalesced; kQuantAhead such loads are in flight per lane.  Bound by HBM for long
-// prompts (2 bytes read and 17/32 written per value), by launch latency for short
-// ones.  The weights' scales (1/16 of their codes'
-// bytes) are laid out by further blocks of the same launch: two stages of a row per
+// One warp takes up to kQuantAhead times 256 values of a row, eight per lane: every load
+// and store is coalesced, all loads are in flight before the first value is used.  For long
+// prompts it reads 2 bytes and writes 17/32 a value: 8192 x 4096 in 14.4 us, 5.9 TB/s (20 us
+// when the magnitudes were taken value by value: the instructions bound it); for short
+// ones the launch is its time.  The weights' scales (1/16 of their codes' bytes) are laid
+// out for linear_pair_kernel by further blocks of the same launch: two stages of a row per
 // thread, neighbouring rows in neighbouring threads.
 constexpr int kQuantAhead = 4;
 
@@ -596,19 +599,26 @@ __global__ void __launch_bounds__(kStreamThreads, (StreamLayout<NT, FUSED>::kPer
 
 // ------------------------------------------------------ product, large batches
 
-// Long prompts are bound by the tensor cores (and by what feeds them), so tokens are
-// the MMA's M side in pairs of CTAs (cta_group::2: 256 tokens x TN weight rows,
-// each CTA loading its 128 tokens and half of the weight rows), persistent, in
-// an order that keeps a weight tile on neighbouring pairs (squarer groups of tiles
-// took the same time).  A stage (256 k) also brings
-// the scale bytes of its rows (sf_block), which four warps, one per tensor-memory lane
-// quadrant, write into tensor memory; letting the MMA thread copy them there
-// (tcgen05.cp, six copies a stage) held the products up by a third, also when issued a
-// stage ahead.  Eight epilogue warps read the accumulator into registers,
-// free it, and store through shared memory in full rows of 64 or 128 bytes.
-// TN = 256 halves what crosses L2 -> shared memory per product (the bound of
-// this shape: 8 KB a CTA per 256 x 256 x 64 MMA, 64 bytes a clock) but has room for one
-// accumulator only; TN = 128 has two, and twice the tiles.
+// Long prompts are bound by the tensor cores and by the shared memory that feeds them,
+// so tokens are the MMA's M side in pairs of CTAs (cta_group::2: 256 tokens x TN weight
+// rows, each CTA loading its 128 tokens and half of the weight rows), persistent, in an
+// order that keeps a weight tile on neighbouring pairs (squarer groups of tiles took the
+// same time).  A stage (256 k) also brings the scale bytes of its rows (sf_block), which
+// four warps, one per tensor-memory lane quadrant, write into tensor memory; letting the
+// MMA thread copy them there (tcgen05.cp, six copies a stage) held the products up by a
+// third, also when issued a stage ahead; eight such warps changed nothing.
+// Eight epilogue warps read the accumulator into registers, free it, and store through
+// shared memory in full lines.
+//
+// An MMA of K = 64 takes about 122 clocks for TN = 256 and hardly fewer for 128 or 192,
+// so TN = 256 does most per clock, although tensor memory then has room for one
+// accumulator only and a tile waits about 800 clocks while the last one is read (192 with
+// two accumulators: 144 us where 256 took 118).  8192 x 8192 x 4096: 88 us, 6.2 PFLOP/s;
+// 9700 clocks for a tile's 64 MMAs (8000 without the loads into shared memory: each stage
+// writes 36 KB there and the MMAs read 32 KB, 128 bytes a clock at most), 800 between
+// tiles, 14 tiles for most pairs and 13 for the others.  Fewer stages (3 or 4 for 5) or
+// half of the loads changed little; output by TMA instead of stores cost 3%: its reads
+// come in a burst that the operands' loads wait for.
 struct PairArgs {
     const uint8_t* sfa;   // x's scale bytes: ceil(T / 256) * 2 rows of blocks
     const uint8_t* sfb;   // the weights': ceil(N / 256) * 2
@@ -1003,13 +1013,14 @@ cudaError_t launch_linear_mxfp4(const LinearMxfp4& p, void* workspace, cudaStrea
     cudaError_t err = p.x_f32 ? launch_quantize_rows<true>(q, s) : launch_quantize_rows<false>(q, s);
     if (err != cudaSuccess) return err;
     if (pairs) {
-        // half-width tiles where the full ones would leave pairs idle: they take 0.6 of the time
-        // (512 x 4096 x 4096, 32 or 64 tiles: 16.8 and 13.7 us; 1024 x 16384 x 4096, 256 or
-        // 512 tiles: 37.7 and 42.7)
+        // half-width tiles where full ones would leave pairs idle: they take three quarters of
+        // the time (turns of the pairs, half and full width, and us with the encoding: 512 x
+        // 4096 x 4096 1 and 1, 11.9 and 13.4; 1536 x 4096 x 4096 3 and 2, 23.2 and 22.2;
+        // 1024 x 16384 x 4096 7 and 4, 42.4 and 35.8)
         const long long mts = (p.T + 255) / 256, most = num_sms() / 2;
         const long long w256 = (mts * ((p.N + 255) / 256) + most - 1) / most, w128 = (mts * ((p.N + 127) / 128) + most - 1) / most;
-        return 3 * w128 < 5 * w256 ? launch_pair<128>(p, q.codes, q.scales, q.wsb, s)
-                                   : launch_pair<256>(p, q.codes, q.scales, q.wsb, s);
+        return 4 * w128 <= 5 * w256 ? launch_pair<128>(p, q.codes, q.scales, q.wsb, s)
+                                    : launch_pair<256>(p, q.codes, q.scales, q.wsb, s);
     }
     // the narrowest token tile that holds the batch
     if (p.T <= 16) return launch_stream<16, false>(p, q.codes, q.scales, q.pitch, s);

@@ -27,18 +27,18 @@ __device__ __forceinline__ float key_to_float(uint32_t k) {
     return __uint_as_float(u);
 }
 
-// Routes the logits load(0) .. load(E - 1) into ids / w (Kt entries each);
-// called by all 32 lanes of a warp.  shared_weight is the shared slot's weight.
-template <int VPL, typename Load>
-__device__ __forceinline__ void route_loaded(Load load, int E, int K, int with_shared,
-                                             int renormalize, float shared_weight, int32_t* ids,
-                                             float* w, int lane) {
+// Routes logits row l (E values) into ids / w (Kt entries each); called by all
+// 32 lanes of a warp.  shared_weight is the shared slot's weight.
+template <int VPL>
+__device__ __forceinline__ void route_token(const float* __restrict__ l, int E, int K,
+                                            int with_shared, int renormalize, float shared_weight,
+                                            int32_t* ids, float* w, int lane) {
     float v[VPL];
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + 32 * i;
-        v[i] = e < E ? load(e) : -INFINITY;
+        v[i] = e < E ? __ldg(l + e) : -INFINITY;
         m = fmaxf(m, v[i]);
     }
 #pragma unroll
@@ -120,15 +120,6 @@ __device__ __forceinline__ void route_loaded(Load load, int E, int K, int with_s
         ids[K] = E;
         w[K] = shared_weight;
     }
-}
-
-// The same for a row of logits that no kernel in flight writes.
-template <int VPL>
-__device__ __forceinline__ void route_token(const float* __restrict__ l, int E, int K,
-                                            int with_shared, int renormalize, float shared_weight,
-                                            int32_t* ids, float* w, int lane) {
-    route_loaded<VPL>([l](int e) { return __ldg(l + e); }, E, K, with_shared, renormalize, shared_weight,
-                      ids, w, lane);
 }
 
 }  // namespace moe
