@@ -231,72 +231,6 @@ __device__ __forceinline__ void store_out(const StreamArgs& a, int t, int n, flo
     }
 }
 
-// 32 rows (tokens t0 ..) x 32 columns (n0 ..) of fp32 staged in shared memory, row pitch
-// `pitch`, to the output: 16 bytes a lane in rows of 64 (bf16) or 128 bytes, or, where
-// rows or the right edge do not allow it, element by element.  All 32 lanes call it.
-__device__ __forceinline__ void store_block(const StreamArgs& a, bool vec, const float* stg, int pitch, int t0, int n0,
-                                            int lane) {
-    if (!vec || n0 + 32 > a.N) {
-        for (int r = 0; r < 32 && t0 + r < a.T; ++r)
-            if (n0 + lane < a.N) store_out(a, t0 + r, n0 + lane, stg[r * pitch + lane]);
-        return;
-    }
-    if (a.out_f32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7), t = t0 + r;
-            if (t >= a.T) break;
-            float4 v = *reinterpret_cast<const float4*>(stg + r * pitch + c);
-            if (a.residual) {
-                const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.residual) + (size_t)t * a.ldr + n0 + c);
-                v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
-            }
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + (size_t)t * a.ldo + n0 + c) = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2), c = 8 * (lane & 3), t = t0 + r;
-            if (t >= a.T) break;
-            const float4 u = *reinterpret_cast<const float4*>(stg + r * pitch + c);
-            const float4 w = *reinterpret_cast<const float4*>(stg + r * pitch + c + 4);
-            float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-            if (a.residual) {
-                const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.residual) + (size_t)t * a.ldr + n0 + c);
-                const uint32_t qq[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[2 * k] += bf16_lo(qq[k]), v[2 * k + 1] += bf16_hi(qq[k]);
-            }
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] = (uint32_t)f32_to_bf16_bits(v[2 * k]) | (uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16;
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (size_t)t * a.ldo + n0 + c) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-    }
-}
-
-// 32 rows x 64 columns of bf16 staged in shared memory in rows of 128 bytes, 16-byte part q of
-// row r at q ^ (r & 7), to the output in full lines.  All 32 lanes call it.
-__device__ __forceinline__ void store_rows_bf16(const StreamArgs& a, const uint8_t* stg, int t0, int n0, int lane) {
-    const int q = lane & 7, n = n0 + 8 * q;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3), t = t0 + r;
-        if (t >= a.T) break;
-        const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((q ^ (r & 7)) << 4));
-        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + (size_t)t * a.ldo + n;
-        if (n + 8 <= a.N) {
-            *reinterpret_cast<uint4*>(o) = v;
-        } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (n + k < a.N) o[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-        }
-    }
-}
-
 StreamArgs stream_args(const LinearMxfp4& p) {
     StreamArgs a = {};
     a.scales = p.scales;
@@ -623,7 +557,6 @@ struct PairArgs {
     const uint8_t* sfa;   // x's scale bytes: ceil(T / 256) * 2 rows of blocks
     const uint8_t* sfb;   // the weights': ceil(N / 256) * 2
     StreamArgs o;         // output, residual, sizes
-    int vec;              // 16-byte stores (and residual loads)
 };
 
 // Four warpgroups: the scale warps; the producer, the MMA and two idle warps; two of epilogue
@@ -642,8 +575,8 @@ struct PairLayout {
     static constexpr int kSf = kABytes + kBBytes;
     static constexpr int kStage = kSf + kSfaBytes + kSfbBytes;
     static_assert(kStage % 1024 == 0, "alignment");
-    static constexpr int kStgRow = 36;                        // fp32 per staged row, padded
-    static constexpr int kStgWarp = 32 * kStgRow * 4;
+    // per epilogue warp: 32 rows x 128 bytes, 16-byte part q of row r at q ^ (r & 7)
+    static constexpr int kStgWarp = 32 * 128;
     static constexpr int kFit = (232448 - 1024 - 256 - 8 * kStgWarp) / kStage;
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kStg = kStages * kStage;
@@ -657,7 +590,10 @@ struct PairLayout {
     static_assert(kSfCol0 + kStages * 32 <= 512, "tensor memory");
 };
 
-template <int TN>
+// ES: bytes of an output value; RES: a residual; VEC: the output's and the residual's rows
+// start on 16 bytes.  (One kernel with all the forms spilled the accumulator: 111 us where
+// these take 103.)
+template <int TN, int ES, bool RES, bool VEC>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const PairArgs a, const __grid_constant__ CUtensorMap x_map,
                        const __grid_constant__ CUtensorMap w_map) {
@@ -704,10 +640,48 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // -------------------------------------------------------- epilogue
         constexpr int kCols = TN / 2;  // columns per warp
         const int quad = warp & 3, half = (warp - kPairEpiWarp0) >> 2;
-        float* stg = reinterpret_cast<float*>(smem + L::kStg + (warp - kPairEpiWarp0) * L::kStgWarp);
+        uint8_t* stg = smem + L::kStg + (warp - kPairEpiWarp0) * L::kStgWarp;
+        auto part = [&](int r, int q) { return stg + r * 128 + ((q ^ (r & 7)) << 4); };
+        // The columns go through shared memory 128 bytes a row at a time (so many passes a
+        // tile), out in full lines; bf16 is rounded before it is staged (half the traffic in
+        // shared memory, which the MMA's operands share).  The residual (RES) comes in the
+        // same way, its loads one pass ahead, asked for while the tile before is multiplied:
+        // 8192 x 8192 x 4096 with one takes 118 us in bf16 and 160 in fp32 (102 and 118
+        // without; 174 and 335 when its loads stood between the accumulator and the stores).
+        // Without VEC the output is written element by element, from fp32 (and store_out
+        // adds the residual).
+        constexpr int kBox = 128 / ES;  // columns a pass
+        const int lr = lane >> 3, lc = (lane & 7) * (16 / ES);  // coalesced: rows lr + 4 i, columns lc ..
+        uint4 rr[RES ? 8 : 1];
+        auto load = [&](int t, int n) {
+#pragma unroll
+            for (int i = 0; i < (RES ? 8 : 0); ++i) {
+                rr[i] = make_uint4(0, 0, 0, 0);
+                const int row = t + lr + 4 * i, col = n + lc;
+                if (row >= T || col >= N) continue;
+                const char* src = reinterpret_cast<const char*>(a.o.residual) + ((size_t)row * a.o.ldr + col) * ES;
+                if (col + 16 / ES <= N) {
+                    rr[i] = *reinterpret_cast<const uint4*>(src);
+                } else {
+                    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < 16 / ES; ++k)
+                        if (col + k < N) {
+                            if (ES == 4)
+                                w[k & 3] = reinterpret_cast<const uint32_t*>(src)[k];
+                            else
+                                w[k >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(src)[k] << (16 * (k & 1));
+                        }
+                    rr[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        };
+        auto t_of = [&](int tile) { return tile % mts * 256 + rank * 128 + quad * 32; };
+        auto n_of = [&](int tile) { return tile / mts * TN + half * kCols; };
+        if (pair < tiles) load(t_of(pair), n_of(pair));
         uint32_t it = 0;
         for (int tile = pair; tile < tiles; tile += pairs, ++it) {
-            const int nt = tile / mts, mt = tile - nt * mts;
+            const int t = t_of(tile), n = n_of(tile);
             const uint32_t b = it % kAccBufs;
             if (!mbar_wait_warp(&acc_full[b], (it / kAccBufs) & 1)) break;
             tc_fence_after();
@@ -724,42 +698,59 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 else
                     mbar_arrive_remote(&acc_free[b], 0);
             }
-            const int t0 = mt * 256 + rank * 128 + quad * 32, n0 = nt * TN + half * kCols;
-            if (t0 >= T) continue;
-            if (a.vec && !a.o.out_f32 && !a.o.residual) {
-                // rounded before staging: half the shared-memory traffic, which the MMA's
-                // operands share
-                uint8_t* row = reinterpret_cast<uint8_t*>(stg) + lane * 128;
 #pragma unroll
-                for (int ch = 0; ch < kCols / 64; ++ch) {
-                    if (n0 + ch * 64 >= N) break;
+            for (int c0 = 0; c0 < kCols; c0 += kBox) {
+                if (t >= T || n + c0 >= N) break;
+                if (RES) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = ch * 64 + 8 * q + 2 * i;
-                            o[i] = f32x2_to_bf16x2_bits(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                        }
-                        *reinterpret_cast<uint4*>(row + ((q ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                    for (int i = 0; i < (RES ? 8 : 0); ++i) *reinterpret_cast<uint4*>(part(lr + 4 * i, lane & 7)) = rr[i];
                     __syncwarp();
-                    store_rows_bf16(a.o, reinterpret_cast<const uint8_t*>(stg), t0, n0 + ch * 64, lane);
-                    __syncwarp();
+                    if (c0 + kBox < kCols) load(t, n + c0 + kBox);
                 }
-                continue;
-            }
 #pragma unroll
-            for (int ch = 0; ch < kCols / 32; ++ch) {
-                if (n0 + ch * 32 >= N) break;
+                for (int q = 0; q < 8; ++q) {
+                    uint4* d = reinterpret_cast<uint4*>(part(lane, q));
+                    uint32_t o[4], p[4] = {0, 0, 0, 0};
+                    if (RES) {
+                        const uint4 x = *d;
+                        p[0] = x.x, p[1] = x.y, p[2] = x.z, p[3] = x.w;
+                    }
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<uint4*>(stg + lane * L::kStgRow + 4 * q) =
-                        make_uint4(v[ch * 32 + 4 * q], v[ch * 32 + 4 * q + 1], v[ch * 32 + 4 * q + 2], v[ch * 32 + 4 * q + 3]);
+                    for (int i = 0; i < 4; ++i) {
+                        if (ES == 4) {
+                            const float x = __uint_as_float(v[c0 + 4 * q + i]);
+                            o[i] = __float_as_uint(RES ? x + __uint_as_float(p[i]) : x);
+                        } else {
+                            float lo = __uint_as_float(v[c0 + 8 * q + 2 * i]), hi = __uint_as_float(v[c0 + 8 * q + 2 * i + 1]);
+                            if (RES) lo += bf16_lo(p[i]), hi += bf16_hi(p[i]);
+                            o[i] = f32x2_to_bf16x2_bits(lo, hi);
+                        }
+                    }
+                    *d = make_uint4(o[0], o[1], o[2], o[3]);
+                }
                 __syncwarp();
-                store_block(a.o, a.vec != 0, stg, L::kStgRow, t0, n0 + ch * 32, lane);
+                if (VEC) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = t + lr + 4 * i, col = n + c0 + lc;
+                        if (row >= T) break;
+                        const uint8_t* src = part(lr + 4 * i, lane & 7);
+                        char* dst = reinterpret_cast<char*>(a.o.out) + ((size_t)row * a.o.ldo + col) * ES;
+                        if (col + 16 / ES <= N)
+                            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+                        else
+                            for (int k = 0; k < (N - col) * ES; k += 2)
+                                *reinterpret_cast<uint16_t*>(dst + k) = *reinterpret_cast<const uint16_t*>(src + k);
+                    }
+                } else {
+                    for (int r = 0; r < 32 && t + r < T; ++r)
+                        if (n + c0 + lane < N)
+                            store_out(a.o, t + r, n + c0 + lane,
+                                      reinterpret_cast<const float*>(part(r, lane >> 2))[lane & 3]);
+                }
                 __syncwarp();
             }
+            if (tile + pairs < tiles) load(t_of(tile + pairs), n_of(tile + pairs));
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegs));
@@ -887,11 +878,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     pdl_end();
 }
 
-template <int TN>
-cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* sfa, const uint8_t* sfb,
-                        cudaStream_t s) {
+template <int TN, int ES, bool RES, bool VEC>
+cudaError_t launch_pair_as(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* sfa, const uint8_t* sfb,
+                           cudaStream_t s) {
+    const auto kernel = linear_pair_kernel<TN, ES, RES, VEC>;
     const size_t smem = PairLayout<TN>::kTotal;
-    cudaError_t err = ensure_dynamic_smem((const void*)linear_pair_kernel<TN>, smem);
+    cudaError_t err = ensure_dynamic_smem((const void*)kernel, smem);
     if (err != cudaSuccess) return err;
     CUtensorMap w_map, x_map;
     err = encode_codes_map(&w_map, p.codes, p.K / 2, (uint64_t)p.N, kRowBytes, TN / 2);
@@ -899,19 +891,30 @@ cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8
     err = encode_codes_map(&x_map, xcodes, p.K / 2, (uint64_t)p.T, kRowBytes, kMRows);
     if (err != cudaSuccess) return err;
     int pairs = 0;
-    err = max_active_pairs((const void*)linear_pair_kernel<TN>, kPairThreads, smem, &pairs);
+    err = max_active_pairs((const void*)kernel, kPairThreads, smem, &pairs);
     if (err != cudaSuccess) return err;
     if (pairs < 1) return cudaErrorNotSupported;
     PairArgs a;
     a.sfa = sfa;
     a.sfb = sfb;
     a.o = stream_args(p);
-    const size_t es = p.out_f32 ? 4 : 2;
-    a.vec = (uintptr_t)p.out % 16 == 0 && p.ldo * es % 16 == 0 &&
-            (!p.residual || ((uintptr_t)p.residual % 16 == 0 && p.ldr * es % 16 == 0));
     const long long tiles = (long long)((p.T + 255) / 256) * ((p.N + TN - 1) / TN);
     const int grid = 2 * (int)std::min<long long>(tiles, pairs);
-    return launch_pdl_cluster(linear_pair_kernel<TN>, dim3((unsigned)grid), dim3(kPairThreads), smem, s, 2u, a, x_map, w_map);
+    return launch_pdl_cluster(kernel, dim3((unsigned)grid), dim3(kPairThreads), smem, s, 2u, a, x_map, w_map);
+}
+
+template <int TN>
+cudaError_t launch_pair(const LinearMxfp4& p, const uint8_t* xcodes, const uint8_t* sfa, const uint8_t* sfb,
+                        cudaStream_t s) {
+    const long long es = p.out_f32 ? 4 : 2;
+    const bool vec = (uintptr_t)p.out % 16 == 0 && p.ldo * es % 16 == 0 &&
+                     (!p.residual || ((uintptr_t)p.residual % 16 == 0 && p.ldr * es % 16 == 0));
+    if (!vec) return launch_pair_as<TN, 4, false, false>(p, xcodes, sfa, sfb, s);
+    if (p.out_f32)
+        return p.residual ? launch_pair_as<TN, 4, true, true>(p, xcodes, sfa, sfb, s)
+                          : launch_pair_as<TN, 4, false, true>(p, xcodes, sfa, sfb, s);
+    return p.residual ? launch_pair_as<TN, 2, true, true>(p, xcodes, sfa, sfb, s)
+                      : launch_pair_as<TN, 2, false, true>(p, xcodes, sfa, sfb, s);
 }
 
 int row_tiles(int N) { return (N + kMRows - 1) / kMRows; }

@@ -107,6 +107,23 @@ def test_types_strides_and_residual(m, T, N, K, xt, ot, pad):
     assert (wide[:, N:] == 123.0).all()
 
 
+@pytest.mark.parametrize("T,N,K", [(65, 129, 96), (130, 777, 512), (300, 1003, 288), (800, 518, 1024)])
+@pytest.mark.parametrize("ot", ["bf16", "f32"])
+@pytest.mark.parametrize("with_res", [False, True])
+def test_rows_on_16_bytes_that_end_inside_one(m, T, N, K, ot, with_res):
+    """out and residual as aligned slices of aligned rows whose width is no multiple of 16 bytes."""
+    x, codes, scales = make(T, N, K, seed=T + K)
+    width = (N + 15) // 8 * 8 + 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    res = torch.randn((T, width), device="cuda", generator=g).to(TYPES[ot])[:, :N] if with_res else None
+    wide = torch.full((T, width), 123.0, dtype=TYPES[ot], device="cuda")
+    out = wide[:, :N]
+    assert m.moe_linear_mxfp4act(x, codes, scales, residual=res, out=out) is out
+    check(out, x, codes, scales, res)
+    assert (wide[:, N:] == 123.0).all()
+
+
 @pytest.mark.parametrize("T,N,K", [(3, 300, 512), (600, 512, 512), (1300, 520, 256)])
 def test_residual_may_be_the_output(m, T, N, K):
     x, codes, scales = make(T, N, K, seed=8)
