@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kStreamThreads, (StreamLayout<NT, FUSED>::kPer
 // 9700 clocks for a tile's 64 MMAs (8000 without the loads into shared memory: each stage
 // writes 36 KB there and the MMAs read 32 KB, 128 bytes a clock at most), 800 between
 // tiles, 14 tiles for most pairs and 13 for the others.  Fewer stages (3 or 4 for 5) or
-// half of the loads changed little; output by TMA instead of stores cost 3%: its reads
+// half of the loads changed little; output by TMA instead of stores cost 8%: its reads
 // come in a burst that the operands' loads wait for.
 struct PairArgs {
     const uint8_t* sfa;   // x's scale bytes: ceil(T / 256) * 2 rows of blocks
