@@ -159,9 +159,7 @@ __device__ __forceinline__ bool grid_wait(const uint32_t* p, uint32_t n) {
     }
 }
 
-__device__ __forceinline__ void consumers_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-}
+__device__ __forceinline__ void consumers_sync() { barrier_sync(1, kConsumers); }
 
 // v / d for v < 2^20 and d < 2^12, m = div_magic(d)
 __host__ __device__ __forceinline__ uint32_t div_magic(uint32_t d) { return d > 1 ? 0xFFFFFFFFu / d + 1u : 0u; }
@@ -485,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducerWarp) {
         // the router's further k, where all of it does not fit at once
         for (int k0 = a.router_k; k0 < H; k0 += a.router_k) {
-            asm volatile("bar.sync 3, %0;" ::"n"(kConsumers + 32) : "memory");
+            barrier_sync(3, kConsumers + 32);
             load_router(k0);
         }
         // whole stages of the shared expert's units need no routing (the ring is free once
         // the router has read it)
-        asm volatile("bar.sync 3, %0;" ::"n"(kConsumers + 32) : "memory");
+        barrier_sync(3, kConsumers + 32);
         const int stages = NC == 1 ? nsh / ups : nsh * NC;
         for (; (int)gs < min(stages, kEarlyStages); ++gs) issue_gate_up(gs, (int)gs, false);
     } else if (warp < kConsumerWarps) {
@@ -505,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int kg = min(a.router_k, H - k0) / 32;
             if (u) {  // the last piece has been read: the next may take its place
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                asm volatile("bar.arrive 3, %0;" ::"n"(kConsumers + 32) : "memory");
+                barrier_arrive(3, kConsumers + 32);
             }
             router_ok = router_ok && mbar_wait_warp(router_full, u & 1);
             if (!router_ok) continue;
@@ -555,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = (l >> 2) + (q & 2 ? 8 : 0), t = 8 * (tid >> 7) + 2 * (l & 3) + (q & 1);
             if (row < rows && t < T) a.logits[(size_t)t * (a.E + 1) + row0 + row] = v;
         }
-        asm volatile("bar.arrive 3, %0;" ::"n"(kConsumers + 32) : "memory");
+        barrier_arrive(3, kConsumers + 32);
         // what gate_up raises starts at zero
         for (int i = b * kConsumers + tid; i < T * Kt; i += G * kConsumers) a.hmax[i] = 0u;
         consumers_sync();

@@ -165,12 +165,31 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, ok) != 0;
 }
 
+// Named barriers and cluster barriers are aligned instructions: the lanes of a
+// warp have to execute one together, and arriving apart is undefined.  Roles that
+// run in one lane (producers, MMA issuers) bring the others here much earlier, so
+// each helper brings the warp together first instead of relying on where the
+// compiler lets it reconverge.
+
+// The `nthreads` threads (whole warps) that meet at named barrier `id`.
+__device__ __forceinline__ void barrier_sync(int id, int nthreads) {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// The same for warps that only announce themselves and do not wait.
+__device__ __forceinline__ void barrier_arrive(int id, int nthreads) {
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // `ok` reduced with AND over the `nthreads` threads (whole warps) that meet
 // at named barrier `id`; every one of them must call it.  Threads that then
 // synchronise at that barrier again act on the same outcome, so none is left
 // waiting there for threads that stopped.
 __device__ __forceinline__ bool all_at_barrier(bool ok, int id, int nthreads) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
@@ -194,6 +213,7 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 // shared-memory writes (barrier inits among them) before the other CTAs'
 // later accesses.
 __device__ __forceinline__ void cluster_sync_all() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
