@@ -7,6 +7,7 @@ there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -50,6 +51,7 @@ MOE_ROUTE_PERMUTE_FUSED_MAX_T = 32
 
 _lock = threading.Lock()
 _lib = None
+_as_is = contextlib.nullcontext()
 
 
 class MoeError(RuntimeError):
@@ -179,6 +181,15 @@ def _stream(stream):
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(stream):
+    """Makes `stream` current for what a call allocates itself: fills then come before the call's
+    kernels, and memory that is freed goes to work that comes after them."""
+    if stream is None:
+        return _as_is
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def _dev(t, dtype_name: str):
@@ -615,16 +626,17 @@ def moe_layer_few(x, w_router, w13, s13, w2, s2, K: int, with_shared: bool = Tru
     if w_shared_gate is not None:
         _dev(w_shared_gate, "w_shared_gate")
         assert w_shared_gate.dtype == bf16 and w_shared_gate.shape == (H,)
-    if out is None:
-        out = torch.empty_like(x)
-    elif not (out.is_cuda and out.is_contiguous() and out.dtype == bf16 and out.shape == x.shape):
+    if out is not None and not (out.is_cuda and out.is_contiguous() and out.dtype == bf16 and out.shape == x.shape):
         raise ValueError("out must be a contiguous CUDA bfloat16 tensor like x")
-    if topk_ids is None:
-        topk_ids = torch.empty((T, K + shared), dtype=torch.int32, device=x.device)
-    if topk_w is None:
-        topk_w = torch.empty((T, K + shared), dtype=torch.float32, device=x.device)
-    if workspace is None:
-        workspace = alloc_workspace_few(T, H, I, E, K, with_shared, x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(x)
+        if topk_ids is None:
+            topk_ids = torch.empty((T, K + shared), dtype=torch.int32, device=x.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, K + shared), dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = alloc_workspace_few(T, H, I, E, K, with_shared, x.device)
     for t, dt in ((topk_ids, torch.int32), (topk_w, torch.float32)):
         assert t.is_cuda and t.is_contiguous() and t.dtype == dt and t.numel() == T * (K + shared)
     status = (_lib or load()).moe_layer_few(
@@ -681,7 +693,8 @@ def moe_linear_mxfp4act(x, codes, scales, residual=None, out=None, out_dtype=Non
     assert codes.dtype == torch.uint8 and scales.dtype == torch.uint8, "weights are uint8"
     if out is None:
         out_dtype = out_dtype or bf16
-        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+        with _on(stream):
+            out = torch.empty((T, N), dtype=out_dtype, device=x.device)
         ldo = N
     else:
         assert out.shape == (T, N) and out_dtype in (None, out.dtype), "out must be [T, N]"
@@ -695,7 +708,8 @@ def moe_linear_mxfp4act(x, codes, scales, residual=None, out=None, out_dtype=Non
         assert residual.shape == (T, N) and residual.dtype == out_dtype, "residual must match out"
         res, ldr = residual.data_ptr(), _row_stride(residual, T, N, "residual")
     if workspace is None:
-        workspace = alloc_workspace_linear(T, N, K, x.device)
+        with _on(stream):
+            workspace = alloc_workspace_linear(T, N, K, x.device)
     status = (_lib or load()).moe_linear_mxfp4act(
         x.data_ptr(), MOE_DTYPE_F32 if xt == f32 else MOE_DTYPE_BF16, _row_stride(x, T, K, "x"),
         codes.data_ptr(), scales.data_ptr(), res, ldr, out.data_ptr(),

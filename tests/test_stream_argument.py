@@ -1,0 +1,78 @@
+"""What a call allocates for itself belongs to the stream that it runs on.  CPU only: the library and
+the stream switch are stand-ins, the tensors live on the host and only say that they are on a GPU."""
+import contextlib
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on a GPU."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """libmoe with a library whose calls do nothing, and the list of (allocator, stream that was
+    current) of every allocation."""
+    from mxfp4_mixture_experts_softmax_gb300 import libmoe
+    real = libmoe.load()
+    current, made = [None], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, current[0] = current[0], s
+        yield
+        current[0] = before
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for name in ("empty", "zeros", "empty_like", "full"):
+        def allocate(*args, _name=name, _real=getattr(torch, name), **kw):
+            made.append((_name, current[0]))
+            kw.pop("device", None)
+            return gpu(_real(*args, **kw))
+        monkeypatch.setattr(torch, name, allocate)
+
+    class Library:
+        def __getattr__(self, name):
+            # sizes are asked of the library itself, everything else would launch
+            return getattr(real, name) if name.endswith(("_size", "_capacity", "_max_tiles")) else lambda *a: 0
+    monkeypatch.setattr(libmoe, "_lib", Library())
+    return libmoe, made
+
+
+SIDE = types.SimpleNamespace(cuda_stream=0x1234)
+
+
+def rand(*shape, dtype=torch.bfloat16):
+    return gpu(torch.zeros(shape).to(dtype))
+
+
+def few(E=8, T=2, H=64, I=32):
+    u8 = torch.uint8
+    return dict(x=rand(T, H), w_router=rand(E, H), w13=rand(E + 1, 2 * I, H // 2, dtype=u8),
+                s13=rand(E + 1, 2 * I, H // 32, dtype=u8), w2=rand(E + 1, H, I // 2, dtype=u8),
+                s2=rand(E + 1, H, I // 32, dtype=u8), K=2)
+
+
+def linear(T=2, N=16, K=64):
+    return dict(x=rand(T, K), codes=rand(N, K // 2, dtype=torch.uint8), scales=rand(N, K // 32, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("name,args,allocations", [("moe_layer_few", few, 4), ("moe_linear_mxfp4act", linear, 2)])
+def test_the_calls_own_buffers(recorded, name, args, allocations):
+    libmoe, made = recorded
+    args = args()
+    made.clear()
+    getattr(libmoe, name)(**args, stream=SIDE)
+    assert len(made) == allocations and all(s is SIDE for _, s in made), made
+    if name == "moe_layer_few":  # its workspace is zeroed in the kernel's stream too
+        assert ("zeros", SIDE) in made
