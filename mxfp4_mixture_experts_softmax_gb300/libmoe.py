@@ -198,16 +198,17 @@ def _dev(t, dtype_name: str):
     return t
 
 
-def _route_outputs(logits, K, with_shared, topk_ids, topk_w, shared_w):
+def _route_outputs(logits, K, with_shared, topk_ids, topk_w, shared_w, stream):
     import torch
     _dev(logits, "logits")
     assert logits.dtype == torch.float32
     T, E = logits.shape
     Kt = K + (1 if with_shared else 0)
-    if topk_ids is None:
-        topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=logits.device)
-    if topk_w is None:
-        topk_w = torch.empty((T, Kt), dtype=torch.float32, device=logits.device)
+    with _on(stream):
+        if topk_ids is None:
+            topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=logits.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, Kt), dtype=torch.float32, device=logits.device)
     if shared_w is not None:
         _dev(shared_w, "shared_w")
         assert shared_w.dtype == torch.float32 and shared_w.shape == (T,)
@@ -218,7 +219,7 @@ def moe_route(logits, K: int, with_shared: bool = True, renormalize: bool = True
               topk_ids=None, topk_w=None, stream=None, shared_w=None):
     """fp32 logits [T, E] -> (int32 ids [T, Kt], fp32 weights [T, Kt]).  shared_w (fp32 [T],
     optional): per-token weight of the shared slot (moe_route_ex)."""
-    T, E, Kt, topk_ids, topk_w = _route_outputs(logits, K, with_shared, topk_ids, topk_w, shared_w)
+    T, E, Kt, topk_ids, topk_w = _route_outputs(logits, K, with_shared, topk_ids, topk_w, shared_w, stream)
     if shared_w is None:
         _check(load().moe_route(_ptr(logits), T, E, K, int(with_shared), int(renormalize),
                                 _ptr(topk_ids), _ptr(topk_w), _stream(stream)), "moe_route")
@@ -234,10 +235,11 @@ def moe_route_permute(logits, K: int, tile_m: int, with_shared: bool = True,
                       perm: dict | None = None, shared_w=None, stream=None):
     """moe_route_ex + moe_permute in one call (one launch for small batches):
     returns (ids, weights, perm dict as from moe_permute)."""
-    T, E, Kt, topk_ids, topk_w = _route_outputs(logits, K, with_shared, topk_ids, topk_w, shared_w)
+    T, E, Kt, topk_ids, topk_w = _route_outputs(logits, K, with_shared, topk_ids, topk_w, shared_w, stream)
     Et = E + (1 if with_shared else 0)
     if perm is None:
-        perm = alloc_permute(T, Kt, Et, tile_m, logits.device)
+        with _on(stream):
+            perm = alloc_permute(T, Kt, Et, tile_m, logits.device)
     _check(load().moe_route_permute(_ptr(logits), _ptr(shared_w), T, E, K, int(with_shared),
                                     int(renormalize), tile_m, _ptr(topk_ids), _ptr(topk_w),
                                     _ptr(perm["sorted_pairs"]), _ptr(perm["expert_offsets"]),
@@ -272,7 +274,8 @@ def moe_permute(topk_ids, Et: int, tile_m: int, out: dict | None = None, stream=
     T, Kt = topk_ids.shape
     _dev(topk_ids, "topk_ids")
     if out is None:
-        out = alloc_permute(T, Kt, Et, tile_m, topk_ids.device)
+        with _on(stream):
+            out = alloc_permute(T, Kt, Et, tile_m, topk_ids.device)
     _check(load().moe_permute(_ptr(topk_ids), T, Kt, Et, tile_m, _ptr(out["sorted_pairs"]),
                               _ptr(out["expert_offsets"]), _ptr(out["inv_pairs"]),
                               _ptr(out["tile_expert"]), _ptr(out["num_tiles"]), _stream(stream)),
@@ -308,10 +311,11 @@ def moe_ffn(x, w13, s13, w2, s2, topk_w, perm: dict, out=None, workspace=None,
     Kt, tile_m = perm["Kt"], perm["tile_m"]
     for t in (x, w13, s13, w2, s2, topk_w):
         _dev(t, "ffn input")
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    if workspace is None:
-        workspace = alloc_workspace(T, H, I, Et, Kt, tile_m, x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        if workspace is None:
+            workspace = alloc_workspace(T, H, I, Et, Kt, tile_m, x.device)
     _check(load().moe_ffn_path(_ptr(x), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(topk_w),
                                _ptr(perm["sorted_pairs"]), _ptr(perm["expert_offsets"]),
                                _ptr(perm["inv_pairs"]), _ptr(perm["tile_expert"]),
@@ -356,7 +360,8 @@ def moe_selftest_wait_split(limit_us: int = 2000, stream=None):
     together (include/moe.h).  Returns the device tensor of the two warps'
     outcomes (int32 [2]; 0 = stopped)."""
     import torch
-    out = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    with _on(stream):
+        out = torch.full((2,), -1, dtype=torch.int32, device="cuda")
     _check(load().moe_selftest_wait_split(int(limit_us), _ptr(out), _stream(stream)),
            "moe_selftest_wait_split")
     return out
@@ -370,7 +375,8 @@ def moe_ffn_noalloc(x, w13, s13, w2, s2, topk_w, perm: dict, out=None, stream=No
     T, H = x.shape
     Et, twoI, _ = w13.shape
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        with _on(stream):
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _check(load().moe_ffn_noalloc(_ptr(x), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(topk_w),
                                   _ptr(perm["sorted_pairs"]), _ptr(perm["expert_offsets"]),
                                   _ptr(perm["inv_pairs"]), _ptr(perm["tile_expert"]),
@@ -441,8 +447,9 @@ def moe_layer(logits, x, w13, s13, w2, s2, K: int, with_shared: bool = True,
     T, E = logits.shape
     Et = w13.shape[0]
     if bufs is None:
-        bufs = alloc_layer(T, E, K, with_shared, x.shape[1], w13.shape[1] // 2, Et, tile_m,
-                           x.device)
+        with _on(stream):
+            bufs = alloc_layer(T, E, K, with_shared, x.shape[1], w13.shape[1] // 2, Et, tile_m,
+                               x.device)
     if Et != E + (1 if with_shared else 0):
         raise ValueError("weights must hold E experts plus the shared one when with_shared")
     ids, w, perm = moe_route_permute(logits, K, tile_m, with_shared, renormalize, bufs["topk_ids"],
@@ -470,10 +477,11 @@ def moe_ffn_dense_shared(x, w13, s13, w2, s2, topk_w, perm: dict, w13s, s13s, w2
     Is = w13s.shape[1] // 2
     Kt, tm = perm["Kt"], perm["tile_m"]
     n = int(load().moe_ffn_dense_shared_workspace_size(T, H, twoI // 2, Et, Kt, Is, tm))
-    if workspace is None:
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _check(load().moe_ffn_dense_shared(
         _ptr(x), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(topk_w),
         _ptr(perm["sorted_pairs"]), _ptr(perm["expert_offsets"]), _ptr(perm["inv_pairs"]),
@@ -492,10 +500,11 @@ def moe_split_e4m3x2(x, stream=None):
     import torch
     _dev(x, "x")
     rows, cols = x.shape
-    q_hi = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    q_lo = torch.empty_like(q_hi)
-    s_hi = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-    s_lo = torch.empty_like(s_hi)
+    with _on(stream):
+        q_hi = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        q_lo = torch.empty_like(q_hi)
+        s_hi = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+        s_lo = torch.empty_like(s_hi)
     _check(load().moe_split_e4m3x2(_ptr(x), rows, cols, _ptr(q_hi), _ptr(q_lo), _ptr(s_hi), _ptr(s_lo),
                                    _stream(stream)), "moe_split_e4m3x2")
     return q_hi, q_lo, s_hi, s_lo
@@ -507,10 +516,11 @@ def moe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
     import torch
     _dev(x, "x")
     rows, cols = x.shape
-    if codes is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-    if scales is None:
-        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+    with _on(stream):
+        if codes is None:
+            codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
     _check(load().moe_quantize_mxfp4(_ptr(x), rows, cols, _ptr(codes), _ptr(scales),
                                      _stream(stream)), "moe_quantize_mxfp4")
     return codes, scales
@@ -536,10 +546,11 @@ def moe_ffn_mxfp4act(x, w13, s13, w2, s2, topk_w, perm: dict, out=None, workspac
     Kt, tile_m = perm["Kt"], perm["tile_m"]
     for t in (x, w13, s13, w2, s2, topk_w):
         _dev(t, "ffn input")
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    if workspace is None:
-        workspace = alloc_workspace_mxfp4act(T, H, twoI // 2, Et, Kt, tile_m, x.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        if workspace is None:
+            workspace = alloc_workspace_mxfp4act(T, H, twoI // 2, Et, Kt, tile_m, x.device)
     _check(load().moe_ffn_mxfp4act(_ptr(x), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(topk_w),
                                    _ptr(perm["sorted_pairs"]), _ptr(perm["expert_offsets"]),
                                    _ptr(perm["inv_pairs"]), _ptr(perm["tile_expert"]),

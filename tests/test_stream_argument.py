@@ -76,3 +76,40 @@ def test_the_calls_own_buffers(recorded, name, args, allocations):
     assert len(made) == allocations and all(s is SIDE for _, s in made), made
     if name == "moe_layer_few":  # its workspace is zeroed in the kernel's stream too
         assert ("zeros", SIDE) in made
+
+
+T, H, I, E, K = 2, 64, 32, 8, 2
+
+
+def layer():
+    f = few(E, T, H, I)
+    del f["w_router"]
+    return dict(f, logits=rand(T, E, dtype=torch.float32))
+
+
+def ffn(libmoe):
+    f = layer()
+    del f["logits"], f["K"]
+    return dict(f, topk_w=rand(T, K + 1, dtype=torch.float32), perm=libmoe.alloc_permute(T, K + 1, E + 1, 8))
+
+
+def dense(libmoe):
+    f = ffn(libmoe)
+    return dict(f, **{n + "s": f[n][0] for n in ("w13", "s13", "w2", "s2")})
+
+
+@pytest.mark.parametrize("name,args", [
+    ("moe_route", lambda m: dict(logits=rand(T, E, dtype=torch.float32), K=K)),
+    ("moe_route_permute", lambda m: dict(logits=rand(T, E, dtype=torch.float32), K=K, tile_m=8)),
+    ("moe_permute", lambda m: dict(topk_ids=rand(T, K, dtype=torch.int32), Et=E, tile_m=8)),
+    ("moe_ffn", ffn), ("moe_ffn_noalloc", ffn), ("moe_ffn_mxfp4act", ffn), ("moe_ffn_dense_shared", dense),
+    ("moe_layer", lambda m: layer()),
+    ("moe_split_e4m3x2", lambda m: dict(x=rand(T, H))), ("moe_quantize_mxfp4", lambda m: dict(x=rand(T, H))),
+    ("moe_selftest_wait_split", lambda m: {}),
+])
+def test_the_other_calls_own_buffers(recorded, name, args):
+    libmoe, made = recorded
+    args = args(libmoe)
+    made.clear()
+    getattr(libmoe, name)(**args, stream=SIDE)
+    assert made and all(s is SIDE for _, s in made), made
