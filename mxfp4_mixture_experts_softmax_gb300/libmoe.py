@@ -592,6 +592,12 @@ def mxfp4act_h_views(workspace, T: int, H: int, I: int, Et: int, Kt: int, tile_m
     return codes, scales
 
 
+def _workspace_bytes(workspace) -> int:
+    """The size of a workspace that the caller passed, in bytes whatever its type."""
+    assert workspace.is_cuda and workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
+    return workspace.numel() * workspace.element_size()
+
+
 # ------------------------------------------------- the layer for a few tokens
 
 def moe_layer_few_workspace_size(T: int, H: int, I: int, E: int, K: int, with_shared: bool) -> int:
@@ -610,7 +616,7 @@ def alloc_workspace_few(T: int, H: int, I: int, E: int, K: int, with_shared: boo
 def moe_layer_few_workspace_init(workspace, stream=None):
     """Zero the barrier counters of a workspace that did not come from alloc_workspace_few
     (include/moe.h)."""
-    _check(load().moe_layer_few_workspace_init(_ptr(workspace), workspace.numel(), _stream(stream)),
+    _check(load().moe_layer_few_workspace_init(_ptr(workspace), _workspace_bytes(workspace), _stream(stream)),
            "moe_layer_few_workspace_init")
 
 
@@ -654,7 +660,7 @@ def moe_layer_few(x, w_router, w13, s13, w2, s2, K: int, with_shared: bool = Tru
         x.data_ptr(), w_router.data_ptr(), None if w_shared_gate is None else w_shared_gate.data_ptr(),
         w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), T, H, I, E, K, shared,
         1 if renormalize else 0, out.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _raw_stream(stream, x))
+        _workspace_bytes(workspace), _raw_stream(stream, x))
     if status:
         raise MoeError(status, "moe_layer_few")
     return out, topk_ids, topk_w
@@ -725,7 +731,7 @@ def moe_linear_mxfp4act(x, codes, scales, residual=None, out=None, out_dtype=Non
         x.data_ptr(), MOE_DTYPE_F32 if xt == f32 else MOE_DTYPE_BF16, _row_stride(x, T, K, "x"),
         codes.data_ptr(), scales.data_ptr(), res, ldr, out.data_ptr(),
         MOE_DTYPE_F32 if out_dtype == f32 else MOE_DTYPE_BF16, ldo, T, N, K, workspace.data_ptr(),
-        workspace.numel(), _raw_stream(stream, x))
+        _workspace_bytes(workspace), _raw_stream(stream, x))
     if status:
         raise MoeError(status, "moe_linear_mxfp4act")
     return out
