@@ -36,9 +36,9 @@ class Linear:
 
 
 class Experts:
-    """Router and expert weights of one layer, a shared expert gated per token."""
+    """Router and expert weights of one layer, a shared expert gated per token; calls of up to `tokens`."""
 
-    def __init__(self, hidden, inner, experts, top_k, batch, gen):
+    def __init__(self, hidden, inner, experts, top_k, tokens, gen):
         import torch
         from mxfp4_mixture_experts_softmax_gb300 import libmoe
 
@@ -51,7 +51,8 @@ class Experts:
         self.gate = (torch.randn(hidden, device="cuda", generator=gen) / hidden ** 0.5).bfloat16()
         self.w13, self.s13 = weight(2 * inner, hidden)
         self.w2, self.s2 = weight(hidden, inner)
-        self.workspace = libmoe.alloc_workspace_few(batch, hidden, inner, experts, top_k, True)
+        # a short prompt takes the few-token layer as the decode steps do
+        self.workspace = libmoe.alloc_workspace_few(min(tokens, libmoe.MOE_LAYER_FEW_MAX_T), hidden, inner, experts, top_k)
 
     def __call__(self, x):
         import torch
@@ -72,7 +73,7 @@ class Decoder:
         most = max(batch, batch * prompt)
         self.embed = torch.randn((vocab, hidden), device="cuda", generator=gen).bfloat16()
         self.blocks = [(Linear(2 * hidden, hidden, most, gen), Linear(hidden, hidden, most, gen),
-                        Experts(hidden, inner, experts, top_k, batch, gen)) for _ in range(layers)]
+                        Experts(hidden, inner, experts, top_k, most, gen)) for _ in range(layers)]
         self.head = Linear(vocab, hidden, batch, gen)
         self.state = torch.zeros((layers, batch, hidden), device="cuda")  # mix's running means
         self.tokens = torch.zeros(batch, dtype=torch.long, device="cuda")
