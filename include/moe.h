@@ -549,9 +549,9 @@ moe_status_t moe_ffn_mxfp4act_h_offsets(int T, int H, int I, int Et, int Kt, int
  * out_t = bf16(sum of w_te W2[e] h_te), h_te = silu(W_gate[e] x_t) * (W_up[e] x_t).
  * As in moe_ffn's decode path x enters the products as f16 scaled per row by a
  * power of two (exact for elements at least 2^-29 of their row's largest).  h is
- * not rounded to bf16: it enters the down product as f16 scaled by powers of two
- * (11 significant bits; elements below 2^-25 of the largest |h| of their token and
- * expert are dropped).
+ * not rounded to bf16: it enters the down product as the sum of two f16 terms scaled by
+ * powers of two (22 significant bits, or 2^-38 of the largest |h| of its token and
+ * expert where that is coarser).
  * Sums are fp32, over k in blocks of 32 and then over a token's slots in
  * ascending order; results do not vary from run to run.  Weight scale bytes
  * 1..254.  A token whose x holds an infinity or a NaN gets NaN outputs; other

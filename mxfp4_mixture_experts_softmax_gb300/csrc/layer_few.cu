@@ -27,8 +27,10 @@
 //            registers until the entry changes, once or twice in a call.  x
 //            enters as f16 rows scaled by a power of two, as in ffn_decode.cu
 //            (exact for elements within 2^29 of the row's largest).
-//   down     an item is 16 output rows of one entry, one slot per 256 of I; each
-//            CTA takes a contiguous range of the items, an entry's rows next to
+//   down     its own list has an entry per touched expert and 4 of its tokens: h takes
+//            part as two f16 terms, the high ones in columns 0 .. 3, what they leave in
+//            columns 4 .. 7.  An item is 16 output rows of one entry, one slot per 256
+//            of I; each CTA takes a contiguous range of the items, an entry's rows next to
 //            each other, so the h fragment too stays in registers.  y goes to the
 //            workspace in fp32 by (token, expert) pair; after a third barrier
 //            each CTA adds up its share of the outputs, a token's pairs in slot
@@ -45,10 +47,13 @@
 // at a time.  A warp turns its slot's scale bytes into fp32 factors once, through shared
 // memory (each of the four lanes that share a row would otherwise do it again: 130
 // of the 330 cycles that 16 warps take per slot and scheduler).
-// h passes between the phases as f16 with a power of two per 8 values (11
-// significant bits); the down product brings a pair's row to one power of two
-// (elements below 2^-14 of the row's largest keep fewer bits, those below 2^-25 of
-// it are dropped).  No result depends on timing.
+// h passes between the phases as the sum of two f16 terms, the nearest and the nearest of
+// what that leaves, with a power of two per 8 values (22 significant bits; one term would err
+// by 2.5e-4 of the result); the down product brings a pair's row to one power of two
+// (elements below 2^-15 of the row's largest keep fewer bits, down to 2^-38 of it).
+// The terms share the columns that 4 tokens leave free, so the products cost what they
+// did with one term; an expert with 5 to 8 tokens is multiplied twice instead (its weights
+// come from L2 the second time).  No result depends on timing.
 // Warps: 16 consumers, one producer (TMA), two epilogue warps, one per stage of a pair
 // (adding the consumers' partial sums over k, SwiGLU, stores).  Every wait
 // is bounded (mbar_wait, grid_wait).
@@ -73,7 +78,8 @@ constexpr int kCodeBytes = kConsumerWarps * kSlotBytes;    // a stage's codes
 constexpr int kScaleBytes = kConsumerWarps * 16 * 8;       // and scale bytes
 constexpr int kStageBytes = kCodeBytes + kScaleBytes;
 constexpr int kSmemLimit = 232448;
-constexpr int kMaxPairs = 528;  // (token, slot) pairs: 16 * 33; also the most list entries
+constexpr int kMaxPairs = 528;  // (token, slot) pairs: 16 * 33
+constexpr int kMaxEntries = 516;  // of either list: at most one per routed pair, 512, and the shared expert's 4
 constexpr int kMaxGrid = 256;
 
 struct FewArgs {
@@ -88,7 +94,7 @@ struct FewArgs {
     uint32_t* sync;          // [4] barrier counters, zero between calls
     float* logits;           // [T][E + 1]: column E the shared expert's gate
     uint32_t* hmax;          // [T * Kt] largest |h| of a pair, as bits
-    uint16_t* h;             // [T * Kt][I] f16, times 2^shift of its 8 values
+    uint16_t* h;             // [T * Kt][2 terms][I] f16, times 2^shift of their 8 values
     int8_t* hshift;          // [T * Kt][shift_pitch(I)], see shift_at
     float* y;                // [T * Kt][H] expert outputs by pair
     int T, H, I, E, K, shared, renorm;
@@ -109,10 +115,10 @@ struct FewMaps {
 // shared memory
 constexpr int kPartBytes = 2 * kConsumerWarps * 32 * 16;  // one buffer: the sums of a pair of stages
 constexpr int kFactorBytes = 2 * kConsumerWarps * 16 * 32;  // a slot's 16 x 8 factors per warp, two stages
-constexpr int kListBytes = kMaxPairs * (2 + 2 + 2 + 4 + 1) + 64 + 32;
+constexpr int kListBytes = kMaxPairs * (4 + 2 + 1) + kMaxEntries * (2 + 2 + 2 + 2) + 64 + 32;
 constexpr int kBarBytes = 192;
 constexpr int kStages = (kSmemLimit - 1024 - kBarBytes - kListBytes - 2 * kPartBytes - kFactorBytes) / kStageBytes;
-static_assert(kStages >= 4, "ring depth");
+static_assert(kStages >= 5, "ring depth");
 constexpr int kPart = kStages * kStageBytes;
 constexpr int kFactors = kPart + 2 * kPartBytes;
 constexpr int kList = kFactors + kFactorBytes;
@@ -124,8 +130,8 @@ static_assert((2 * kStages + 6) * 8 <= kBarBytes, "barriers");
 constexpr int kMask = kPart;                 // [1025] token masks by expert
 constexpr int kFirst = kMask + 1028 * 4;     // [1025] first pair by expert (16 bits)
 constexpr int kIds = kFirst + 1028 * 2;      // [16][33]
-constexpr int kSums = kIds + 16 * 33 * 4;    // [16][2]
-static_assert(kSums + 16 * 2 * 4 <= kFactors, "routing scratch");
+constexpr int kSums = kIds + 16 * 33 * 4;    // [16]
+static_assert(kSums + 16 * 4 <= kFactors, "routing scratch");
 constexpr int kLogitStages = 2;              // 64 KB: 16 tokens x 1024 experts
 constexpr int kEarlyStages = kStages - kLogitStages;  // loads before the routing is known
 
@@ -360,10 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* rscale = w_s + kMaxPairs;                                    // [16] factor undoing x's scaling
     int32_t* info = reinterpret_cast<int32_t*>(rscale + 16);            // [0] entries, [1] outcome of the first
                                                                         // barrier, [2] of the second, [3] of the
-                                                                        // third
+                                                                        // third, [4] down's entries
     uint16_t* list_e = reinterpret_cast<uint16_t*>(info + 8);           // an entry's expert
-    uint16_t* list_p = list_e + kMaxPairs;                              // its first pair << 4 | its tokens
-    uint16_t* pair_of = list_p + kMaxPairs;                             // [T][Kt] pair of a token's slot
+    uint16_t* list_p = list_e + kMaxEntries;                            // its first pair << 4 | its tokens
+    uint16_t* down_e = list_p + kMaxEntries;                            // the same for down's entries
+    uint16_t* down_p = down_e + kMaxEntries;
+    uint16_t* pair_of = down_p + kMaxEntries;                           // [T][Kt] pair of a token's slot
     uint8_t* pair_t = reinterpret_cast<uint8_t*>(pair_of + kMaxPairs);  // a pair's token
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBar);
     uint64_t* empty = full + kStages;
@@ -601,58 +609,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             consumers_sync();
-            // list: the shared expert first, then the touched routed ones by id;
-            // warp w orders experts 64 w .. 64 w + 63
-            int32_t* sums = reinterpret_cast<int32_t*>(smem + kSums);  // entries, pairs by warp
-            int ne[2], np[2];
-            uint32_t mk[2];
-            int ce = 0, cp = 0;
+            // lists: the shared expert first, then the touched routed ones by id;
+            // warp w orders experts 64 w .. 64 w + 63.  An expert's pairs, its entries of down
+            // and of gate_up are counted together, in 12, 10 and 10 bits (at most 528, 516, 516)
+            uint32_t* sums = reinterpret_cast<uint32_t*>(smem + kSums);  // by warp
+            auto counts = [](int n) { return (uint32_t)n | (uint32_t)((n + 3) / 4) << 12 | (uint32_t)((n + 7) / 8) << 22; };
+            uint32_t at[2], mk[2], run = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int e = 64 * warp + 32 * i + lane;
                 mk[i] = e < a.E ? mask[e] : 0u;
-                int n = __popc(mk[i]);
-                const uint32_t one = __ballot_sync(0xFFFFFFFFu, n > 0), two = __ballot_sync(0xFFFFFFFFu, n > 8);
-                const int own = n;
+                const uint32_t own = counts(__popc(mk[i]));
+                uint32_t v = own;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xFFFFFFFFu, n, o);
-                    if (lane >= o) n += v;
+                    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                    if (lane >= o) v += u;
                 }
-                ne[i] = ce + __popc(one & lanemask_lt()) + __popc(two & lanemask_lt());
-                np[i] = cp + n - own;
-                ce += __popc(one) + __popc(two);
-                cp += __shfl_sync(0xFFFFFFFFu, n, 31);
+                at[i] = run + v - own;
+                run += __shfl_sync(0xFFFFFFFFu, v, 31);
             }
-            if (lane == 0) {
-                sums[2 * warp] = ce;
-                sums[2 * warp + 1] = cp;
-            }
+            if (lane == 0) sums[warp] = run;
             consumers_sync();
-            int be = a.shared ? (T + 7) / 8 : 0, bp = a.shared ? T : 0, te = be;
+            uint32_t before = a.shared ? counts(T) : 0u, total = before;
             for (int i = 0; i < kConsumerWarps; ++i) {
-                if (i < warp) {
-                    be += sums[2 * i];
-                    bp += sums[2 * i + 1];
-                }
-                te += sums[2 * i];
+                if (i < warp) before += sums[i];
+                total += sums[i];
             }
-            // entries of expert e from `at` on, its pairs from p on
-            auto enter = [&](int e, int at, int p, int n) {
-                list_e[at] = (uint16_t)e;
-                list_p[at] = (uint16_t)(p << 4 | min(n, 8));
-                if (n > 8) {
-                    list_e[at + 1] = (uint16_t)e;
-                    list_p[at + 1] = (uint16_t)((p + 8) << 4 | (n - 8));
+            // expert e with n tokens, `c` counted before it
+            auto enter = [&](int e, uint32_t c, int n) {
+                const int p = c & 4095u, d = (c >> 12) & 1023u, g = c >> 22;
+                for (int j = 0; j < n; j += 8) {
+                    list_e[g + j / 8] = (uint16_t)e;
+                    list_p[g + j / 8] = (uint16_t)((p + j) << 4 | min(n - j, 8));
+                }
+                for (int j = 0; j < n; j += 4) {
+                    down_e[d + j / 4] = (uint16_t)e;
+                    down_p[d + j / 4] = (uint16_t)((p + j) << 4 | min(n - j, 4));
                 }
                 first[e] = (uint16_t)p;
             };
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (mk[i]) enter(64 * warp + 32 * i + lane, be + ne[i], bp + np[i], __popc(mk[i]));
+                if (mk[i]) enter(64 * warp + 32 * i + lane, before + at[i], __popc(mk[i]));
             if (tid == 0) {
-                info[0] = te;
-                if (a.shared) enter(a.E, 0, 0, T);
+                info[0] = (int)(total >> 22);
+                info[4] = (int)((total >> 12) & 1023u);
+                if (a.shared) enter(a.E, 0, T);
             }
             consumers_sync();
             for (int i = tid; i < T * Kt; i += kConsumers) {
@@ -668,13 +671,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();  // the list is there (or the barrier gave up)
 
     const bool routed = info[1] != 0;
-    const int nent = routed ? info[0] : 0;
+    const int nent = routed ? info[0] : 0, ndown = routed ? info[4] : 0;
     const int others = max(nent * upe - shared_units, 0);
     other0 = cut(others, b, G);
     nunits = routed ? nsh + cut(others, b + 1, G) - other0 : 0;
     const int gstages = NC == 1 ? (nunits + ups - 1) / ups : nunits * NC;
     // down: items (entry, 16 output rows) in that order, cut into one range per CTA
-    const int items = RU * nent;
+    const int items = RU * ndown;
     const int lo = cut(items, b, G), hi = cut(items, b + 1, G);
     const int dstages = (hi - lo + ips - 1) / ips * spi;
     // the stages of a phase are consumed in pairs (a unit's or item's two stages, or two
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane < n) {
                 const int i = (int)div_by((uint32_t)(it0 + lane), ru_m);
-                const int row = (int)list_e[i] * H + (it0 + lane - i * RU) * 16;
+                const int row = (int)down_e[i] * H + (it0 + lane - i * RU) * 16;
                 const uint32_t base = smem_u32(smem + s * kStageBytes);
                 const uint32_t dst = base + (spi > 1 ? 0 : lane * sd) * kSlotBytes;
                 if (whole) tma_load_3d(dst, sl0 > 0 ? &maps.w2_rest : &maps.w2, 0, row, sl0, &full[s]);
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!SF && sl0 == 0) {
                 for (int q = lane; q < n * 16; q += 32) {
                     const int it = it0 + q / 16, i = (int)div_by((uint32_t)it, ru_m);
-                    const uint8_t* p = a.s2 + ((size_t)list_e[i] * H + (it - i * RU) * 16 + q % 16) * KGI;
+                    const uint8_t* p = a.s2 + ((size_t)down_e[i] * H + (it - i * RU) * 16 + q % 16) * KGI;
                     for (int o = 0; o < KGI; o += 128) prefetch_l2(p + o);
                 }
             }
@@ -840,15 +843,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int hpitch = shift_pitch(I);
             uint4 hb[8];
             int have = -1;  // entry (times stages per item, plus the chunk) whose h fragment is in hb
-            // h as f16 with one power of two for the row: each 8 values' own shift
-            // comes down to the row's
+            // column r: term r / 4 of h of the entry's token r % 4, with one power of two for
+            // the row: each 8 values' own shift comes down to the row's
             auto load_h = [&](int i, int slice, int key) {
-                const int n = list_p[i] & 15, p = (list_p[i] >> 4) + r;
+                const int n = down_p[i] & 15, p = (down_p[i] >> 4) + (r & 3);
                 have = key;
 #pragma unroll
                 for (int gl = 0; gl < 8; ++gl) hb[gl] = make_uint4(0, 0, 0, 0);
-                if (r >= n) return;
-                const uint16_t* hp = a.h + (size_t)p * I + 256 * slice + 8 * c;
+                if ((r & 3) >= n) return;
+                const uint16_t* hp = a.h + (size_t)(2 * p + (r >> 2)) * I + 256 * slice + 8 * c;
 #pragma unroll
                 for (int gl = 0; gl < 8; ++gl)
                     if (256 * slice + 32 * gl < I) hb[gl] = __ldcg(reinterpret_cast<const uint4*>(hp + 32 * gl));
@@ -875,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sw[i] = 0;
                     if (SF || j >= ips || item >= hi || grp >= KGI) continue;
                     const int e = (int)div_by((uint32_t)item, ru_m);
-                    sw[i] = load_scales(a.s2, ((size_t)list_e[e] * H + (item - e * RU) * 16 + srow) * KGI + grp, KGI - grp, words);
+                    sw[i] = load_scales(a.s2, ((size_t)down_e[e] * H + (item - e * RU) * 16 + srow) * KGI + grp, KGI - grp, words);
                 }
             };
             load_sw(0);
@@ -947,8 +950,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int o = 4; o < 32; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
                     if (on) {
                         const int sh = f32_f16_shift(mx);
-                        a.h[(size_t)p * I + blk * 8 + r] =
-                            __half_as_ushort(__float2half_rn(hv * __uint_as_float((uint32_t)(127 + sh) << 23)));
+                        const float s = hv * __uint_as_float((uint32_t)(127 + sh) << 23);
+                        const __half hi = __float2half_rn(s);
+                        // (nothing is left next to an infinity)
+                        const __half lo = __float2half_rn(fabsf(s) < 65504.0f ? s - __half2float(hi) : 0.0f);
+                        uint16_t* h = a.h + (size_t)(2 * p) * I + blk * 8 + r;
+                        h[0] = __half_as_ushort(hi);
+                        h[I] = __half_as_ushort(lo);
                         if (r == 0) {
                             // (eight zeros: a shift so high that they come down to zero)
                             a.hshift[(size_t)p * hpitch + shift_at(blk)] = (int8_t)(mx ? sh : 127);
@@ -982,7 +990,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int item = spi == 1 ? lo + (2 * h + me) * ips + j : (me ? hi : lo + h);
                 if (item >= hi) break;
                 const int i = (int)div_by((uint32_t)item, ru_m);
-                const int n = list_p[i] & 15, p = (list_p[i] >> 4) + 2 * c;
+                // this lane's columns 2c and 2c + 1: tokens (c < 2), or the rest terms of lane
+                // c - 2's, which are added to those
+                const int n = down_p[i] & 15, p = (down_p[i] >> 4) + 2 * c;
                 if (i != have) {
                     have = i;
 #pragma unroll
@@ -990,7 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (2 * c + q < n)
                             f[q] = __uint_as_float((uint32_t)(127 - f32_f16_shift(__ldcg(a.hmax + p + q))) << 23);
                 }
-                const float4 v = spi == 1 ? sum_of(buf, j * sd, sd) : sum_of(buf, 0, kConsumerWarps);
+                float4 v = spi == 1 ? sum_of(buf, j * sd, sd) : sum_of(buf, 0, kConsumerWarps);
+                v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, 2), v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, 2);
+                v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, 2), v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, 2);
                 float* y = a.y + (size_t)p * H + (item - i * RU) * 16 + r;
                 if (2 * c < n) {
                     __stcg(y, v.x * f[0]);
@@ -1051,7 +1063,7 @@ FewWorkspace few_workspace(int T, int H, int I, int E, int Kt) {
     w.logits = 256;
     w.hmax = w.logits + align256((size_t)T * (E + 1) * 4);
     w.h = w.hmax + align256(pairs * 4);
-    w.hshift = w.h + align256(pairs * I * 2);
+    w.hshift = w.h + align256(pairs * I * 2 * 2);
     w.y = w.hshift + align256(pairs * shift_pitch(I));
     w.total = w.y + align256(pairs * H * 4);
     return w;
