@@ -592,7 +592,7 @@ struct PairLayout {
 
 // ES: bytes of an output value; RES: a residual; VEC: the output's and the residual's rows
 // start on 16 bytes.  (One kernel with all the forms spilled the accumulator: 111 us where
-// these take 103.)
+// these take 102.  Of these only the 256-wide ones with a residual spill, up to 52 bytes.)
 template <int TN, int ES, bool RES, bool VEC>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const PairArgs a, const __grid_constant__ CUtensorMap x_map,
@@ -752,6 +752,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             if (tile + pairs < tiles) load(t_of(tile + pairs), n_of(tile + pairs));
         }
+        // The kernel's end, as below, but apart from the other roles': where they met at one
+        // barrier, values that only those need stayed in these warps' registers over the loop
+        // (36 bytes of spills; 8192 x 8192 x 4096: 112 us for 102).
+        tc_fence_before();
+        cluster_sync_all();
+        pdl_end();
+        return;
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegs));
         if (warp == kPairProducer) {
