@@ -598,6 +598,8 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype_t;
  *   residual NULL, or [T] rows of N values of out_type, ldr elements apart; may
  *            be out itself (same pointer, ldr = ldo).
  *   out      [T] rows of N values of out_type, ldo elements apart.
+ *   out overlaps no other argument (but residual as above): a launch may still read
+ *   x while it writes out.
  *   ldx >= 0, ldr >= 0, ldo >= N: rows may be slices of wider ones; those that
  *   are only read may overlap (0: one row for every token).
  * For each token t:

@@ -202,7 +202,7 @@ const char* moe_status_string(moe_status_t status) {
         case MOE_OK: return "MOE_OK";
         case MOE_ERR_INVALID_ARG: return "MOE_ERR_INVALID_ARG: null, negative or misaligned argument";
         case MOE_ERR_UNSUPPORTED_SHAPE: return "MOE_ERR_UNSUPPORTED_SHAPE: size outside the supported limits";
-        case MOE_ERR_WORKSPACE_TOO_SMALL: return "MOE_ERR_WORKSPACE_TOO_SMALL: workspace smaller than moe_ffn_workspace_size()";
+        case MOE_ERR_WORKSPACE_TOO_SMALL: return "MOE_ERR_WORKSPACE_TOO_SMALL: workspace smaller than the call's moe_..._workspace_size()";
         case MOE_ERR_CUDA: return "MOE_ERR_CUDA: a CUDA launch failed (see cudaGetLastError)";
         case MOE_ERR_INTERNAL: return "MOE_ERR_INTERNAL: internal error";
     }

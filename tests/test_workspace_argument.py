@@ -32,3 +32,9 @@ def test_sizes_count_bytes(recorded, monkeypatch):  # noqa: F811
     monkeypatch.setattr(type(libmoe._lib), "moe_linear_mxfp4act", lambda self, *a: sizes.append(a[-2]) or 0, raising=False)
     libmoe.moe_linear_mxfp4act(**linear(), workspace=gpu(torch.ones(1024, dtype=torch.int32)), stream=SIDE)
     assert sizes == [4096]
+
+
+def test_the_message_names_no_other_call():
+    from mxfp4_mixture_experts_softmax_gb300 import libmoe
+    text = libmoe.status_string(libmoe.MOE_ERR_WORKSPACE_TOO_SMALL)
+    assert "moe_ffn_workspace_size" not in text and "workspace" in text
