@@ -36,12 +36,14 @@
 //            each CTA adds up its share of the outputs, a token's pairs in slot
 //            order, times routing weight.
 // Measured (cold weights, call after call in one graph; 4096/1024, top-10 of 512 and a shared
-// expert): 38 us for one token (74 MB of weights), 86 for 5, 210 for 16 (105 touched
-// experts, 938 MB of weights, 4.5 TB/s).  One token: the launch 2.8, router and first
-// barrier 5, top-K and list 4, gate_up 12, second barrier 3.5, down 5.5, third barrier and
-// sum 4.  16 tokens: 15 until the list is there, gate_up 121, down 61 -- there the
-// consumers, not HBM, set the pace: a stage arrives every 0.8 us and takes them 1.3 (issue
-// slots half used, the conversion and its scaling most of them, waits for a stage a tenth).
+// expert): 36.7 us for one token (74 MB of weights), 84 for 5, 189 for 16 (about 140 touched
+// experts, 940 MB of weights, 5.0 TB/s).  By clock stamps in a build with them, one token:
+// router and first barrier 5.2, top-K and lists 4.3, gate_up 13, second barrier 3, down 6,
+// third barrier and sum 4.6.  16 tokens, 206 with the stamps: 16 until the lists are there,
+// gate_up 112, second barrier 10 (the slowest CTA ends 6 after the mean), down 62, third
+// barrier and sum 6 -- there the consumers, not HBM, set the pace: HBM would bring a stage
+// every 0.8 us, and one takes them 0.95 in gate_up and 1.04 in down (issue slots half used,
+// the conversion and its scaling most of them, waits for a stage a tenth).
 // What a warp does for a stage beside its products (waits, arrivals, handing its sums
 // over) takes longer than one slot's products, so the consumers take the stages two
 // at a time.  A warp turns its slot's scale bytes into fp32 factors once, through shared

@@ -548,9 +548,10 @@ __global__ void __launch_bounds__(kStreamThreads, (StreamLayout<NT, FUSED>::kPer
 // so TN = 256 does most per clock, although tensor memory then has room for one
 // accumulator only and a tile waits about 800 clocks while the last one is read (192 with
 // two accumulators: 144 us where 256 took 118).  8192 x 8192 x 4096: 88 us, 6.2 PFLOP/s;
-// 9700 clocks for a tile's 64 MMAs (8000 without the loads into shared memory: each stage
-// writes 36 KB there and the MMAs read 32 KB, 128 bytes a clock at most), 800 between
-// tiles, 14 tiles for most pairs and 13 for the others.  Fewer stages (3 or 4 for 5) or
+// 9700 clocks for a tile's 64 MMAs (8000 without the loads into shared memory), 800 between
+// tiles, 14 tiles for most pairs and 13 for the others.  Shared memory is what bounds it: each
+// of a tile's 16 stages writes 36 KB there and its MMAs read 32 KB, at 128 bytes a clock
+// 8700 of the 9700 clocks.  Fewer stages (3 or 4 for 5) or
 // half of the loads changed little; output by TMA instead of stores cost 8%: its reads
 // come in a burst that the operands' loads wait for.
 struct PairArgs {
@@ -646,10 +647,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // tile), out in full lines; bf16 is rounded before it is staged (half the traffic in
         // shared memory, which the MMA's operands share).  The residual (RES) comes in the
         // same way, its loads one pass ahead, asked for while the tile before is multiplied:
-        // 8192 x 8192 x 4096 with one takes 118 us in bf16 and 160 in fp32 (102 and 118
+        // 8192 x 8192 x 4096 with one takes 121 us in bf16 and 161 in fp32 (102 and 120
         // without; 174 and 335 when its loads stood between the accumulator and the stores).
         // Without VEC the output is written element by element, from fp32 (and store_out
-        // adds the residual).
+        // adds the residual): 173 us in both types, 718 and 869 with a residual, whose
+        // elements come one by one between the accumulator and the stores; 128 x 100003 x 4096
+        // in fp32 86 us, where 100000 columns take 67.
         constexpr int kBox = 128 / ES;  // columns a pass
         const int lr = lane >> 3, lc = (lane & 7) * (16 / ES);  // coalesced: rows lr + 4 i, columns lc ..
         uint4 rr[RES ? 8 : 1];
