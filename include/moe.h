@@ -554,7 +554,9 @@ moe_status_t moe_ffn_mxfp4act_h_offsets(int T, int H, int I, int Et, int Kt, int
  * expert where that is coarser).
  * Sums are fp32, over k in blocks of 32 and then over a token's slots in
  * ascending order; results do not vary from run to run.  Weight scale bytes
- * 1..254.  A token whose x holds an infinity or a NaN gets NaN outputs; other
+ * 1..224 are exact factors; 225..254 are too, but there a sum may leave fp32's
+ * range although the result would not (a row's largest element counts as up to
+ * 2^15 in it).  A token whose x holds an infinity or a NaN gets NaN outputs; other
  * tokens are not touched.
  * Limits: T <= MOE_LAYER_FEW_MAX_T (0 is a no-op), H % 32 == I % 32 == 0, H <= 8192,
  * I <= 8192, E <= 1024, K <= min(E, 32).  Pointers 16-byte

@@ -77,3 +77,18 @@ def test_an_infinite_element_of_h(m, T):
     assert np.array_equal(out[1].double().cpu().numpy(), want, equal_nan=True)
     rest = [t for t in range(T) if t != 1]
     check(out[rest], reference(d)[0][rest])
+
+
+@pytest.mark.parametrize("gate,up,down", [(224, 30, 224), (1, 224, 224), (224, 1, 127), (30, 224, 1), (127, 127, 224)])
+@pytest.mark.parametrize("T", [1, 9])
+def test_scale_bytes_at_the_ends_of_their_range(m, T, gate, up, down):
+    """Weights of 2^-126 and of 2^97 next to each other.  The outputs lie inside bf16's normal range, or
+    are skipped below it."""
+    d = make(T, 512, 96, 6, 2, True, False, seed=gate + up + T)
+    d["s13"][:, :96], d["s13"][:, 96:], d["s2"][:] = gate, up, down
+    ref = reference(d)[0]
+    assert np.abs(ref).max() < 2.0 ** 126
+    if np.abs(ref).max() < 2.0 ** -100:
+        assert np.isfinite(m.moe_layer_few(**d)[0].double().cpu().numpy()).all()
+    else:
+        check(m.moe_layer_few(**d)[0], ref)
