@@ -183,10 +183,11 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _on(stream):
-    """Makes `stream` current for what a call allocates itself: fills then come before the call's
-    kernels, and memory that is freed goes to work that comes after them."""
-    if stream is None:
+def _on(stream, *buffers):
+    """Makes `stream` current for what a call allocates itself (the `buffers` that are None): fills
+    then come before the call's kernels, and memory that is freed goes to work that comes after
+    them."""
+    if stream is None or (buffers and all(b is not None for b in buffers)):
         return _as_is
     import torch
     return torch.cuda.stream(stream)
@@ -204,7 +205,7 @@ def _route_outputs(logits, K, with_shared, topk_ids, topk_w, shared_w, stream):
     assert logits.dtype == torch.float32
     T, E = logits.shape
     Kt = K + (1 if with_shared else 0)
-    with _on(stream):
+    with _on(stream, topk_ids, topk_w):
         if topk_ids is None:
             topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=logits.device)
         if topk_w is None:
@@ -311,7 +312,7 @@ def moe_ffn(x, w13, s13, w2, s2, topk_w, perm: dict, out=None, workspace=None,
     Kt, tile_m = perm["Kt"], perm["tile_m"]
     for t in (x, w13, s13, w2, s2, topk_w):
         _dev(t, "ffn input")
-    with _on(stream):
+    with _on(stream, out, workspace):
         if out is None:
             out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
         if workspace is None:
@@ -477,7 +478,7 @@ def moe_ffn_dense_shared(x, w13, s13, w2, s2, topk_w, perm: dict, w13s, s13s, w2
     Is = w13s.shape[1] // 2
     Kt, tm = perm["Kt"], perm["tile_m"]
     n = int(load().moe_ffn_dense_shared_workspace_size(T, H, twoI // 2, Et, Kt, Is, tm))
-    with _on(stream):
+    with _on(stream, workspace, out):
         if workspace is None:
             workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
         if out is None:
@@ -516,7 +517,7 @@ def moe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
     import torch
     _dev(x, "x")
     rows, cols = x.shape
-    with _on(stream):
+    with _on(stream, codes, scales):
         if codes is None:
             codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
         if scales is None:
@@ -546,7 +547,7 @@ def moe_ffn_mxfp4act(x, w13, s13, w2, s2, topk_w, perm: dict, out=None, workspac
     Kt, tile_m = perm["Kt"], perm["tile_m"]
     for t in (x, w13, s13, w2, s2, topk_w):
         _dev(t, "ffn input")
-    with _on(stream):
+    with _on(stream, out, workspace):
         if out is None:
             out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
         if workspace is None:
@@ -645,7 +646,7 @@ def moe_layer_few(x, w_router, w13, s13, w2, s2, K: int, with_shared: bool = Tru
         assert w_shared_gate.dtype == bf16 and w_shared_gate.shape == (H,)
     if out is not None and not (out.is_cuda and out.is_contiguous() and out.dtype == bf16 and out.shape == x.shape):
         raise ValueError("out must be a contiguous CUDA bfloat16 tensor like x")
-    with _on(stream):
+    with _on(stream, out, topk_ids, topk_w, workspace):
         if out is None:
             out = torch.empty_like(x)
         if topk_ids is None:

@@ -113,3 +113,31 @@ def test_the_other_calls_own_buffers(recorded, name, args):
     made.clear()
     getattr(libmoe, name)(**args, stream=SIDE)
     assert made and all(s is SIDE for _, s in made), made
+
+
+def given(libmoe, name):
+    """Arguments with every buffer among them."""
+    u8, bf16 = torch.uint8, torch.bfloat16
+    ids, w = rand(T, K + 1, dtype=torch.int32), rand(T, K + 1, dtype=torch.float32)
+    perm, ws, out = libmoe.alloc_permute(T, K + 1, E + 1, 8), rand(1 << 20, dtype=u8), rand(T, H)
+    return {
+        "moe_route": dict(logits=rand(T, E, dtype=torch.float32), K=K, topk_ids=ids, topk_w=w),
+        "moe_route_permute": dict(logits=rand(T, E, dtype=torch.float32), K=K, tile_m=8, topk_ids=ids, topk_w=w, perm=perm),
+        "moe_ffn": dict(ffn(libmoe), out=out, workspace=ws), "moe_ffn_mxfp4act": dict(ffn(libmoe), out=out, workspace=ws),
+        "moe_ffn_dense_shared": dict(dense(libmoe), out=out, workspace=ws),
+        "moe_quantize_mxfp4": dict(x=rand(T, H), codes=rand(T, H // 2, dtype=u8), scales=rand(T, H // 32, dtype=u8)),
+        "moe_layer_few": dict(few(E, T, H, I), out=out, topk_ids=ids, topk_w=w, workspace=ws),
+        "moe_linear_mxfp4act": dict(linear(T, 16, H), out=rand(T, 16, dtype=bf16), workspace=ws),
+    }[name]
+
+
+@pytest.mark.parametrize("name", ["moe_route", "moe_route_permute", "moe_ffn", "moe_ffn_mxfp4act", "moe_ffn_dense_shared",
+                                  "moe_quantize_mxfp4", "moe_layer_few", "moe_linear_mxfp4act"])
+def test_no_stream_switch_when_everything_is_given(recorded, monkeypatch, name):
+    """A call that allocates nothing does not pay for a switch."""
+    libmoe, made = recorded
+    args = given(libmoe, name)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: pytest.fail("switched"))
+    made.clear()
+    getattr(libmoe, name)(**args, stream=SIDE)
+    assert not made
