@@ -208,7 +208,8 @@ def _plain_route(s):
 
 
 def _plain_lora(s):
-    out = s["res"].float() if s["res"] is not None else torch.zeros((s["T"], s["N"]), device=DEV)
+    # (a copy: the sums below must not go into the residual itself)
+    out = s["res"].to(torch.float32, copy=True) if s["res"] is not None else torch.zeros((s["T"], s["N"]), device=DEV)
     for a, rows, rank in s["groups_of"]:
         v = s["x"][rows].float() @ s["a"][a, :rank].float().t()
         out[rows] = out[rows] + s["scale"][a] * (v @ s["bt"][a, :, :rank].float().t())
