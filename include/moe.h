@@ -626,6 +626,125 @@ moe_status_t moe_linear_mxfp4act(const void* x, moe_dtype_t x_type, int64_t ldx,
                                  moe_dtype_t out_type, int64_t ldo, int T, int N, int K,
                                  void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * ------------------------------------------- what lies between the products
+ * Routing of other models, adapters beside the projections, and the sums and
+ * norms between two blocks.  The pages name such parts of a served model (expert
+ * groups, norms fused with their residual) but not these calls.
+ */
+
+/* How moe_route_grouped scores an expert: over all experts, or each by itself. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+/*
+ * moe_route_grouped -- routing by scores, with a bias for balance and groups.
+ *
+ *   logits    [T] rows of E values of logits_type, row t at logits + t * ldl
+ *             (ldl >= 0; rows may be slices of wider ones).
+ *   bias      fp32 [E] or NULL: added to the scores for the choice alone.
+ *   shared_w  fp32 [T] or NULL: as for moe_route_ex.
+ *   topk_ids, topk_w  int32 and fp32 [T, K + (with_shared ? 1 : 0)] out.
+ * For each token:
+ *   s_e = softmax(l)_e or 1 / (1 + exp(-l_e));  c_e = s_e + bias_e
+ *   groups of E / n_groups consecutive experts, each worth the sum of its
+ *   group_top (1 or 2) largest c; the topk_groups of the largest worth stay;
+ *   ids: the K largest c of their experts, in descending order;
+ *   w = scale * s_id, divided by the sum of the K chosen s with renormalize.
+ * Equal values go to the lower group and the lower expert.  Without a bias c is
+ * ordered as the logits are, also where scores round alike.  Choices are those of
+ * the values in 64 bits: the fp32 values decide only where they lie further apart
+ * than their error.  Weights agree with the formula to a few fp32 ulp; with
+ * renormalize also where every chosen score underflows.
+ * With with_shared slot K holds expert id E with weight 1 or shared_w[t] (scale
+ * does not apply to it).  topk_groups = n_groups: groups play no part.
+ * A NaN logit counts as -inf.  With an infinite logit under softmax, or a bias
+ * that is not finite, the ids are distinct and in range and the weights unspecified.
+ * A token whose logits are all -inf has weights of 0 under softmax and under
+ * renormalize.
+ * Limits: E <= 1024, K <= 32, n_groups <= 32 and a divisor of E, K <= topk_groups *
+ * E / n_groups, group_top <= E / n_groups where groups play a part.  T = 0 is a
+ * no-op.  Outputs overlap no input.
+ */
+moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits_type, int64_t ldl, const float* bias,
+                               const float* shared_w, int T, int E, int K, moe_score_t score, int n_groups,
+                               int topk_groups, int group_top, int with_shared, int renormalize, float scale,
+                               int32_t* topk_ids, float* topk_w, cudaStream_t stream);
+
+/*
+ * moe_lora -- low-rank adapters of many requests beside a shared projection:
+ *   out[t] = residual[t] + scale[e] * B[e] (A[e] x_t),  e the adapter of token t;
+ *   out[t] = residual[t] (zeros without a residual) for a token without one.
+ *
+ *   x         [T] rows of K values of x_type, ldx elements apart.
+ *   a         bf16 [adapters, R, K]; b  bf16 [adapters, N, R].
+ *   scale     fp32 [adapters], or NULL for 1.
+ *   ranks     int32 [adapters], or NULL for R: rank r of an adapter with fewer ranks
+ *             than R.  Its rows of a and columns of b from r on are ignored,
+ *             whatever they hold.  Values are clamped to [0, R].
+ *   sorted_pairs, inv_pairs, tile_expert, num_tiles: moe_permute's outputs for
+ *             the tokens' adapters (topk_ids [T, 1], Kt = 1, Et = adapters) and the
+ *             same tile_m; an id outside [0, adapters), such as -1, is a token without
+ *             an adapter.  One grouping serves every projection of a step.
+ *   residual  NULL, or [T] rows of N values of out_type, ldr elements apart; may be
+ *             out itself (same pointer, ldr = ldo): rows without an adapter are then
+ *             not touched.
+ *   out       [T] rows of N values of out_type, ldo >= N elements apart; overlaps
+ *             no other argument (but residual as above).
+ * moe_lora_tile_m gives a tile height that suits T tokens of that many adapters.
+ * Products of bf16 values are exact (an fp32 x enters as three bf16 terms, exactly)
+ * and sums fp32; A x enters the second product rounded to 2^-16 of itself for bf16
+ * outputs and 2^-24 for fp32 ones; one rounding to out_type.  Results do not vary
+ * from run to run, nor with the other tokens of the batch, as long as T, adapters
+ * and tile_m are the same.  A token whose x holds an infinity or a NaN does not change others.
+ * One launch, no workspace.  T = 0 is a no-op.
+ * Limits: K % 8 == 0, K <= 65536, N <= 2^24, T <= 2^20, R % 8 == 0, R <=
+ * MOE_LORA_MAX_RANK, adapters <= 1025, tile_m 16, 32 or 64.  a and b 16-byte aligned, the
+ * others to their element; x, residual and out rows on 16-byte boundaries are read
+ * and written faster.  A grouping that names an adapter or a token outside the range
+ * is not followed there (moe_device_error value 2).
+ */
+#define MOE_LORA_MAX_RANK 128
+int moe_lora_tile_m(int T, int adapters);
+moe_status_t moe_lora(const void* x, moe_dtype_t x_type, int64_t ldx, const uint16_t* a, const uint16_t* b,
+                      const float* scale, const int32_t* ranks, const int32_t* sorted_pairs,
+                      const int32_t* inv_pairs, const int32_t* tile_expert, const int32_t* num_tiles, int tile_m,
+                      int adapters, const void* residual, int64_t ldr, void* out, moe_dtype_t out_type,
+                      int64_t ldo, int T, int N, int K, int R, cudaStream_t stream);
+
+/* What moe_combine_norm does to its gate's values. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_SILU = 2 } moe_gate_act_t;
+
+/*
+ * moe_combine_norm -- from a block's output to the next block's input:
+ *   y  = sum over j ascending of y[t * slots + j]        (slots = 1: y itself)
+ *   u  = y, or N(y; post_w) with post_norm;  u *= act(gate)  with a gate
+ *   h' = beta * h + alpha * u                            (no h: alpha * u)
+ *   n  = N(h'; pre_w)                                    (no pre_w: weights 1)
+ *   N(v; w) = v / sqrt(mean(v^2) + eps) * (w + w_offset)
+ * as the sum of a token's expert outputs (moe_ffn_down's y, slots = Kt), the
+ * residual and the norm of what comes next, in one pass.
+ *
+ *   y        [T * slots] rows of H values of y_type, ldy elements apart.
+ *   post_w, pre_w  [H] of w_type, or NULL (post_w only without post_norm).
+ *   gate     NULL, or [T] rows of gate_cols values of gate_type, ldg elements apart
+ *            (0: one row for every token); gate_cols is H, or 1: one value a token.
+ *   h        NULL, or [T] rows of H values of h_type, ldh elements apart.
+ *   h_out    NULL, or [T] rows of h_type, ldho >= H elements apart: h', rounded.
+ *            May be h itself (same pointer and stride).
+ *   n_out    NULL, or [T] rows of n_type, ldn >= H elements apart: n, of h' before
+ *            its rounding.  May be y itself (same pointer, type and stride, slots = 1).
+ * One output at least; otherwise they overlap no argument.  Everything is fp32 up
+ * to the two roundings.  Results do not vary from run to run.
+ * Limits: H <= 16384, slots <= 64.  Pointers aligned to their element; rows on
+ * 16-byte boundaries (8-byte: half as wide) are accessed faster.  T = 0 is a no-op.
+ */
+moe_status_t moe_combine_norm(const void* y, moe_dtype_t y_type, int64_t ldy, int slots, int post_norm,
+                              const void* post_w, const void* pre_w, moe_dtype_t w_type, float w_offset, float eps,
+                              const void* gate, moe_dtype_t gate_type, int64_t ldg, int gate_cols,
+                              moe_gate_act_t gate_act, const void* h, int64_t ldh, float alpha, float beta,
+                              void* h_out, moe_dtype_t h_type, int64_t ldho, void* n_out, moe_dtype_t n_type,
+                              int64_t ldn, int T, int H, cudaStream_t stream);
+
 /* The regime MOE_PATH_AUTO picks for these sizes [VL, small-M vs large-M]:
  * MOE_PATH_DECODE or MOE_PATH_PREFILL (the large-M regime, whichever of its
  * two paths moe_ffn_auto_path_shape names). */

@@ -223,7 +223,9 @@ moe_status_t moe_device_error(int* flag, int clear) {
     int f = 0;
     if (err == cudaSuccess) err = read_device_error_linear(&e, clear);
     if (err == cudaSuccess) err = read_device_error_few(&f, clear);
-    *flag = a | b | c | d | e | f;
+    int g = 0;
+    if (err == cudaSuccess) err = read_device_error_lora(&g, clear);
+    *flag = a | b | c | d | e | f | g;
     return cuda_status(err);
 }
 
@@ -1049,6 +1051,153 @@ moe_status_t moe_layer_few(const uint16_t* x, const uint16_t* w_router, const ui
     p.topk_w = topk_w;
     if (ws_bytes < layer_few_workspace(T, H, I, E, K + p.shared)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     return cuda_status(launch_layer_few(p, workspace, stream));
+}
+
+// ------------------------------------------------------- grouped routing
+
+moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits_type, int64_t ldl, const float* bias,
+                               const float* shared_w, int T, int E, int K, moe_score_t score, int n_groups,
+                               int topk_groups, int group_top, int with_shared, int renormalize, float scale,
+                               int32_t* topk_ids, float* topk_w, cudaStream_t stream) {
+    if (T < 0 || E < 1 || K < 1 || n_groups < 1 || topk_groups < 1 || ldl < 0) return MOE_ERR_INVALID_ARG;
+    if ((logits_type != MOE_DTYPE_BF16 && logits_type != MOE_DTYPE_F32) ||
+        (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) || (group_top != 1 && group_top != 2))
+        return MOE_ERR_INVALID_ARG;
+    if (E > 1024 || K > 32 || n_groups > 32 || E % n_groups || topk_groups > n_groups ||
+        K > topk_groups * (E / n_groups) || (n_groups > topk_groups && group_top > E / n_groups))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!ptrs_ok({logits}, logits_type == MOE_DTYPE_F32 ? 4 : 2) || !ptrs_ok({topk_ids, topk_w}, 4) ||
+        !aligned(bias, 4) || !aligned(shared_w, 4) || (shared_w && !with_shared))
+        return MOE_ERR_INVALID_ARG;
+    RouteGrouped p = {};
+    p.logits = logits;
+    p.bf16 = logits_type == MOE_DTYPE_BF16;
+    p.ld = ldl;
+    p.bias = bias;
+    p.shared_w = shared_w;
+    p.T = T;
+    p.E = E;
+    p.K = K;
+    p.sigmoid = score == MOE_SCORE_SIGMOID;
+    p.groups = n_groups;
+    p.chosen = topk_groups;
+    p.top = group_top;
+    p.shared = with_shared ? 1 : 0;
+    p.renorm = renormalize ? 1 : 0;
+    p.scale = scale;
+    p.ids = topk_ids;
+    p.w = topk_w;
+    return cuda_status(launch_route_grouped(p, stream));
+}
+
+// ----------------------------------------------------- low-rank adapters
+
+int moe_lora_tile_m(int T, int adapters) {
+    if (T < 0 || adapters < 1) return 0;
+    return lora_tile_rule(T, adapters);
+}
+
+moe_status_t moe_lora(const void* x, moe_dtype_t x_type, int64_t ldx, const uint16_t* a, const uint16_t* b,
+                      const float* scale, const int32_t* ranks, const int32_t* sorted_pairs,
+                      const int32_t* inv_pairs, const int32_t* tile_expert, const int32_t* num_tiles, int tile_m,
+                      int adapters, const void* residual, int64_t ldr, void* out, moe_dtype_t out_type,
+                      int64_t ldo, int T, int N, int K, int R, cudaStream_t stream) {
+    if (T < 0 || N < 1 || K < 1 || R < 1 || adapters < 1) return MOE_ERR_INVALID_ARG;
+    if ((x_type != MOE_DTYPE_BF16 && x_type != MOE_DTYPE_F32) ||
+        (out_type != MOE_DTYPE_BF16 && out_type != MOE_DTYPE_F32))
+        return MOE_ERR_INVALID_ARG;
+    if (K % 8 || K > 65536 || N > (1 << 24) || T > (1 << 20) || R % 8 || R > MOE_LORA_MAX_RANK || adapters > 1025 ||
+        !lora_tile_supported(tile_m))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    const size_t xa = x_type == MOE_DTYPE_F32 ? 4 : 2, oa = out_type == MOE_DTYPE_F32 ? 4 : 2;
+    if (!ptrs_ok({x}, xa) || !ptrs_ok({out}, oa) || !aligned(residual, oa) || !ptrs_ok({a, b}, 16) ||
+        !aligned(scale, 4) || !aligned(ranks, 4) ||
+        !ptrs_ok({sorted_pairs, inv_pairs, tile_expert, num_tiles}, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (ldx < 0 || (residual && ldr < 0) || ldo < N) return MOE_ERR_INVALID_ARG;
+    Lora p = {};
+    p.x = x;
+    p.x_f32 = x_type == MOE_DTYPE_F32;
+    p.ldx = ldx;
+    p.a = a;
+    p.b = b;
+    p.scale = scale;
+    p.ranks = ranks;
+    p.sorted_pairs = sorted_pairs;
+    p.inv_pairs = inv_pairs;
+    p.tile_expert = tile_expert;
+    p.num_tiles = num_tiles;
+    p.tile_m = tile_m;
+    p.max_tiles = (int)(capacity64(T, 1, adapters, tile_m) / tile_m);
+    p.adapters = adapters;
+    p.residual = residual;
+    p.ldr = residual ? ldr : 0;
+    p.out = out;
+    p.out_f32 = out_type == MOE_DTYPE_F32;
+    p.ldo = ldo;
+    p.T = T;
+    p.N = N;
+    p.K = K;
+    p.R = R;
+    return cuda_status(launch_lora(p, stream));
+}
+
+// ----------------------------------------------- between two blocks
+
+static bool dtype_ok(moe_dtype_t t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
+static size_t dtype_bytes(moe_dtype_t t) { return t == MOE_DTYPE_F32 ? 4 : 2; }
+
+moe_status_t moe_combine_norm(const void* y, moe_dtype_t y_type, int64_t ldy, int slots, int post_norm,
+                              const void* post_w, const void* pre_w, moe_dtype_t w_type, float w_offset, float eps,
+                              const void* gate, moe_dtype_t gate_type, int64_t ldg, int gate_cols,
+                              moe_gate_act_t gate_act, const void* h, int64_t ldh, float alpha, float beta,
+                              void* h_out, moe_dtype_t h_type, int64_t ldho, void* n_out, moe_dtype_t n_type,
+                              int64_t ldn, int T, int H, cudaStream_t stream) {
+    if (T < 0 || H < 1 || slots < 1) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(y_type) || !dtype_ok(w_type) || !dtype_ok(gate_type) || !dtype_ok(h_type) || !dtype_ok(n_type) ||
+        gate_act < MOE_GATE_NONE || gate_act > MOE_GATE_SILU)
+        return MOE_ERR_INVALID_ARG;
+    if (H > kCombineNormMaxH || slots > 64) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    const size_t wa = dtype_bytes(w_type), ha = dtype_bytes(h_type);
+    if (!ptrs_ok({y}, dtype_bytes(y_type)) || (!h_out && !n_out) || !aligned(h, ha) || !aligned(h_out, ha) ||
+        !aligned(n_out, dtype_bytes(n_type)) || !aligned(post_w, wa) || !aligned(pre_w, wa) ||
+        !aligned(gate, dtype_bytes(gate_type)))
+        return MOE_ERR_INVALID_ARG;
+    if ((post_norm && !post_w) || (gate && gate_cols != 1 && gate_cols != H)) return MOE_ERR_INVALID_ARG;
+    if (ldy < 0 || (gate && ldg < 0) || (h && ldh < 0) || (h_out && ldho < H) || (n_out && ldn < H))
+        return MOE_ERR_INVALID_ARG;
+    CombineNorm p = {};
+    p.y = y;
+    p.y_f32 = y_type == MOE_DTYPE_F32;
+    p.ldy = ldy;
+    p.slots = slots;
+    p.post = post_norm ? 1 : 0;
+    p.post_w = post_norm ? post_w : nullptr;
+    p.pre_w = n_out ? pre_w : nullptr;
+    p.w_f32 = w_type == MOE_DTYPE_F32;
+    p.w_offset = w_offset;
+    p.eps = eps;
+    p.gate = gate;
+    p.gate_f32 = gate_type == MOE_DTYPE_F32;
+    p.ldg = gate ? ldg : 0;
+    p.gate_cols = gate ? gate_cols : 1;
+    p.act = (int)gate_act;
+    p.h = h;
+    p.ldh = h ? ldh : 0;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.h_out = h_out;
+    p.h_f32 = h_type == MOE_DTYPE_F32;
+    p.ldho = h_out ? ldho : 0;
+    p.n_out = n_out;
+    p.n_f32 = n_type == MOE_DTYPE_F32;
+    p.ldn = n_out ? ldn : 0;
+    p.T = T;
+    p.H = H;
+    return cuda_status(launch_combine_norm(p, stream));
 }
 
 }  // extern "C"

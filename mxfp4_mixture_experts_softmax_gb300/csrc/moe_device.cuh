@@ -218,6 +218,16 @@ __device__ __forceinline__ void cluster_sync_all() {
                      : "memory");
 }
 
+// The two halves of cluster_sync_all, for a CTA with work of its own in between.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Arrive on the mbarrier at the same shared-memory offset in CTA `rank` of
 // the cluster, with the arrive's default semantics (release at CTA scope): no
 // cluster-scope fence, which stalled every arriving warp for microseconds.

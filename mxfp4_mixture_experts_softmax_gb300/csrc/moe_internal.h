@@ -330,6 +330,80 @@ size_t layer_few_workspace(int T, int H, int I, int E, int Kt);
 cudaError_t launch_layer_few(const LayerFew& p, void* workspace, cudaStream_t s);
 cudaError_t read_device_error_few(int* flag, int clear);
 
+// Routing with scores, bias and groups (route_grouped.cu).
+struct RouteGrouped {
+    const void* logits;     // [T] rows of E fp32 or bf16, ld elements apart
+    int bf16;
+    long long ld;
+    const float* bias;      // [E] or null
+    const float* shared_w;  // [T] or null
+    int T, E, K;
+    int sigmoid;            // else softmax
+    int groups, chosen;     // the best `chosen` of the groups stay
+    int top;                // a group's value: the sum of its `top` (1 or 2) largest
+    int shared, renorm;
+    float scale;
+    int32_t* ids;           // [T][K + shared]
+    float* w;
+    int lanes;              // lanes a group (set by the launcher)
+};
+cudaError_t launch_route_grouped(const RouteGrouped& p, cudaStream_t s);
+
+// Low-rank adapters beside a projection (lora.cu).
+struct Lora {
+    const void* x;                 // [T] rows of K values, ldx elements apart
+    int x_f32;                     // fp32 rows, else bf16
+    long long ldx;
+    const uint16_t* a;             // bf16 [adapters][R][K]
+    const uint16_t* b;             // bf16 [adapters][N][R]
+    const float* scale;            // [adapters] or null
+    const int32_t* ranks;          // [adapters] or null
+    const int32_t *sorted_pairs, *inv_pairs, *tile_expert, *num_tiles;  // moe_permute with Kt = 1
+    int tile_m, max_tiles, adapters;
+    const void* residual;          // [T] rows, ldr elements apart, of out's type; or null
+    long long ldr;
+    void* out;
+    int out_f32;
+    long long ldo;
+    int T, N, K, R;
+    // set by the launcher: most tiles that T tokens can use, CTAs a tile, rows that can be
+    // accessed 16 bytes at a time
+    int tiles, ctas, x_wide, res_wide, out_wide;
+};
+bool lora_tile_supported(int tile_m);
+int lora_tile_rule(int T, int adapters);
+cudaError_t launch_lora(const Lora& p, cudaStream_t s);
+cudaError_t read_device_error_lora(int* flag, int clear);
+
+// Sum over a token's slots, norms, gate and residual (combine_norm.cu).
+constexpr int kCombineNormMaxH = 16384;
+struct CombineNorm {
+    const void* y;           // [T * slots] rows of H values, ldy elements apart
+    int y_f32;
+    long long ldy;
+    int slots;
+    int post;                // norm of y with post_w
+    const void *post_w, *pre_w;  // [H]; pre_w or null (weights 1)
+    int w_f32;
+    float w_offset, eps;
+    const void* gate;        // null, or rows of gate_cols (1 or H) values, ldg elements apart
+    int gate_f32;
+    long long ldg;
+    int gate_cols;
+    int act;                 // 0 none, 1 sigmoid, 2 silu
+    const void* h;           // [T] rows or null
+    long long ldh;
+    float alpha, beta;
+    void* h_out;             // of h's type, or null
+    int h_f32;
+    long long ldho;
+    void* n_out;             // or null
+    int n_f32;
+    long long ldn;
+    int T, H;
+};
+cudaError_t launch_combine_norm(const CombineNorm& p, cudaStream_t s);
+
 // grouping of one dense expert over T tokens (Kt = 1); ones[T] = 1 if given
 cudaError_t launch_identity_perm(int T, int tile_m, int cap, int max_tiles, int32_t* sorted_pairs,
                                  int32_t* tile_expert, int32_t* num_tiles, float* ones,

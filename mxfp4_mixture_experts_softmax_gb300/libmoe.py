@@ -29,6 +29,13 @@ MOE_PATH_PREFILL_FP8X2 = 3
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
+MOE_GATE_NONE = 0
+MOE_GATE_SIGMOID = 1
+MOE_GATE_SILU = 2
+
 EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_route_ex", "moe_permute_capacity",
            "moe_permute_max_tiles", "moe_permute", "moe_route_permute", "moe_ffn_workspace_size",
            "moe_ffn",
@@ -40,12 +47,15 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_route", "moe_route_ex", "moe
            "moe_ffn_mxfp4act", "moe_ffn_mxfp4act_gate_up", "moe_ffn_mxfp4act_down",
            "moe_ffn_mxfp4act_h_offsets", "moe_ffn_down_combine", "moe_split_e4m3x2", "moe_ffn_auto_path_shape",
            "moe_linear_mxfp4act_workspace_size", "moe_linear_mxfp4act",
-           "moe_layer_few_workspace_size", "moe_layer_few_workspace_init", "moe_layer_few")
+           "moe_layer_few_workspace_size", "moe_layer_few_workspace_init", "moe_layer_few",
+           "moe_route_grouped", "moe_lora_tile_m", "moe_lora", "moe_combine_norm")
 
 # bytes of the fixed device scratch behind moe_ffn_noalloc (include/moe.h)
 MOE_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 # most tokens of moe_layer_few (include/moe.h)
 MOE_LAYER_FEW_MAX_T = 16
+# most ranks of an adapter of moe_lora (include/moe.h)
+MOE_LORA_MAX_RANK = 128
 # batches up to this many tokens route and permute in one launch (include/moe.h)
 MOE_ROUTE_PERMUTE_FUSED_MAX_T = 32
 
@@ -156,6 +166,16 @@ def load(build: bool = True):
         L.moe_layer_few_workspace_init.restype = ci
         L.moe_layer_few.argtypes = [vp] * 7 + [ci] * 7 + [vp, vp, vp, vp, sz, vp]
         L.moe_layer_few.restype = ci
+        cf = ctypes.c_float
+        L.moe_route_grouped.argtypes = [vp, ci, i64, vp, vp] + [ci] * 9 + [cf, vp, vp, vp]
+        L.moe_route_grouped.restype = ci
+        L.moe_lora_tile_m.argtypes = [ci, ci]
+        L.moe_lora_tile_m.restype = ci
+        L.moe_lora.argtypes = [vp, ci, i64, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, vp, i64, vp, ci, i64, ci, ci, ci, ci, vp]
+        L.moe_lora.restype = ci
+        L.moe_combine_norm.argtypes = [vp, ci, i64, ci, ci, vp, vp, ci, cf, cf, vp, ci, i64, ci, ci, vp, i64, cf, cf,
+                                       vp, ci, i64, vp, ci, i64, ci, ci, vp]
+        L.moe_combine_norm.restype = ci
         L.moe_device_error.argtypes = [vp, ci]
         L.moe_device_error.restype = ci
         _lib = L
@@ -736,3 +756,150 @@ def moe_linear_mxfp4act(x, codes, scales, residual=None, out=None, out_dtype=Non
     if status:
         raise MoeError(status, "moe_linear_mxfp4act")
     return out
+
+
+# ------------------------------------------------- what lies between the products
+
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_GATES = {"none": MOE_GATE_NONE, "sigmoid": MOE_GATE_SIGMOID, "silu": MOE_GATE_SILU}
+
+
+def _dtype_code(t, what: str) -> int:
+    """MOE_DTYPE_... of a tensor."""
+    import torch
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return MOE_DTYPE_BF16
+    assert dt is torch.float32, f"{what} must be bfloat16 or float32"
+    return MOE_DTYPE_F32
+
+
+def moe_route_grouped(logits, K: int, bias=None, score: str = "sigmoid", n_groups: int = 1, topk_groups: int = 1,
+                      group_top: int = 2, with_shared: bool = True, renormalize: bool = True, scale: float = 1.0,
+                      topk_ids=None, topk_w=None, shared_w=None, stream=None):
+    """fp32 or bf16 logits [T, E] (rows may be slices of wider ones) -> (int32 ids [T, Kt], fp32
+    weights [T, Kt]), by softmax or sigmoid scores plus bias (fp32 [E]), within the topk_groups best
+    of n_groups groups of experts, each worth the sum of its group_top largest (include/moe.h)."""
+    import torch
+    T, E = logits.shape
+    Kt = K + 1 if with_shared else K
+    with _on(stream, topk_ids, topk_w):
+        if topk_ids is None:
+            topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=logits.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, Kt), dtype=torch.float32, device=logits.device)
+    for t, dt in ((topk_ids, torch.int32), (topk_w, torch.float32)):
+        assert t.is_cuda and t.is_contiguous() and t.dtype == dt and t.numel() == T * Kt, \
+            "topk_ids and topk_w must be contiguous int32 and float32 [T, Kt]"
+    for t, shape, what in ((bias, (E,), "bias"), (shared_w, (T,), "shared_w")):
+        if t is not None:
+            _dev(t, what)
+            assert t.dtype == torch.float32 and t.shape == shape, f"{what} must be float32 {shape}"
+    status = (_lib or load()).moe_route_grouped(
+        logits.data_ptr(), _dtype_code(logits, "logits"), _row_stride(logits, T, E, "logits"),
+        None if bias is None else bias.data_ptr(), None if shared_w is None else shared_w.data_ptr(), T, E, K,
+        _SCORES[score], n_groups, topk_groups, group_top, 1 if with_shared else 0, 1 if renormalize else 0, scale,
+        topk_ids.data_ptr(), topk_w.data_ptr(), _raw_stream(stream, logits))
+    if status:
+        raise MoeError(status, "moe_route_grouped")
+    return topk_ids, topk_w
+
+
+def moe_lora_tile_m(T: int, adapters: int) -> int:
+    return int(load().moe_lora_tile_m(T, adapters))
+
+
+def moe_lora_plan(adapter_ids, adapters: int, tile_m: int | None = None, out: dict | None = None, stream=None) -> dict:
+    """The grouping of tokens by adapter that moe_lora takes: int32 adapter_ids [T] (-1: none) ->
+    moe_permute's dict.  One serves every projection of a step."""
+    T, = adapter_ids.shape
+    return moe_permute(adapter_ids.view(T, 1), adapters, tile_m or moe_lora_tile_m(T, adapters), out=out, stream=stream)
+
+
+def moe_lora(x, a, b, plan: dict, scale=None, ranks=None, residual=None, out=None, out_dtype=None, stream=None):
+    """residual + scale * B (A x) with each token's own adapter: x [T, K] bf16 or fp32, a bf16
+    [adapters, R, K], b bf16 [adapters, N, R], plan from moe_lora_plan, scale fp32 and ranks int32
+    [adapters], residual [T, N] (may be out) (include/moe.h).  x, residual and out may be row slices of
+    wider tensors; out_dtype: torch.bfloat16 (default) or torch.float32."""
+    import torch
+    T, K = x.shape
+    n, N, R = b.shape
+    assert plan["T"] == T and plan["Kt"] == 1 and plan["Et"] == n, "plan does not match x and the adapters"
+    assert a.shape == (n, R, K) and a.dtype == b.dtype == torch.bfloat16, "a and b must be bfloat16 [n, R, K] and [n, N, R]"
+    _dev(a, "a")
+    _dev(b, "b")
+    for t, dt, what in ((scale, torch.float32, "scale"), (ranks, torch.int32, "ranks")):
+        if t is not None:
+            _dev(t, what)
+            assert t.dtype == dt and t.shape == (n,), f"{what} must be {dt} [{n}]"
+    if out is None:
+        with _on(stream):
+            out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+        ldo = N
+    else:
+        assert out.shape == (T, N) and out_dtype in (None, out.dtype), "out must be [T, N]"
+        ldo = _row_stride(out, T, N, "out")
+    res, ldr = None, 0
+    if residual is not None:
+        assert residual.shape == (T, N) and residual.dtype == out.dtype, "residual must match out"
+        res, ldr = residual.data_ptr(), _row_stride(residual, T, N, "residual")
+    status = (_lib or load()).moe_lora(
+        x.data_ptr(), _dtype_code(x, "x"), _row_stride(x, T, K, "x"), a.data_ptr(), b.data_ptr(),
+        None if scale is None else scale.data_ptr(), None if ranks is None else ranks.data_ptr(),
+        plan["sorted_pairs"].data_ptr(), plan["inv_pairs"].data_ptr(), plan["tile_expert"].data_ptr(),
+        plan["num_tiles"].data_ptr(), plan["tile_m"], n, res, ldr, out.data_ptr(), _dtype_code(out, "out"), ldo, T, N, K, R,
+        _raw_stream(stream, x))
+    if status:
+        raise MoeError(status, "moe_lora")
+    return out
+
+
+def moe_combine_norm(y, h=None, slots: int = 1, post_w=None, gate=None, gate_act: str = "none", alpha: float = 1.0,
+                     beta: float = 1.0, pre_w=None, w_offset: float = 0.0, eps: float = 1e-6, h_out=None, n_out=None,
+                     h_dtype=None, n_dtype=None, stream=None):
+    """From a block's output to the next block's input: y [T * slots, H] summed over a token's slots,
+    its norm with post_w, times act(gate) (gate [T or 1, H or 1]), h' = beta h + alpha u, and the norm of
+    h' with pre_w -> (h' [T, H], n [T, H]) (include/moe.h).  h_out may be h, n_out may be y.  Without h, h'
+    has h_dtype (default bfloat16) and is not written if h_out is False; n has n_dtype (default
+    bfloat16) and is not written if n_out is False."""
+    import torch
+    rows, H = y.shape
+    T = rows // slots
+    assert T * slots == rows, "y must hold slots rows a token"
+    dev, bf16 = y.device, torch.bfloat16
+    with _on(stream, *(b if b is not False else 0 for b in (h_out, n_out))):
+        if h_out is None:
+            h_out = torch.empty((T, H), dtype=h.dtype if h is not None else h_dtype or bf16, device=dev)
+        if n_out is None:
+            n_out = torch.empty((T, H), dtype=n_dtype or bf16, device=dev)
+    args = []
+    for t, what in ((h, "h"), (h_out, "h_out"), (n_out, "n_out")):
+        if t is None or t is False:
+            args.append((None, 0, 0))
+        else:
+            assert t.shape == (T, H), f"{what} must be [T, H]"
+            args.append((t.data_ptr(), _dtype_code(t, what), _row_stride(t, T, H, what)))
+    (hp, ht, ldh), (hop, hot, ldho), (np_, nt, ldn) = args
+    assert hp is None or hop is None or ht == hot, "h_out must have h's type"
+    w_type = 0
+    for w, what in ((post_w, "post_w"), (pre_w, "pre_w")):
+        if w is not None:
+            _dev(w, what)
+            assert w.shape == (H,), f"{what} must be [H]"
+            w_type = _dtype_code(w, what)
+    assert post_w is None or pre_w is None or post_w.dtype == pre_w.dtype, "post_w and pre_w must have one type"
+    gp, gt, ldg, cols = None, 0, 0, 1
+    if gate is not None:
+        grows, cols = gate.shape
+        assert grows in (1, T) and cols in (1, H), "gate must be [T or 1, H or 1]"
+        gp, gt = gate.data_ptr(), _dtype_code(gate, "gate")
+        ldg = 0 if grows == 1 else _row_stride(gate, T, cols, "gate")
+        assert gate.is_cuda and (cols == 1 or gate.stride(1) == 1), "gate must be a CUDA tensor with contiguous rows"
+    status = (_lib or load()).moe_combine_norm(
+        y.data_ptr(), _dtype_code(y, "y"), _row_stride(y, rows, H, "y"), slots, 0 if post_w is None else 1,
+        None if post_w is None else post_w.data_ptr(), None if pre_w is None else pre_w.data_ptr(), w_type, w_offset, eps,
+        gp, gt, ldg, cols, _GATES[gate_act], hp, ldh, alpha, beta, hop, ht if hp is not None else hot, ldho, np_, nt, ldn,
+        T, H, _raw_stream(stream, y))
+    if status:
+        raise MoeError(status, "moe_combine_norm")
+    return h_out, n_out
