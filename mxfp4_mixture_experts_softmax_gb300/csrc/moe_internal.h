@@ -345,7 +345,7 @@ struct RouteGrouped {
     float scale;
     int32_t* ids;           // [T][K + shared]
     float* w;
-    int lanes;              // lanes a group (set by the launcher)
+    int group_size, lanes_log2;  // experts and (log2 of the) lanes a group; set by the launcher
 };
 cudaError_t launch_route_grouped(const RouteGrouped& p, cudaStream_t s);
 

@@ -86,12 +86,27 @@ def test_against_the_definition(m, score, biased, T, E, K, G, chosen, top):
     check(m, logits, K, bias, score, G, chosen, top, renormalize=False, scale=2.5)
 
 
+MANY = [  # long batches, several tokens a warp where K, E and the groups allow it
+    (4096, 256, 8, 8, 4, 2), (4099, 512, 10, 1, 1, 1), (5001, 64, 6, 1, 1, 1), (4097, 128, 16, 16, 9, 2), (4200, 96, 4, 3, 2, 1),
+    (6002, 16, 8, 2, 1, 2), (4111, 512, 16, 8, 2, 2), (4098, 256, 8, 1, 1, 2), (4100, 60, 3, 5, 2, 1), (4101, 128, 8, 2, 1, 1),
+    (4103, 1024, 8, 1, 1, 1), (4105, 64, 12, 32, 20, 1), (4104, 36, 8, 1, 1, 1), (4106, 32, 1, 8, 1, 2), (4107, 500, 16, 1, 1, 1),
+]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("T,E,K,G,chosen,top", MANY)
+def test_long_batches(m, score, biased, T, E, K, G, chosen, top):
+    test_against_the_definition(m, score, biased, T, E, K, G, chosen, top)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("G,chosen,top", [(1, 1, 1), (8, 4, 2), (8, 3, 1)])
-def test_equal_and_nearly_equal_values(m, score, G, chosen, top):
+@pytest.mark.parametrize("T", [200, 4200])
+def test_equal_and_nearly_equal_values(m, score, G, chosen, top, T):
     """Values that round to one another in fp32, and exact ties."""
     rng = np.random.default_rng(3)
-    T, E, K = 200, 64, 8
+    E, K = 64, 8
     for bias in (None, np.zeros(E, np.float32), np.full(E, 0.37, np.float32)):
         check(m, np.zeros((T, E), np.float32), K, bias, score, G, chosen, top)
         # few different logits: ties everywhere
@@ -109,9 +124,10 @@ def test_equal_and_nearly_equal_values(m, score, G, chosen, top):
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
-def test_masked_experts_and_wide_ranges(m, score):
+@pytest.mark.parametrize("T", [50, 4100])
+def test_masked_experts_and_wide_ranges(m, score, T):
     rng = np.random.default_rng(4)
-    T, E, K = 50, 128, 6
+    E, K = 128, 6
     bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
     logits = (20.0 * rng.standard_normal((T, E))).astype(np.float32)
     logits[:, ::3] = -np.inf
@@ -128,18 +144,19 @@ def test_masked_experts_and_wide_ranges(m, score):
     check(m, low, 2, None, score)
 
 
-def test_what_is_not_a_number(m):
+@pytest.mark.parametrize("T", [40, 4100])
+def test_what_is_not_a_number(m, T):
     """NaN counts as -inf; ids stay distinct and in range whatever the values are."""
     rng = np.random.default_rng(5)
-    logits = rng.standard_normal((40, 64)).astype(np.float32)
+    logits = rng.standard_normal((T, 64)).astype(np.float32)
     plain = logits.copy()
-    logits[rng.random((40, 64)) < 0.3] = np.nan
+    logits[rng.random((T, 64)) < 0.3] = np.nan
     plain[np.isnan(logits)] = -np.inf
     for score in ("sigmoid", "softmax"):
         a = m.moe_route_grouped(torch.from_numpy(logits).cuda(), 8, None, score, 8, 4, 2)
         b = m.moe_route_grouped(torch.from_numpy(plain).cuda(), 8, None, score, 8, 4, 2)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
-        wild = rng.choice(np.array([np.nan, np.inf, -np.inf, 0.0, 3e38, -3e38], np.float32), (200, 64))
+        wild = rng.choice(np.array([np.nan, np.inf, -np.inf, 0.0, 3e38, -3e38], np.float32), (160 + T, 64))
         bias = rng.choice(np.array([np.nan, np.inf, -np.inf, 0.0, 1.0], np.float32), 64)
         for bb in (None, bias):
             for G, chosen, top in ((1, 1, 1), (8, 4, 2), (16, 9, 1)):
@@ -150,11 +167,12 @@ def test_what_is_not_a_number(m):
 
 
 @pytest.mark.parametrize("pad", [0, 3, 8])
-def test_bf16_rows_and_slices(m, pad):
+@pytest.mark.parametrize("T", [70, 4200])
+def test_bf16_rows_and_slices(m, pad, T):
     rng = np.random.default_rng(6)
-    wide = torch.from_numpy(rng.standard_normal((70, 96 + pad)).astype(np.float32)).cuda()
+    wide = torch.from_numpy(rng.standard_normal((T, 96 + pad)).astype(np.float32)).cuda()
     bias = torch.from_numpy((0.1 * rng.standard_normal(96)).astype(np.float32)).cuda()
-    for rows in (wide[:, pad:], wide.bfloat16()[:, pad:], wide[:1].expand(70, -1)[:, :96], wide.bfloat16()[3:4, pad // 2:]):
+    for rows in (wide[:, pad:], wide.bfloat16()[:, pad:], wide[:1].expand(T, -1)[:, :96], wide.bfloat16()[3:4, pad // 2:]):
         rows = rows[:, :96]
         ids, w = m.moe_route_grouped(rows, 6, bias, "sigmoid", 8, 4, 2, with_shared=False)
         want, ww = definition(rows.float().cpu().numpy(), 6, bias.cpu().numpy(), "sigmoid", 8, 4, 2)
