@@ -9,12 +9,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "lib", "libmoe.so")
+PYCALL = os.path.join(HERE, "lib", "_pycall.so")
 SOURCES = ["moe_api.cu", "route.cu", "permute.cu", "ffn_decode.cu", "ffn_prefill.cu",
            "ffn_mxfp4act.cu", "ffn_fp8x2.cu", "linear_mxfp4.cu", "layer_few.cu",
            "moe_noalloc.cu", "route_grouped.cu", "lora.cu", "combine_norm.cu"]
@@ -37,7 +39,25 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_pycall(force: bool = False) -> str:
+    """The CPython wrappers of the binding (pycall.c), with the system's C compiler."""
+    src = os.path.join(CSRC, "pycall.c")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(ROOT, "include", "moe.h")))
+    if not force and os.path.exists(PYCALL) and os.path.getmtime(PYCALL) >= newest:
+        return PYCALL
+    os.makedirs(os.path.dirname(PYCALL), exist_ok=True)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = PYCALL + f".tmp{os.getpid()}"
+    r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+                        "-I", cuda, src, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the C compiler failed on pycall.c:\n{r.stderr}")
+    os.replace(tmp, PYCALL)
+    return PYCALL
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    build_pycall(force)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -9,6 +9,8 @@
 // its rounding to h_out.  The row stays in registers, so each value is read and
 // written once and the kernel is bound by HBM where there are many tokens, by
 // latency (launch, the loads, one or two block sums) where there are few.
+#include <algorithm>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -68,11 +70,10 @@ __device__ __forceinline__ void store_values(void* p, int f32, long long i, cons
     }
 }
 
-// The sum over the block's threads, the same on each of them: warps in order.
-__device__ __forceinline__ float block_sum(float v, float* slots) {
+// The sum over a row's threads, the same on each of them: one warp's, or the block's warps in order.
+__device__ __forceinline__ float row_sum(float v, int warps, float* slots) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    const int warps = blockDim.x >> 5;
     if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -89,37 +90,44 @@ __device__ __forceinline__ float gate_of(float z, int act) {
     return act == 1 ? s : z * s;
 }
 
-// Thread i of the block has the chunks i, i + threads, ... of V values.
+// One row at a time: thread i of its p.row_warps warps has the chunks i, i + threads, ... of V values.
+// Rows of one warp share a block of up to 8.
 template <int V, int CH>
 __global__ void __launch_bounds__(1024) combine_norm_kernel(const __grid_constant__ CombineNorm p) {
     __shared__ float sums[2][32];
     pdl_begin();
-    const long long t = blockIdx.x;
-    const int step = blockDim.x * V, c0 = threadIdx.x * V;
+    const int threads = p.row_warps * 32, rank = p.row_warps == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const long long t = p.row_warps == 1 ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (t >= p.T) return;
+    const int step = threads * V, c0 = rank * V;
     float u[CH][V], h[CH][V];
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int k = 0; k < V; ++k) u[i][k] = h[i][k] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-        if (c0 + i * step < p.H) load_values<V>(p.y, p.y_f32, t * p.slots * p.ldy + c0 + i * step, u[i]);
     if (p.h) {
 #pragma unroll
         for (int i = 0; i < CH; ++i)
             if (c0 + i * step < p.H) load_values<V>(p.h, p.h_f32, t * p.ldh + c0 + i * step, h[i]);
     }
-    for (int j = 1; j < p.slots; ++j) {
-        float v[CH][V];
+    // the slots in order, the loads of several together
+    constexpr int kAhead = V * CH >= 16 ? 2 : 4;
+    for (int j = 0; j < p.slots; j += kAhead) {
+        float v[kAhead][CH][V];
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (c0 + i * step < p.H) load_values<V>(p.y, p.y_f32, (t * p.slots + j) * p.ldy + c0 + i * step, v[i]);
+        for (int a = 0; a < kAhead; ++a)
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (c0 + i * step < p.H) {
+            for (int i = 0; i < CH; ++i)
+                if (j + a < p.slots && c0 + i * step < p.H)
+                    load_values<V>(p.y, p.y_f32, (t * p.slots + j + a) * p.ldy + c0 + i * step, v[a][i]);
 #pragma unroll
-                for (int k = 0; k < V; ++k) u[i][k] += v[i][k];
-            }
+        for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                if (j + a < p.slots && c0 + i * step < p.H) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) u[i][k] += v[a][i][k];
+                }
     }
     const float inv = 1.0f / (float)p.H;
     if (p.post) {
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(const __grid_constan
         for (int i = 0; i < CH; ++i)
 #pragma unroll
             for (int k = 0; k < V; ++k) q += u[i][k] * u[i][k];
-        const float r = 1.0f / sqrtf(block_sum(q, sums[0]) * inv + p.eps);
+        const float r = rsqrtf(row_sum(q, p.row_warps, sums[0]) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < CH; ++i)
             if (c0 + i * step < p.H) {
@@ -173,7 +181,7 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(const __grid_constan
             if (c0 + i * step < p.H) store_values<V>(p.h_out, p.h_f32, t * p.ldho + c0 + i * step, u[i]);
     }
     if (p.n_out) {
-        const float r = 1.0f / sqrtf(block_sum(q, sums[1]) * inv + p.eps);
+        const float r = rsqrtf(row_sum(q, p.row_warps, sums[1]) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < CH; ++i)
             if (c0 + i * step < p.H) {
@@ -187,10 +195,340 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(const __grid_constan
     pdl_end();
 }
 
+// Eight values as they lie in memory.
+template <bool F32>
+struct Raw {
+    uint4 w[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* p, long long i) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (F32 ? 4 : 2));
+#pragma unroll
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) w[k] = q[k];
+    }
+    __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) {
+            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (F32) {
+                    v[4 * k + j] = __uint_as_float(x[j]);
+                } else {
+                    v[2 * j] = __uint_as_float(x[j] << 16);
+                    v[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+};
+
+// The sum over a block of up to 16 warps, in order; slots behind the last warp's hold 0.
+__device__ __forceinline__ float block_sum(float v, int warps, float* slots) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int w = 0; w < warps; w += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(slots + w);
+        v += (s.x + s.y) + (s.z + s.w);
+    }
+    return v;
+}
+
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// factors[i] = alpha times the weight after the block times a gate that all rows share (if there
+// is one: returned), factors[H + i] = the weight before the next block.  The caller synchronises.
+__device__ __forceinline__ bool fill_factors(const CombineNorm& p, float* factors) {
+    const bool shared_gate = p.gate && p.gate_cols != 1 && p.ldg == 0;
+    for (int i = 8 * threadIdx.x; i < p.H; i += 8 * blockDim.x) {
+        float f[8], w[8], v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = p.alpha, w[k] = 1.0f;
+        if (p.post) {
+            load_values<8>(p.post_w, p.w_f32, i, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= v[k] + p.w_offset;
+        }
+        if (shared_gate) {
+            load_values<8>(p.gate, p.gate_f32, i, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= gate_of(v[k], p.act);
+        }
+        if (p.pre_w) {
+            load_values<8>(p.pre_w, p.w_f32, i, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = v[k] + p.w_offset;
+        }
+        store_values<8>(factors, 1, i, f);
+        store_values<8>(factors + p.H, 1, i, w);
+    }
+    return shared_gate;
+}
+
+// Many short rows (up to 512 values), no slots.  A row has `lanes` lanes of a warp (8 to 32), and a
+// thread two times 8 neighbouring values of it; rows are taken in turn, the next one's y and h loaded
+// before the work on this one.  What is the same for every row -- alpha, the weights after the
+// block and a gate that all rows share, as one factor, and the weights before the next one -- lies
+// in shared memory.
+constexpr int kShortRow = 512, kShortThreads = 256;
+template <bool YF, bool HF>
+__global__ void __launch_bounds__(kShortThreads) combine_norm_short_kernel(const __grid_constant__ CombineNorm p) {
+    extern __shared__ __align__(16) float factors[];  // [2][H]
+    pdl_begin();
+    const int lanes = p.row_lanes, rows = kShortThreads / lanes, rank = threadIdx.x & (lanes - 1);
+    const bool shared_gate = fill_factors(p, factors);
+    __syncthreads();
+
+    const int c[2] = {8 * rank, 8 * (rank + lanes)};
+    const bool in[2] = {c[0] < p.H, c[1] < p.H};
+    long long t = (long long)blockIdx.x * rows + threadIdx.x / lanes;
+    const long long step = (long long)gridDim.x * rows;
+    // (the rows of a block end their turns together: a warp's meet in the sums)
+    const long long last = ((long long)p.T + rows - 1) / rows * rows;
+    Raw<YF> y[2];
+    Raw<HF> h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int k = 0; k < (YF ? 2 : 1); ++k) y[i].w[k] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < (HF ? 2 : 1); ++k) h[i].w[k] = make_uint4(0, 0, 0, 0);
+        if (in[i] && t < p.T) {
+            y[i].load(p.y, t * p.ldy + c[i]);
+            if (p.h) h[i].load(p.h, t * p.ldh + c[i]);
+        }
+    }
+    const float inv = 1.0f / (float)p.H;
+    for (; t < last; t += step) {
+        const bool live = t < p.T;
+        float u[2][8];
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            y[i].get(u[i]);
+            if (in[i] && t + step < p.T) y[i].load(p.y, (t + step) * p.ldy + c[i]);
+        }
+        float f = 1.0f;
+        if (p.post) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) q += u[i][k] * u[i][k];
+            f = rsqrtf(lanes_sum(q, lanes) * inv + p.eps);
+        }
+        if (p.gate && !shared_gate && live) {
+            if (p.gate_cols == 1) {
+                float z;
+                load_values<1>(p.gate, p.gate_f32, t * p.ldg, &z);
+                f *= gate_of(z, p.act);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (in[i]) {
+                        float z[8];
+                        load_values<8>(p.gate, p.gate_f32, t * p.ldg + c[i], z);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) u[i][k] *= gate_of(z[k], p.act);
+                    }
+            }
+        }
+        q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float r[8];
+            h[i].get(r);
+            if (p.h && in[i] && t + step < p.T) h[i].load(p.h, (t + step) * p.ldh + c[i]);
+            if (in[i]) {
+                const float4 a = *reinterpret_cast<const float4*>(factors + c[i]), b = *reinterpret_cast<const float4*>(factors + c[i] + 4);
+                const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    u[i][k] = p.h ? p.beta * r[k] + u[i][k] * f * w[k] : u[i][k] * f * w[k];
+                    q += u[i][k] * u[i][k];
+                }
+                if (p.h_out && live) store_values<8>(p.h_out, p.h_f32, t * p.ldho + c[i], u[i]);
+            }
+        }
+        if (p.n_out) {
+            const float g = rsqrtf(lanes_sum(q, lanes) * inv + p.eps);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (in[i]) {
+                    const float4 a = *reinterpret_cast<const float4*>(factors + p.H + c[i]),
+                                 b = *reinterpret_cast<const float4*>(factors + p.H + c[i] + 4);
+                    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) u[i][k] = u[i][k] * g * w[k];
+                    if (live) store_values<8>(p.n_out, p.n_f32, t * p.ldn + c[i], u[i]);
+                }
+        }
+    }
+    pdl_end();
+}
+
+// Many longer rows, no slots.  A block takes rows in turn; one thread keeps the next rows' y, h and
+// gate coming as bulk copies into a ring of p.stages in shared memory, so that HBM always has whole rows
+// of every block outstanding (with the next row in registers instead: 62 us for 8192 rows of 4096 with
+// norms on both sides, a row a block without turns: 76).  A thread has the chunks i and i + threads
+// of 8 values.
+constexpr int kStreamThreads = 512;
+template <bool YF, bool HF>
+__global__ void __launch_bounds__(kStreamThreads) combine_norm_stream_kernel(const __grid_constant__ CombineNorm p) {
+    extern __shared__ __align__(16) float factors[];  // [2][H], then the ring
+    __shared__ __align__(16) float sums[2][2][16];
+    __shared__ __align__(8) uint64_t full[kCombineNormStages];
+    pdl_begin();
+    const int warps = blockDim.x >> 5;
+    const uint32_t y_bytes = p.H * (YF ? 4 : 2), h_bytes = p.h ? p.H * (HF ? 4 : 2) : 0;
+    const bool full_gate = p.gate && p.gate_cols != 1 && p.ldg != 0;
+    const uint32_t g_bytes = full_gate ? p.H * (p.gate_f32 ? 4 : 2) : 0, stage_bytes = y_bytes + h_bytes + g_bytes;
+    uint8_t* ring = reinterpret_cast<uint8_t*>(factors + 2 * p.H);
+    if (threadIdx.x < 64) (&sums[0][0][0])[threadIdx.x] = 0.0f;
+    const auto fetch = [&](long long t, int stage) {
+        uint8_t* to = ring + (size_t)stage * stage_bytes;
+        mbar_arrive_expect_tx(&full[stage], stage_bytes);
+        bulk_copy_g2s(smem_u32(to), static_cast<const uint8_t*>(p.y) + t * p.ldy * (YF ? 4 : 2), y_bytes, &full[stage]);
+        if (h_bytes)
+            bulk_copy_g2s(smem_u32(to + y_bytes), static_cast<const uint8_t*>(p.h) + t * p.ldh * (HF ? 4 : 2), h_bytes, &full[stage]);
+        if (g_bytes)
+            bulk_copy_g2s(smem_u32(to + y_bytes + h_bytes),
+                          static_cast<const uint8_t*>(p.gate) + t * p.ldg * (p.gate_f32 ? 4 : 2), g_bytes, &full[stage]);
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) mbar_init(&full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int i = 0; i < p.stages; ++i) {
+            const long long t = blockIdx.x + (long long)i * gridDim.x;
+            if (t < p.T) fetch(t, i);
+        }
+    }
+    __syncwarp();
+    const bool shared_gate = fill_factors(p, factors);
+    __syncthreads();
+
+    const int c[2] = {8 * (int)threadIdx.x, 8 * (int)(threadIdx.x + blockDim.x)};
+    const bool in[2] = {c[0] < p.H, c[1] < p.H};
+    const float inv = 1.0f / (float)p.H;
+    int stage = 0, parity = 0, turn = 0;
+    for (long long t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+        // (a wait that gave up has raised the error flag; the row is then not what it should be, and the
+        // block goes on so that its threads stay together)
+        mbar_wait(&full[stage], parity);
+        const uint8_t* from = ring + (size_t)stage * stage_bytes;
+        float u[2][8], r[2][8];
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[i][k] = r[i][k] = 0.0f;
+            if (in[i]) {
+                load_values<8>(from, YF, c[i], u[i]);
+                if (h_bytes) load_values<8>(from + y_bytes, HF, c[i], r[i]);
+            }
+        }
+        float f = 1.0f;
+        if (p.post) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) q += u[i][k] * u[i][k];
+            f = rsqrtf(block_sum(q, warps, sums[turn][0]) * inv + p.eps);
+        }
+        if (full_gate) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (in[i]) {
+                    float z[8];
+                    load_values<8>(from + y_bytes + h_bytes, p.gate_f32, c[i], z);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) u[i][k] *= gate_of(z[k], p.act);
+                }
+        } else if (p.gate && !shared_gate) {
+            float z;
+            load_values<1>(p.gate, p.gate_f32, t * p.ldg, &z);
+            f *= gate_of(z, p.act);
+        }
+        q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (in[i]) {
+                float w[8];
+                load_values<8>(factors, 1, c[i], w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    u[i][k] = h_bytes ? p.beta * r[i][k] + u[i][k] * f * w[k] : u[i][k] * f * w[k];
+                    q += u[i][k] * u[i][k];
+                }
+            }
+        // (every thread is past its reads of the stage when the sum is done)
+        const float g = rsqrtf(block_sum(q, warps, sums[turn][1]) * inv + p.eps);
+        if (threadIdx.x == 0 && t + (long long)p.stages * gridDim.x < p.T) fetch(t + (long long)p.stages * gridDim.x, stage);
+        if (++stage == p.stages) stage = 0, parity ^= 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (in[i]) {
+                if (p.h_out) store_values<8>(p.h_out, p.h_f32, t * p.ldho + c[i], u[i]);
+                if (p.n_out) {
+                    float w[8];
+                    load_values<8>(factors + p.H, 1, c[i], w);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) u[i][k] = u[i][k] * g * w[k];
+                    store_values<8>(p.n_out, p.n_f32, t * p.ldn + c[i], u[i]);
+                }
+            }
+    }
+    pdl_end();
+}
+
 template <int V, int CH>
-cudaError_t launch(const CombineNorm& p, cudaStream_t s) {
-    const int threads = ((p.H + V * CH - 1) / (V * CH) + 31) / 32 * 32;
-    return launch_pdl(combine_norm_kernel<V, CH>, dim3(p.T), dim3(threads), 0, s, p);
+cudaError_t launch(CombineNorm p, cudaStream_t s) {
+    p.row_warps = ((p.H + V * CH - 1) / (V * CH) + 31) / 32;
+    const int rows = p.row_warps == 1 ? std::min(8, p.T) : 1;
+    return launch_pdl(combine_norm_kernel<V, CH>, dim3((unsigned)(((long long)p.T + rows - 1) / rows)),
+                      dim3(p.row_warps * 32 * rows), 0, s, p);
+}
+
+template <bool YF, bool HF>
+cudaError_t launch_short(CombineNorm p, cudaStream_t s) {
+    p.row_lanes = 8;
+    while (16 * p.row_lanes < p.H) p.row_lanes *= 2;
+    const int rows = kShortThreads / p.row_lanes;
+    const long long blocks = std::min<long long>(num_sms() * 4LL, ((long long)p.T + rows - 1) / rows);
+    return launch_pdl(combine_norm_short_kernel<YF, HF>, dim3((unsigned)blocks), dim3(kShortThreads), 2 * sizeof(float) * p.H, s, p);
+}
+
+// The stream kernel's threads, blocks an SM and stages for these rows: up to 1024 threads an SM, as
+// long as two stages fit each block, and the ring takes what is left.  0 stages: they do not fit.
+struct StreamShape {
+    int threads, per_sm, stages;
+    size_t smem;
+};
+StreamShape stream_shape(const CombineNorm& p) {
+    const bool full_gate = p.gate && p.gate_cols != 1 && p.ldg != 0;
+    const size_t stage = (size_t)p.H * ((p.y_f32 ? 4 : 2) + (p.h ? (p.h_f32 ? 4 : 2) : 0) + (full_gate ? (p.gate_f32 ? 4 : 2) : 0));
+    const size_t factors = 2 * sizeof(float) * p.H, most = 220 * 1024, fixed = 1024;  // a block's own 1 KB
+    StreamShape r;
+    r.threads = ((p.H / 8 + 1) / 2 + 31) / 32 * 32;
+    r.per_sm = std::max(1, 1024 / r.threads);
+    while (r.per_sm > 1 && (factors + 2 * stage + fixed) * r.per_sm > most) --r.per_sm;
+    const size_t room = most / r.per_sm - fixed;
+    r.stages = factors + 2 * stage > room ? 0 : (int)std::min<size_t>(kCombineNormStages, (room - factors) / stage);
+    r.smem = factors + r.stages * stage;
+    return r;
+}
+
+template <bool YF, bool HF>
+cudaError_t launch_stream(CombineNorm p, const StreamShape& shape, cudaStream_t s) {
+    const auto kernel = combine_norm_stream_kernel<YF, HF>;
+    p.stages = shape.stages;
+    const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), shape.smem);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)num_sms() * shape.per_sm, p.T)), dim3(shape.threads),
+                      shape.smem, s, p);
 }
 
 // Whether rows of this type, `ld` elements apart, can be read V values at a time.
@@ -209,9 +547,33 @@ bool vectors(const CombineNorm& p, int V) {
 }  // namespace
 
 cudaError_t launch_combine_norm(const CombineNorm& p, cudaStream_t s) {
-    if (vectors(p, 8)) return p.H <= 256 ? launch<8, 1>(p, s) : launch<8, 2>(p, s);
-    if (vectors(p, 4)) return p.H <= 512 ? launch<4, 2>(p, s) : launch<4, 4>(p, s);
-    return p.H <= 1024 ? launch<1, 4>(p, s) : launch<1, 16>(p, s);
+    if (vectors(p, 8)) {
+        // without slots and with rows for several turns of every block
+        if (p.slots == 1 && (long long)p.T * p.H >= 2LL * 16 * 1024 * num_sms()) {
+            if (p.H <= kShortRow) {
+                if (p.y_f32) return p.h_f32 ? launch_short<true, true>(p, s) : launch_short<true, false>(p, s);
+                return p.h_f32 ? launch_short<false, true>(p, s) : launch_short<false, false>(p, s);
+            }
+            const StreamShape shape = stream_shape(p);
+            if (p.H <= 16 * kStreamThreads && shape.stages > 0) {
+                if (p.y_f32) return p.h_f32 ? launch_stream<true, true>(p, shape, s) : launch_stream<true, false>(p, shape, s);
+                return p.h_f32 ? launch_stream<false, true>(p, shape, s) : launch_stream<false, false>(p, shape, s);
+            }
+        }
+        return p.H <= 8192 ? launch<8, 1>(p, s) : launch<8, 2>(p, s);
+    }
+    if (vectors(p, 4)) return p.H <= 4096 ? launch<4, 1>(p, s) : launch<4, 4>(p, s);
+    return p.H <= 4096 ? launch<1, 4>(p, s) : launch<1, 16>(p, s);
+}
+
+cudaError_t read_device_error_norm(int* flag, int clear) {
+    int wait = 0;
+    cudaError_t err = cudaMemcpyFromSymbol(&wait, g_device_error, sizeof(int));
+    if (err != cudaSuccess) return err;
+    *flag = wait ? 1 : 0;
+    if (!clear) return cudaSuccess;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
 }
 
 }  // namespace moe

@@ -223,9 +223,10 @@ moe_status_t moe_device_error(int* flag, int clear) {
     int f = 0;
     if (err == cudaSuccess) err = read_device_error_linear(&e, clear);
     if (err == cudaSuccess) err = read_device_error_few(&f, clear);
-    int g = 0;
+    int g = 0, h = 0;
     if (err == cudaSuccess) err = read_device_error_lora(&g, clear);
-    *flag = a | b | c | d | e | f | g;
+    if (err == cudaSuccess) err = read_device_error_norm(&h, clear);
+    *flag = a | b | c | d | e | f | g | h;
     return cuda_status(err);
 }
 

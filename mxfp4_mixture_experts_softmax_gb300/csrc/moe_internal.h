@@ -376,7 +376,7 @@ cudaError_t launch_lora(const Lora& p, cudaStream_t s);
 cudaError_t read_device_error_lora(int* flag, int clear);
 
 // Sum over a token's slots, norms, gate and residual (combine_norm.cu).
-constexpr int kCombineNormMaxH = 16384;
+constexpr int kCombineNormMaxH = 16384, kCombineNormStages = 6;
 struct CombineNorm {
     const void* y;           // [T * slots] rows of H values, ldy elements apart
     int y_f32;
@@ -401,8 +401,10 @@ struct CombineNorm {
     int n_f32;
     long long ldn;
     int T, H;
+    int row_warps, row_lanes, stages;  // set by the launcher
 };
 cudaError_t launch_combine_norm(const CombineNorm& p, cudaStream_t s);
+cudaError_t read_device_error_norm(int* flag, int clear);
 
 // grouping of one dense expert over T tokens (Kt = 1); ones[T] = 1 if given
 cudaError_t launch_identity_perm(int T, int tile_m, int cap, int max_tiles, int32_t* sorted_pairs,

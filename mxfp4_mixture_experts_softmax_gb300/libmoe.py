@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -178,6 +179,13 @@ def load(build: bool = True):
         L.moe_combine_norm.restype = ci
         L.moe_device_error.argtypes = [vp, ci]
         L.moe_device_error.restype = ci
+        # the same functions without ctypes' conversion of every argument (csrc/pycall.c)
+        spec = importlib.util.spec_from_file_location("_pycall", build_lib.PYCALL)
+        direct = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(direct)
+        for name in ("moe_route_grouped", "moe_lora", "moe_combine_norm"):
+            direct.bind(name, ctypes.cast(getattr(L, name), vp).value)
+            setattr(L, "direct_" + name, getattr(direct, name))
         _lib = L
         return L
 
@@ -774,6 +782,13 @@ def _dtype_code(t, what: str) -> int:
     return MOE_DTYPE_F32
 
 
+def _vector(t, n: int, dtype, what: str) -> int:
+    """The address of a contiguous CUDA tensor [n] of this type."""
+    assert t.is_cuda and t.is_contiguous() and t.dtype is dtype and t.shape == (n,), \
+        f"{what} must be a contiguous CUDA tensor of {dtype} [{n}]"
+    return t.data_ptr()
+
+
 def moe_route_grouped(logits, K: int, bias=None, score: str = "sigmoid", n_groups: int = 1, topk_groups: int = 1,
                       group_top: int = 2, with_shared: bool = True, renormalize: bool = True, scale: float = 1.0,
                       topk_ids=None, topk_w=None, shared_w=None, stream=None):
@@ -783,21 +798,19 @@ def moe_route_grouped(logits, K: int, bias=None, score: str = "sigmoid", n_group
     import torch
     T, E = logits.shape
     Kt = K + 1 if with_shared else K
-    with _on(stream, topk_ids, topk_w):
-        if topk_ids is None:
-            topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=logits.device)
-        if topk_w is None:
-            topk_w = torch.empty((T, Kt), dtype=torch.float32, device=logits.device)
-    for t, dt in ((topk_ids, torch.int32), (topk_w, torch.float32)):
-        assert t.is_cuda and t.is_contiguous() and t.dtype == dt and t.numel() == T * Kt, \
-            "topk_ids and topk_w must be contiguous int32 and float32 [T, Kt]"
-    for t, shape, what in ((bias, (E,), "bias"), (shared_w, (T,), "shared_w")):
-        if t is not None:
-            _dev(t, what)
-            assert t.dtype == torch.float32 and t.shape == shape, f"{what} must be float32 {shape}"
-    status = (_lib or load()).moe_route_grouped(
+    if topk_ids is None or topk_w is None:
+        with _on(stream):
+            if topk_ids is None:
+                topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=logits.device)
+            if topk_w is None:
+                topk_w = torch.empty((T, Kt), dtype=torch.float32, device=logits.device)
+    assert topk_ids.is_cuda and topk_ids.is_contiguous() and topk_ids.dtype is torch.int32 and topk_ids.numel() == T * Kt \
+        and topk_w.is_cuda and topk_w.is_contiguous() and topk_w.dtype is torch.float32 and topk_w.numel() == T * Kt, \
+        "topk_ids and topk_w must be contiguous CUDA tensors of int32 and float32 [T, Kt]"
+    status = (_lib or load()).direct_moe_route_grouped(
         logits.data_ptr(), _dtype_code(logits, "logits"), _row_stride(logits, T, E, "logits"),
-        None if bias is None else bias.data_ptr(), None if shared_w is None else shared_w.data_ptr(), T, E, K,
+        None if bias is None else _vector(bias, E, torch.float32, "bias"),
+        None if shared_w is None else _vector(shared_w, T, torch.float32, "shared_w"), T, E, K,
         _SCORES[score], n_groups, topk_groups, group_top, 1 if with_shared else 0, 1 if renormalize else 0, scale,
         topk_ids.data_ptr(), topk_w.data_ptr(), _raw_stream(stream, logits))
     if status:
@@ -824,28 +837,25 @@ def moe_lora(x, a, b, plan: dict, scale=None, ranks=None, residual=None, out=Non
     import torch
     T, K = x.shape
     n, N, R = b.shape
+    bf16 = torch.bfloat16
     assert plan["T"] == T and plan["Kt"] == 1 and plan["Et"] == n, "plan does not match x and the adapters"
-    assert a.shape == (n, R, K) and a.dtype == b.dtype == torch.bfloat16, "a and b must be bfloat16 [n, R, K] and [n, N, R]"
-    _dev(a, "a")
-    _dev(b, "b")
-    for t, dt, what in ((scale, torch.float32, "scale"), (ranks, torch.int32, "ranks")):
-        if t is not None:
-            _dev(t, what)
-            assert t.dtype == dt and t.shape == (n,), f"{what} must be {dt} [{n}]"
+    assert a.shape == (n, R, K) and a.dtype is bf16 and b.dtype is bf16, "a and b must be bfloat16 [n, R, K] and [n, N, R]"
+    assert a.is_cuda and a.is_contiguous() and b.is_cuda and b.is_contiguous(), "a and b must be contiguous CUDA tensors"
     if out is None:
         with _on(stream):
-            out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+            out = torch.empty((T, N), dtype=out_dtype or bf16, device=x.device)
         ldo = N
     else:
         assert out.shape == (T, N) and out_dtype in (None, out.dtype), "out must be [T, N]"
         ldo = _row_stride(out, T, N, "out")
     res, ldr = None, 0
     if residual is not None:
-        assert residual.shape == (T, N) and residual.dtype == out.dtype, "residual must match out"
+        assert residual.shape == (T, N) and residual.dtype is out.dtype, "residual must match out"
         res, ldr = residual.data_ptr(), _row_stride(residual, T, N, "residual")
-    status = (_lib or load()).moe_lora(
+    status = (_lib or load()).direct_moe_lora(
         x.data_ptr(), _dtype_code(x, "x"), _row_stride(x, T, K, "x"), a.data_ptr(), b.data_ptr(),
-        None if scale is None else scale.data_ptr(), None if ranks is None else ranks.data_ptr(),
+        None if scale is None else _vector(scale, n, torch.float32, "scale"),
+        None if ranks is None else _vector(ranks, n, torch.int32, "ranks"),
         plan["sorted_pairs"].data_ptr(), plan["inv_pairs"].data_ptr(), plan["tile_expert"].data_ptr(),
         plan["num_tiles"].data_ptr(), plan["tile_m"], n, res, ldr, out.data_ptr(), _dtype_code(out, "out"), ldo, T, N, K, R,
         _raw_stream(stream, x))
@@ -866,40 +876,39 @@ def moe_combine_norm(y, h=None, slots: int = 1, post_w=None, gate=None, gate_act
     rows, H = y.shape
     T = rows // slots
     assert T * slots == rows, "y must hold slots rows a token"
-    dev, bf16 = y.device, torch.bfloat16
-    with _on(stream, *(b if b is not False else 0 for b in (h_out, n_out))):
-        if h_out is None:
-            h_out = torch.empty((T, H), dtype=h.dtype if h is not None else h_dtype or bf16, device=dev)
-        if n_out is None:
-            n_out = torch.empty((T, H), dtype=n_dtype or bf16, device=dev)
-    args = []
-    for t, what in ((h, "h"), (h_out, "h_out"), (n_out, "n_out")):
-        if t is None or t is False:
-            args.append((None, 0, 0))
-        else:
-            assert t.shape == (T, H), f"{what} must be [T, H]"
-            args.append((t.data_ptr(), _dtype_code(t, what), _row_stride(t, T, H, what)))
-    (hp, ht, ldh), (hop, hot, ldho), (np_, nt, ldn) = args
-    assert hp is None or hop is None or ht == hot, "h_out must have h's type"
-    w_type = 0
-    for w, what in ((post_w, "post_w"), (pre_w, "pre_w")):
-        if w is not None:
-            _dev(w, what)
-            assert w.shape == (H,), f"{what} must be [H]"
-            w_type = _dtype_code(w, what)
-    assert post_w is None or pre_w is None or post_w.dtype == pre_w.dtype, "post_w and pre_w must have one type"
+    if h_out is None or n_out is None:
+        with _on(stream):
+            if h_out is None:
+                h_out = torch.empty((T, H), dtype=h.dtype if h is not None else h_dtype or torch.bfloat16, device=y.device)
+            if n_out is None:
+                n_out = torch.empty((T, H), dtype=n_dtype or torch.bfloat16, device=y.device)
+    shape = (T, H)
+    hp, ht, ldh, hop, ldho, np_, nt, ldn = None, 0, 0, None, 0, None, 0, 0
+    if h is not None:
+        assert h.shape == shape, "h must be [T, H]"
+        hp, ht, ldh = h.data_ptr(), _dtype_code(h, "h"), _row_stride(h, T, H, "h")
+    if h_out is not False:
+        assert h_out.shape == shape and (h is None or h_out.dtype is h.dtype), "h_out must be [T, H] of h's type"
+        hop, ht, ldho = h_out.data_ptr(), _dtype_code(h_out, "h_out"), _row_stride(h_out, T, H, "h_out")
+    if n_out is not False:
+        assert n_out.shape == shape, "n_out must be [T, H]"
+        np_, nt, ldn = n_out.data_ptr(), _dtype_code(n_out, "n_out"), _row_stride(n_out, T, H, "n_out")
+    w_type, pw, w = 0, None, None
+    if pre_w is not None:
+        w_type, w = _dtype_code(pre_w, "pre_w"), _vector(pre_w, H, pre_w.dtype, "pre_w")
+    if post_w is not None:
+        assert pre_w is None or pre_w.dtype is post_w.dtype, "post_w and pre_w must have one type"
+        w_type, pw = _dtype_code(post_w, "post_w"), _vector(post_w, H, post_w.dtype, "post_w")
     gp, gt, ldg, cols = None, 0, 0, 1
     if gate is not None:
         grows, cols = gate.shape
         assert grows in (1, T) and cols in (1, H), "gate must be [T or 1, H or 1]"
-        gp, gt = gate.data_ptr(), _dtype_code(gate, "gate")
-        ldg = 0 if grows == 1 else _row_stride(gate, T, cols, "gate")
-        assert gate.is_cuda and (cols == 1 or gate.stride(1) == 1), "gate must be a CUDA tensor with contiguous rows"
-    status = (_lib or load()).moe_combine_norm(
-        y.data_ptr(), _dtype_code(y, "y"), _row_stride(y, rows, H, "y"), slots, 0 if post_w is None else 1,
-        None if post_w is None else post_w.data_ptr(), None if pre_w is None else pre_w.data_ptr(), w_type, w_offset, eps,
-        gp, gt, ldg, cols, _GATES[gate_act], hp, ldh, alpha, beta, hop, ht if hp is not None else hot, ldho, np_, nt, ldn,
-        T, H, _raw_stream(stream, y))
+        gp, gt, ldg = gate.data_ptr(), _dtype_code(gate, "gate"), _row_stride(gate, grows, cols, "gate")
+        ldg = ldg if grows > 1 else 0
+    status = (_lib or load()).direct_moe_combine_norm(
+        y.data_ptr(), _dtype_code(y, "y"), _row_stride(y, rows, H, "y"), slots, 0 if pw is None else 1, pw, w, w_type, w_offset,
+        eps, gp, gt, ldg, cols, _GATES[gate_act], hp, ldh, alpha, beta, hop, ht, ldho, np_, nt, ldn, T, H,
+        _raw_stream(stream, y))
     if status:
         raise MoeError(status, "moe_combine_norm")
     return h_out, n_out

@@ -156,3 +156,31 @@ def test_bindings_refuse(recorded):  # noqa: F811
         m.moe_route_grouped(**dict(r, score="relu"), stream=SIDE)
     with pytest.raises(KeyError):
         m.moe_combine_norm(**n, gate_act="relu", stream=SIDE)
+
+
+def test_direct_calls_are_those_of_the_library(m):
+    """The wrappers that skip ctypes pass every argument on: the same refusals, in the same places."""
+    lib = m.load()
+    p, bad, shape = 0x1000, m.MOE_ERR_INVALID_ARG, m.MOE_ERR_UNSUPPORTED_SHAPE
+    route = [p, 1, 64, None, None, 4, 64, 8, 1, 8, 4, 2, 0, 1, 1.0, p, p, None]
+    lora = [p, 0, 64, p, p, None, None, p, p, p, p, 16, 4, None, 0, p, 0, 100, 4, 100, 64, 16, None]
+    norm = [p, 0, 64, 1, 0, None, p, 0, 0.0, 1e-6, None, 0, 0, 64, 0, p, 64, 1.0, 1.0, p, 0, 64, p, 0, 64, 4, 64, None]
+    for name, good, changes in (
+            ("moe_route_grouped", route, {0: None, 1: 2, 2: -1, 3: 2, 4: p, 5: -1, 6: 0, 7: 0, 8: 2, 9: 7, 10: 9, 11: 3,
+                                          15: None, 16: None}),
+            ("moe_lora", lora, {0: 1, 1: 2, 2: -1, 3: 8, 4: 8, 5: 1, 6: 1, 7: 1, 8: 1, 9: 1, 10: 1, 11: 8, 12: 1026, 13: 1,
+                                15: 1, 16: 2, 17: 99, 18: -1, 19: 0, 20: 60, 21: 12}),
+            ("moe_combine_norm", norm, {0: 1, 1: 2, 2: -1, 3: 65, 4: 1, 6: 1, 7: 2, 10: 1, 11: 2, 14: 3, 15: 1, 16: -1, 19: 1,
+                                        20: 2, 21: 63, 22: 1, 23: 2, 24: 63, 25: -1, 26: 0})):
+        direct, plain = getattr(lib, "direct_" + name), getattr(lib, name)
+        for i, v in changes.items():
+            args = list(good)
+            args[i] = v
+            want = plain(*args)
+            assert want in (bad, shape) and direct(*args) == want, (name, i)
+        with pytest.raises(TypeError):
+            direct(*good[:-1])
+        with pytest.raises((TypeError, OverflowError)):
+            direct(*[1 << 40 if isinstance(v, int) and v == 4 else v for v in good])
+        with pytest.raises(TypeError):
+            direct("x", *good[1:])

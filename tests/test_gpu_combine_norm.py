@@ -78,6 +78,18 @@ def test_norms_on_both_sides_and_gates(m, gate, act, H):
           alpha=0.3, beta=0.7, w_offset=1.0, eps=1e-3)
 
 
+@pytest.mark.parametrize("T,H", [(1300, 4096), (2600, 2088), (700, 8192), (20000, 128), (9001, 264), (40003, 64), (700, 8200)])
+@pytest.mark.parametrize("ydt,hdt", [(BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
+def test_many_rows(m, T, H, ydt, hdt):
+    torch.manual_seed(T)
+    y, h, pre, post = rows(T, H, ydt), rows(T, H, hdt, 8), rows(1, H, BF16)[0], rows(1, H, BF16)[0]
+    check(m, y, h=h, pre_w=pre)
+    check(m, y, h=h, post_w=post, pre_w=pre, gate=rows(1, H, BF16), gate_act="silu", alpha=0.5, beta=0.25, w_offset=1.0)
+    check(m, y, h=h, post_w=post, gate=rows(T, H, F32), gate_act="sigmoid")
+    check(m, y, post_w=post, pre_w=pre, gate=rows(T, 1, BF16), h_out=False)
+    check(m, y, h=h, gate=rows(1, 1, BF16), n_out=False)
+
+
 @pytest.mark.parametrize("slots", [1, 2, 9, 11, 64])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_slots(m, slots, dtype):
