@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "lib", "libmoe.so")
 PYCALL = os.path.join(HERE, "lib", "_pycall.so")
 SOURCES = ["moe_api.cu", "route.cu", "permute.cu", "ffn_decode.cu", "ffn_prefill.cu",
            "ffn_mxfp4act.cu", "ffn_fp8x2.cu", "linear_mxfp4.cu", "layer_few.cu",
-           "moe_noalloc.cu", "route_grouped.cu", "lora.cu", "combine_norm.cu"]
+           "moe_noalloc.cu", "route_grouped.cu", "lora.cu", "lora_prompt.cu",
+           "combine_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", os.path.join(ROOT, "include")]

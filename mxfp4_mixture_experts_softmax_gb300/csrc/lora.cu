@@ -19,7 +19,7 @@
 // v, a hundredth of the output's own rounding), three for fp32 (2^-24).
 #include <algorithm>
 
-#include "moe_internal.h"
+#include "lora_device.cuh"
 
 namespace moe {
 
@@ -41,18 +41,6 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
     return v;
-}
-
-// v = hi + the return value, hi the upper 16 bits (a bf16, exact); infinities and
-// NaN stay whole in hi.
-__device__ __forceinline__ float split_bf16(float v, uint32_t& hi) {
-    const uint32_t b = __float_as_uint(v);
-    if ((b & 0x7F800000u) == 0x7F800000u) {
-        hi = (b & 0x007FFFFFu) ? 0x7FC0u : b >> 16;
-        return 0.0f;
-    }
-    hi = b >> 16;
-    return v - __uint_as_float(b & 0xFFFF0000u);
 }
 
 // Eight fp32 values as three words-of-two-bf16 terms each: v = t[0] + t[1] + t[2] exactly.
@@ -196,59 +184,6 @@ __device__ __forceinline__ void shrink(const Lora& p, const uint16_t* a, int ran
         }
 }
 
-// Eight values of a row of `out`'s type from element n on; those from `count` on are not touched.
-__device__ __forceinline__ void load_out(const void* base, int f32, long long i, int count, bool wide, float* v) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-    if (f32) {
-        const float* q = static_cast<const float*>(base) + i;
-        if (wide && count >= 8) {
-            const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < count) v[k] = q[k];
-        }
-    } else {
-        const uint16_t* q = static_cast<const uint16_t*>(base) + i;
-        if (wide && count >= 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(q);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < count) v[k] = __uint_as_float((uint32_t)q[k] << 16);
-        }
-    }
-}
-
-__device__ __forceinline__ void store_out(void* base, int f32, long long i, int count, bool wide, const float* v) {
-    if (f32) {
-        float* q = static_cast<float*>(base) + i;
-        if (wide && count >= 8) {
-            *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < count) q[k] = v[k];
-        }
-    } else {
-        uint16_t* q = static_cast<uint16_t*>(base) + i;
-        if (wide && count >= 8)
-            *reinterpret_cast<uint4*>(q) = make_uint4(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]),
-                                                      f32x2_to_bf16x2_bits(v[4], v[5]), f32x2_to_bf16x2_bits(v[6], v[7]));
-        else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < count) q[k] = f32_to_bf16_bits(v[k]);
-        }
-    }
-}
-
 // out for this CTA's columns, 32 a warp at a time, all tokens of the tile.
 template <int MT, int RT, int TW>
 __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int rank, const int* tok, int cta, int ctas,
@@ -331,24 +266,6 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
     }
 }
 
-// Rows without an adapter among tokens [t0, t0 + kThreads): residual or zeros.  Each warp has 32 of
-// the tokens and takes every ctas-th of their rows.
-__device__ __forceinline__ void copy_rows(const Lora& p, int t0, int cta, int ctas) {
-    const int lane = threadIdx.x & 31, first = t0 + ((int)threadIdx.x & ~31);
-    const bool bare = first + lane < p.T && __ldg(p.inv_pairs + first + lane) < 0;
-    uint32_t rows = __ballot_sync(0xFFFFFFFFu, bare);
-    for (int turn = 0; rows; ++turn) {
-        const int t = first + __ffs((int)rows) - 1;
-        rows &= rows - 1;
-        if (turn % ctas != cta) continue;
-        for (int n = 8 * lane; n < p.N; n += 256) {
-            float v[8];
-            load_out(p.residual, p.out_f32, (long long)t * p.ldr + n, p.residual ? p.N - n : 0, p.res_wide, v);
-            store_out(p.out, p.out_f32, (long long)t * p.ldo + n, p.N - n, p.out_wide, v);
-        }
-    }
-}
-
 template <int MT, int RT, int TW, bool XF32>
 __global__ void __launch_bounds__(kThreads) lora_kernel(const __grid_constant__ Lora p) {
     using S = Shape<MT, RT, TW>;
@@ -357,17 +274,19 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const __grid_constant__ 
     pdl_begin();
     const int ctas = p.ctas, item = blockIdx.x / ctas, cta = blockIdx.x % ctas;
     if (item >= p.tiles) {
-        copy_rows(p, (item - p.tiles) * kThreads, cta, ctas);
+        copy_rows<kThreads>(p, (item - p.tiles) * kThreads, cta, ctas);
         pdl_end();
         return;
     }
     int used = __ldg(p.num_tiles);
-    if (used < 0 || used > p.tiles) {
+    if (used < 0 || used > p.tiles / (p.tile_m / S::kTokens)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) flag_index_error();
         used = 0;
     }
-    if (item >= used) return;
-    const int adapter = __ldg(p.tile_expert + item);
+    // a tile of 128 is taken as two
+    const int halves = p.tile_m / S::kTokens, tile = item / halves;
+    if (tile >= used) return;
+    const int adapter = __ldg(p.tile_expert + tile);
     if ((unsigned)adapter >= (unsigned)p.adapters) {
         if (threadIdx.x == 0) flag_index_error();
         return;
@@ -378,6 +297,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const __grid_constant__ 
     float* sum = part + S::kPartFloats;
     uint16_t* terms = reinterpret_cast<uint16_t*>(part);
     if (threadIdx.x < S::kTokens) {
+        // (positions follow one another from tile to tile)
         int q = __ldg(p.sorted_pairs + (size_t)item * S::kTokens + threadIdx.x);
         if (q >= p.T) {
             flag_index_error();
@@ -460,13 +380,13 @@ bool wide_rows(const void* p, int f32, long long ld) {
 
 }  // namespace
 
-bool lora_tile_supported(int tile_m) { return tile_m == 16 || tile_m == 32 || tile_m == 64; }
+bool lora_tile_supported(int tile_m) { return tile_m == 16 || tile_m == 32 || tile_m == 64 || tile_m == 128; }
 
 // Tile height: tokens that share an adapter share its reads, so the height follows the
 // tokens an adapter has on average, as long as there are tiles enough for the SMs.
 int lora_tile_rule(int T, int adapters) {
     const int each = T / std::max(1, std::min(T, adapters));
-    return each >= 64 && T >= 4096 ? 64 : each >= 32 && T >= 1024 ? 32 : 16;
+    return each >= 96 && T >= 1024 ? 128 : each >= 64 && T >= 4096 ? 64 : each >= 32 && T >= 1024 ? 32 : 16;
 }
 
 cudaError_t launch_lora(const Lora& given, cudaStream_t s) {
@@ -477,6 +397,8 @@ cudaError_t launch_lora(const Lora& given, cudaStream_t s) {
     p.x_wide = wide_rows(p.x, p.x_f32, p.ldx);
     p.res_wide = p.residual && wide_rows(p.residual, p.out_f32, p.ldr);
     p.out_wide = wide_rows(p.out, p.out_f32, p.ldo);
+    if (lora_prompt_supported(p)) return launch_lora_prompt(p, s);
+    if (p.tile_m == 128) p.tiles *= 2;
     // CTAs a tile: about two for each SM in all
     const int widest = std::max(p.K, p.N);
     p.ctas = 8;

@@ -223,10 +223,11 @@ moe_status_t moe_device_error(int* flag, int clear) {
     int f = 0;
     if (err == cudaSuccess) err = read_device_error_linear(&e, clear);
     if (err == cudaSuccess) err = read_device_error_few(&f, clear);
-    int g = 0, h = 0;
+    int g = 0, h = 0, i = 0;
     if (err == cudaSuccess) err = read_device_error_lora(&g, clear);
     if (err == cudaSuccess) err = read_device_error_norm(&h, clear);
-    *flag = a | b | c | d | e | f | g | h;
+    if (err == cudaSuccess) err = read_device_error_lora_prompt(&i, clear);
+    *flag = a | b | c | d | e | f | g | h | i;
     return cuda_status(err);
 }
 

@@ -374,6 +374,10 @@ bool lora_tile_supported(int tile_m);
 int lora_tile_rule(int T, int adapters);
 cudaError_t launch_lora(const Lora& p, cudaStream_t s);
 cudaError_t read_device_error_lora(int* flag, int clear);
+// the same for prompts: tiles of 128 tokens on the tcgen05 tensor cores (lora_prompt.cu)
+bool lora_prompt_supported(const Lora& p);
+cudaError_t launch_lora_prompt(const Lora& p, cudaStream_t s);
+cudaError_t read_device_error_lora_prompt(int* flag, int clear);
 
 // Sum over a token's slots, norms, gate and residual (combine_norm.cu).
 constexpr int kCombineNormMaxH = 16384, kCombineNormStages = 6;

@@ -49,7 +49,7 @@ def test_lora(m):
     assert call(T=-1) == bad and call(xt=2) == bad and call(ot=-1) == bad
     assert call(K=60) == shape and call(K=65544) == shape and call(R=12) == shape and call(R=136) == shape
     assert call(N=(1 << 24) + 1) == shape and call(T=(1 << 20) + 1) == shape and call(n=1026) == shape
-    for tile in (0, 8, 24, 128):
+    for tile in (0, 8, 24, 96, 256):
         assert call(tile=tile) == shape
     for name in ("x", "a", "b", "sp", "iv", "te", "nt", "out"):
         assert call(**{name: NUL}) == bad and call(**{name: ODD}) == bad, name
@@ -62,7 +62,7 @@ def test_lora(m):
 def test_lora_tile_heights(m):
     for T in (0, 1, 16, 100, 1000, 5000, 1 << 20):
         for n in (1, 7, 64, 1025):
-            assert m.moe_lora_tile_m(T, n) in (16, 32, 64)
+            assert m.moe_lora_tile_m(T, n) in (16, 32, 64, 128)
     assert m.load().moe_lora_tile_m(-1, 4) == 0 and m.load().moe_lora_tile_m(4, 0) == 0
 
 

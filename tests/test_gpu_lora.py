@@ -70,7 +70,7 @@ def ids_of(T, n, without=0.0, seed=0):
     (100, 7, 31, 2048, 32), (33, 4, 640, 136, 40), (257, 3, 96, 264, 64), (70, 70, 128, 128, 128), (300, 2, 72, 8192, 104),
     (1, 1, 1, 8, 8), (1100, 3, 264, 512, 16), (4200, 5, 136, 96, 64),
 ])
-@pytest.mark.parametrize("tile", [16, 32, 64])
+@pytest.mark.parametrize("tile", [16, 32, 64, 128])
 def test_against_the_formula(m, T, n, N, K, R, tile):
     torch.manual_seed(T + N)
     a, b, scale = adapters(n, N, K, R)
@@ -79,12 +79,30 @@ def test_against_the_formula(m, T, n, N, K, R, tile):
 
 @pytest.mark.parametrize("x,out", [(BF16, F32), (F32, BF16), (F32, F32)])
 @pytest.mark.parametrize("R", [8, 16, 24, 32, 64, 128])
-@pytest.mark.parametrize("tile", [16, 32, 64])
+@pytest.mark.parametrize("tile", [16, 32, 64, 128])
 def test_types_and_ranks(m, x, out, R, tile):
     torch.manual_seed(R)
     a, b, scale = adapters(3, 200, 320, R)
     check(m, rows(90, 320, x), a, b, ids_of(90, 3), tile, scale, residual=rows(90, 200, out), out_dtype=out)
     check(m, rows(90, 320, x), a, b, ids_of(90, 3), tile, out_dtype=out)
+
+
+@pytest.mark.parametrize("T,n,N,K,R", [
+    (128, 1, 128, 64, 16), (1, 1, 8, 8, 8), (129, 1, 64, 128, 64), (300, 3, 1032, 1032, 8), (500, 2, 4096, 4096, 64),
+    (1000, 5, 136, 2048, 128), (2100, 3, 2048, 520, 40), (777, 40, 320, 256, 24), (256, 2, 8192, 16, 96), (640, 1, 16, 8192, 104),
+    (3000, 2, 72, 72, 120), (130, 2, 1024, 4104, 48),
+])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_prompts(m, T, n, N, K, R, out):
+    """Tiles of 128 tokens, with tokens of one adapter together and apart, and without one."""
+    torch.manual_seed(T)
+    a, b, scale = adapters(n, N, K, R)
+    x, res = rows(T, K, BF16, 8), rows(T, N, out, 8, 8)
+    for ids in (ids_of(T, n, 0.1), ids_of(T, n).sort()[0]):
+        got, plan = check(m, x, a, b, ids, 128, scale, residual=res, out_dtype=out)
+        assert torch.equal(m.moe_lora(x, a, b, plan, scale=scale, residual=res, out_dtype=out), got)
+    check(m, x, a, b, ids, 128, out_dtype=out)
+    check(m, x, a, b, ids, 128, scale, residual=res, out=res)
 
 
 @pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 0), (0, 1), (4, 4)])
@@ -138,17 +156,17 @@ def test_ranks_of_their_own(m):
 
 def test_tokens_do_not_mix(m):
     """Another token's infinities and NaN, and which tokens share a tile, change nothing."""
-    for dtype in (BF16, F32):
+    for dtype, tile in ((BF16, 16), (F32, 16), (BF16, 128)):
         a, b, scale = adapters(2, 96, 128, 16)
         x, ids = rows(50, 128, dtype), ids_of(50, 2)
-        want, plan = check(m, x, a, b, ids, scale=scale)
+        want, plan = check(m, x, a, b, ids, tile, scale=scale)
         x[7, 3], x[8], x[9] = float("nan"), float("inf"), -3e38
         got = m.moe_lora(x, a, b, plan, scale=scale)
         keep = [t for t in range(50) if t not in (7, 8, 9)]
         assert torch.equal(got[keep], want[keep])
         assert torch.isnan(got[7]).all() and not torch.isfinite(got[8]).any()
         order = torch.randperm(50, device="cuda")
-        assert torch.equal(m.moe_lora(x[order].contiguous(), a, b, m.moe_lora_plan(ids[order].contiguous(), 2), scale=scale)[
+        assert torch.equal(m.moe_lora(x[order].contiguous(), a, b, m.moe_lora_plan(ids[order].contiguous(), 2, tile), scale=scale)[
             order.argsort()][keep], want[keep])
 
 
@@ -167,12 +185,13 @@ def test_a_bad_plan_is_reported(m):
     compares each with its range before it uses it.)"""
     a, b, _ = adapters(3, 64, 64, 8)
     x, res = rows(20, 64, BF16), rows(20, 64, BF16)
-    for key, value in (("tile_expert", 3), ("tile_expert", -1), ("sorted_pairs", 20), ("num_tiles", 1 << 20), ("num_tiles", -1)):
-        plan = m.moe_lora_plan(ids_of(20, 3), 3)
-        plan[key][0] = value
-        m.moe_lora(x, a, b, plan, residual=res)
-        assert m.moe_device_error() == 2, key
-        assert m.moe_device_error() == 0
+    for tile in (16, 128):
+        for key, value in (("tile_expert", 3), ("tile_expert", -1), ("sorted_pairs", 20), ("num_tiles", 1 << 20), ("num_tiles", -1)):
+            plan = m.moe_lora_plan(ids_of(20, 3), 3, tile)
+            plan[key][0] = value
+            m.moe_lora(x, a, b, plan, residual=res)
+            assert m.moe_device_error() == 2, key
+            assert m.moe_device_error() == 0
 
 
 def test_offsets_past_32_bits(m):
