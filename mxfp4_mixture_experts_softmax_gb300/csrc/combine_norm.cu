@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(MOST) combine_norm_kernel(const __grid_constan
     if (p.h) load_row<V, CH>(p.h, p.h_f32, t * p.ldh, c0, step, p.H, h);
     // the slots in order, the loads of several together
     load_row<V, CH>(p.y, p.y_f32, t * p.slots * p.ldy, c0, step, p.H, u);
-    constexpr int kAhead = V * CH <= 8 ? 4 : 2;
+    constexpr int kAhead = V == 8 && CH == 1 ? 4 : 2;
     for (int j = 1; j < p.slots; j += kAhead) {
         float v[kAhead][CH][V];
 #pragma unroll
@@ -533,7 +533,7 @@ template <bool YF, bool HF>
 cudaError_t launch_stream(CombineNorm p, const StreamShape& shape, cudaStream_t s) {
     const auto kernel = combine_norm_stream_kernel<YF, HF>;
     p.stages = shape.stages;
-    const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), shape.smem);
+    const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), shape.smem + 1024);
     if (err != cudaSuccess) return err;
     return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)num_sms() * shape.per_sm, p.T)), dim3(shape.threads),
                       shape.smem, s, p);

@@ -86,6 +86,18 @@ __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
     return v;
 }
 
+// 16 bytes of the residual and the output, which no other thread touches: free of the order that the
+// compiler keeps between accesses that may alias (an output that is its own residual is read before it is
+// written, through the registers).
+__device__ __forceinline__ uint4 ld_global(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void st_global(void* p, uint4 v) {
+    asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+}
+
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -95,6 +107,9 @@ template <bool OF32>
 struct Rows {
     static constexpr int kV = OF32 ? 4 : 8, kLanes = 64 / kV, kRows = 32 / kLanes, kPasses = 32 / kRows,
                          kAhead = OF32 ? 1 : 2;  // pieces whose residual is on its way
+    // Where a staged row has its column c (a multiple of 4): for bf16 the even fours first, so that the lanes
+    // of a row, each with two neighbouring fours, read 128 bytes in a row twice.
+    __device__ static __forceinline__ int place(int c) { return OF32 ? c : ((c >> 3) << 2) + ((c & 4) << 3); }
 };
 
 template <bool OF32>
@@ -135,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blocks = Rp <= 64 ? 1 : 2;      // of 64 ranks
     const uint32_t stage_bytes = kXBytes + 128 * Rp;
     const int stages = min(kMaxStages, kRing / (int)stage_bytes);
-    const int ks = (p.K + 63) / 64, k0 = (int)((long long)ks * cta / ctas), nk = (int)((long long)ks * (cta + 1) / ctas) - k0;
-    const int tn = (p.N + NT - 1) / NT, n0 = (int)((long long)tn * cta / ctas), nn = (int)((long long)tn * (cta + 1) / ctas) - n0;
+    const int ks = (p.K + 63) / 64, nk = (ks - cta + ctas - 1) / ctas;
+    const int tn = (p.N + NT - 1) / NT, nn = (tn - cta + ctas - 1) / ctas;
     const int terms = OF32 ? 3 : 2;
     // the warps that read a D2 buffer: all eight of a tile of 128 outputs, four (by the tile's parity) of one of 64
     const int readers = NT == 128 ? 8 : 4;
@@ -214,23 +229,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) row[i] = min(row[i], p.T - 1);
         }
         bool ok = true;
-        for (int i = 0; i < nk && ok; ++i) {
-            const int s = i % stages;
-            if (i >= stages) ok = mbar_wait_warp(&empty[s], ((i / stages) - 1) & 1);
+        for (int i = 0, s = 0, parity = 1; i < nk && ok; ++i) {
+            if (i >= stages) ok = mbar_wait_warp(&empty[s], parity);
             if (!ok) break;
             uint8_t* to = smem + (size_t)s * stage_bytes;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&full[s], x_bytes + 128 * p.R);
-                tma_load_2d(smem_u32(to + kXBytes), &a_map, (k0 + i) * 64, adapter * p.R, &full[s]);
+                tma_load_2d(smem_u32(to + kXBytes), &a_map, (cta + i * ctas) * 64, adapter * p.R, &full[s]);
             }
             __syncwarp();
             const uint32_t dst = smem_u32(to) + lane * 512;
             if (rows == 32)
-                tma_load_2d(dst, &x32_map, (k0 + i) * 64, row[0], &full[s]);
+                tma_load_2d(dst, &x32_map, (cta + i * ctas) * 64, row[0], &full[s]);
             else if (rows == 8)
-                tma_load_2d(dst, &x8_map, (k0 + i) * 64, row[0], &full[s]);
+                tma_load_2d(dst, &x8_map, (cta + i * ctas) * 64, row[0], &full[s]);
             else if (rows == 4)
-                tma_gather4(dst, &x_map, (k0 + i) * 64, row, &full[s]);
+                tma_gather4(dst, &x_map, (cta + i * ctas) * 64, row, &full[s]);
+            if (++s == stages) s = 0, parity ^= 1;
         }
         __syncwarp();
         // B's stages lie where the last of those were
@@ -247,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t* to = smem + kBOffset + s * kBBytes;
                 mbar_arrive_expect_tx(&b_full[s], kBBytes);
                 for (int j = 0; j < blocks; ++j)
-                    tma_load_2d(smem_u32(to + j * NT * 128), &b_map, j * 64, adapter * p.N + (n0 + i) * NT, &b_full[s]);
+                    tma_load_2d(smem_u32(to + j * NT * 128), &b_map, j * 64, adapter * p.N + (cta + i * ctas) * NT, &b_full[s]);
             }
             __syncwarp();
         }
@@ -256,20 +271,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------- MMA
         bool ok = true;
         const uint32_t id1 = idesc_bf16(Rp), id2 = idesc_bf16(NT);
-        for (int i = 0; i < nk && ok; ++i) {
-            const int s = i % stages;
-            ok = mbar_wait_warp(&full[s], (i / stages) & 1);
+        // (a descriptor's low bits are its address in units of 16 bytes)
+        const uint64_t x_desc = sdesc_sw128(smem_u32(smem)), a_desc = sdesc_sw128(smem_u32(smem + kXBytes)),
+                       b_desc = sdesc_sw128(smem_u32(smem + kBOffset));
+        for (int i = 0, s = 0, parity = 0; i < nk && ok; ++i) {
+            ok = mbar_wait_warp(&full[s], parity);
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
-                const uint64_t ad = sdesc_sw128(smem_u32(smem + (size_t)s * stage_bytes));
-                const uint64_t bd = sdesc_sw128(smem_u32(smem + (size_t)s * stage_bytes + kXBytes));
+                const uint64_t ad = x_desc + s * (stage_bytes >> 4), bd = a_desc + s * (stage_bytes >> 4);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mma_ss(tmem + kD2, ad + 2 * k, bd + 2 * k, id1, (i | k) != 0);
                 mma_commit(&empty[s]);
                 if (i == nk - 1) mma_commit(&d1_full);
             }
             __syncwarp();
+            if (++s == stages) s = 0, parity ^= 1;
         }
         if (nk == 0 && lane == 0) mbar_arrive(&d1_full);
         __syncwarp();
@@ -284,12 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (lane == 0) {
                 const uint32_t d = tmem + kD2 + buf * 128;
+                const uint64_t bd = b_desc + s * (kBBytes >> 4);
                 // v's smallest term first
-                for (int e = terms - 1, n = 0; e >= 0; --e)
-                    for (int k = 0; k < Rp / 16; ++k, ++n) {
-                        const uint64_t bd = sdesc_sw128(smem_u32(smem + kBOffset + s * kBBytes + (k >> 2) * NT * 128)) + 2 * (k & 3);
-                        mma_ts(d, tmem + kV + e * (Rp / 2) + 8 * k, bd, id2, n != 0);
-                    }
+                for (int e = terms - 1; e >= 0; --e) {
+                    const uint32_t a = tmem + kV + e * (Rp / 2);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (16 * k < Rp) mma_ts(d, a + 8 * k, bd + (k >> 2) * (NT * 128 >> 4) + 2 * (k & 3), id2, e != terms - 1 || k != 0);
+                }
                 mma_commit(&b_empty[s]);
                 mma_commit(&d2_full[buf]);
             }
@@ -380,18 +399,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* stage = reinterpret_cast<float*>(smem + kRing) + (size_t)ew * 32 * kPitch;
         const int col = (lane % W::kLanes) * W::kV, sub = lane / W::kLanes;
         const int first = NT == 128 ? 0 : half, every = NT == 128 ? 1 : 2;
-        const auto column = [&](int i) { return (n0 + i) * NT + (NT == 128 ? 64 * half : 0) + col; };
+        const auto column = [&](int i) { return (cta + i * ctas) * NT + (NT == 128 ? 64 * half : 0) + col; };
+        // the lane's rows, one for each pass, and what it has of them
+        int rows[W::kPasses];
+#pragma unroll
+        for (int k = 0; k < W::kPasses; ++k) rows[k] = tok[32 * quad + k * W::kRows + sub];
         uint4 res[W::kAhead][W::kPasses];
-        const auto fetch = [&](uint4& to, int i, int pass) {
-            const int t = tok[32 * quad + pass * W::kRows + sub], n = column(i);
-            to = make_uint4(0, 0, 0, 0);
-            if (p.residual && i < nn && t >= 0 && n < p.N)
-                to = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.residual) + ((long long)t * p.ldr + n) * (OF32 ? 4 : 2));
-        };
 #pragma unroll
         for (int a = 0; a < W::kAhead; ++a)
 #pragma unroll
-            for (int k = 0; k < W::kPasses; ++k) fetch(res[a][k], first + a * every, k);
+            for (int k = 0; k < W::kPasses; ++k) res[a][k] = make_uint4(0, 0, 0, 0);
+        // Without a choice for each load, which would wait for it: where there is no token or no output, what is
+        // read lies in the first row or the last columns, and goes nowhere.
+        const auto fetch = [&](uint4* to, int i) {
+            if (!p.residual || i >= nn) return;
+            const int n = min(column(i), p.N - W::kV);
+#pragma unroll
+            for (int k = 0; k < W::kPasses; ++k)
+                to[k] = ld_global(static_cast<const uint8_t*>(p.residual) + ((long long)max(rows[k], 0) * p.ldr + n) * (OF32 ? 4 : 2));
+        };
+#pragma unroll
+        for (int a = 0; a < W::kAhead; ++a) fetch(res[a], first + a * every);
         if (!sums) meet_once();
         for (int i = first; i < nn && ok; i += W::kAhead * every) {
 #pragma unroll
@@ -410,33 +438,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 32; c += 4)
-                        *reinterpret_cast<uint4*>(stage + lane * kPitch + h + c) = make_uint4(d[c], d[c + 1], d[c + 2], d[c + 3]);
+                        *reinterpret_cast<uint4*>(stage + lane * kPitch + W::place(h + c)) = make_uint4(d[c], d[c + 1], d[c + 2], d[c + 3]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&d2_empty[buf]);
+                // all sums before the first store: stores that may alias what is read would part the passes
                 const int n = column(j);
 #pragma unroll
                 for (int k = 0; k < W::kPasses; ++k) {
-                    const int r = k * W::kRows + sub, t = tok[32 * quad + r];
-                    const float4 u = *reinterpret_cast<const float4*>(stage + r * kPitch + col);
-                    const uint4 q = res[a][k];
-                    uint4 o;
+                    const float* at = stage + (k * W::kRows + sub) * kPitch;
+                    const float4 u = *reinterpret_cast<const float4*>(at + W::place(col));
+                    uint4& q = res[a][k];
                     if constexpr (OF32) {
-                        o = make_uint4(__float_as_uint(u.x + __uint_as_float(q.x)), __float_as_uint(u.y + __uint_as_float(q.y)),
+                        q = make_uint4(__float_as_uint(u.x + __uint_as_float(q.x)), __float_as_uint(u.y + __uint_as_float(q.y)),
                                        __float_as_uint(u.z + __uint_as_float(q.z)), __float_as_uint(u.w + __uint_as_float(q.w)));
                     } else {
-                        const float4 w = *reinterpret_cast<const float4*>(stage + r * kPitch + col + 4);
-                        o = make_uint4(f32x2_to_bf16x2_bits(u.x + bf16_lo(q.x), u.y + bf16_hi(q.x)),
+                        const float4 w = *reinterpret_cast<const float4*>(at + W::place(col + 4));
+                        q = make_uint4(f32x2_to_bf16x2_bits(u.x + bf16_lo(q.x), u.y + bf16_hi(q.x)),
                                        f32x2_to_bf16x2_bits(u.z + bf16_lo(q.y), u.w + bf16_hi(q.y)),
                                        f32x2_to_bf16x2_bits(w.x + bf16_lo(q.z), w.y + bf16_hi(q.z)),
                                        f32x2_to_bf16x2_bits(w.z + bf16_lo(q.w), w.w + bf16_hi(q.w)));
                     }
-                    if (t >= 0 && n < p.N)
-                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((long long)t * p.ldo + n) * (OF32 ? 4 : 2)) = o;
-                    fetch(res[a][k], j + W::kAhead * every, k);
                 }
                 __syncwarp();
+#pragma unroll
+                for (int k = 0; k < W::kPasses; ++k)
+                    if (rows[k] >= 0 && n < p.N)
+                        st_global(static_cast<uint8_t*>(p.out) + ((long long)rows[k] * p.ldo + n) * (OF32 ? 4 : 2), res[a][k]);
+                if (!p.residual) {
+#pragma unroll
+                    for (int k = 0; k < W::kPasses; ++k) res[a][k] = make_uint4(0, 0, 0, 0);
+                }
+                fetch(res[a], j + W::kAhead * every);
             }
         }
     } else {
