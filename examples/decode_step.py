@@ -2,13 +2,18 @@
 moe_linear_mxfp4act, the mixture-of-experts layer through moe_layer_few (up to 16
 sequences), one CUDA graph per step.
 
-    python examples/decode_step.py [--layers 4] [--batch 4] [--steps 64] [--small]
+    python examples/decode_step.py [--layers 4] [--batch 4] [--steps 64] [--small] [--adapters 3]
 
 A block is  h += W_out mix(W_in norm(h));  h += moe(norm(h))  and the model ends in
 norm and an fp32 output head.  `mix` (here a gated running mean, one state per
 sequence) stands where a model has its attention, which libmoe does not do; the
 prompt runs through the same calls, many tokens at a time, with moe_layer for
 the experts.  Weights are random: the text is not.
+
+With --adapters each sequence has a low-rank adapter of its own beside every
+projection (moe_lora), experts are chosen by sigmoid scores with a bias and in
+groups (moe_route_grouped), and residual and norms between the blocks are one call
+(moe_combine_norm).
 """
 import argparse
 import os
@@ -125,6 +130,55 @@ class Decoder:
         return graph
 
 
+class AdapterDecoder(Decoder):
+    """The same model with an adapter for each sequence, grouped sigmoid routing, and sums and norms in one
+    call.  n is the normed stream that a block reads, h the stream itself."""
+
+    def __init__(self, adapters=3, rank=16, groups=4, seed=0, **size):
+        import torch
+        super().__init__(seed=seed, **size)
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(seed + 1)
+
+        def pair(linear):
+            n, k = linear.codes.shape[0], 2 * linear.codes.shape[1]
+            a = torch.randn((adapters, rank, k), device="cuda", generator=gen) / k ** 0.5
+            b = torch.randn((adapters, n, rank), device="cuda", generator=gen) / rank ** 0.5
+            return a.bfloat16(), b.bfloat16()
+        self.pairs = [(pair(w_in), pair(w_out)) for w_in, w_out, _ in self.blocks]
+        self.scale = torch.full((adapters,), 0.5, device="cuda")
+        self.adapter = (torch.arange(self.batch, device="cuda") % (adapters + 1) - 1).int()  # -1: none
+        self.adapters, self.groups = adapters, groups
+        self.bias = [0.05 * torch.randn(e.router.shape[0], device="cuda", generator=gen) for _, _, e in self.blocks]
+        self.norm_w = torch.ones(self.hidden, device="cuda").bfloat16()
+
+    def _experts(self, i, n):
+        import torch
+        from mxfp4_mixture_experts_softmax_gb300 import libmoe
+        e = self.blocks[i][2]
+        logits = n.float() @ e.router.float().T
+        shared_w = torch.sigmoid(n.float() @ e.gate.float())
+        return libmoe.moe_layer(logits, n, e.w13, e.s13, e.w2, e.s2, e.k, tile_m=8 if n.shape[0] <= 64 else 64,
+                                router=dict(bias=self.bias[i], n_groups=self.groups, topk_groups=self.groups // 2, scale=2.0,
+                                            shared_w=shared_w))
+
+    def forward(self, tokens):
+        from mxfp4_mixture_experts_softmax_gb300 import libmoe
+        h = self.embed[tokens.reshape(-1)]
+        plan = libmoe.moe_lora_plan(self.adapter.repeat_interleave(tokens.shape[1]), self.adapters)  # one a step
+        _, n = libmoe.moe_combine_norm(h, pre_w=self.norm_w, h_out=False)
+        for i, (w_in, w_out, _) in enumerate(self.blocks):
+            (a_in, b_in), (a_out, b_out) = self.pairs[i]
+            z = w_in(n)
+            libmoe.moe_lora(n, a_in, b_in, plan, scale=self.scale, residual=z, out=z)
+            mixed = self._mix(i, z)
+            y = w_out(mixed)
+            libmoe.moe_lora(mixed, a_out, b_out, plan, scale=self.scale, residual=y, out=y)
+            h, n = libmoe.moe_combine_norm(y, h, pre_w=self.norm_w)
+            h, n = libmoe.moe_combine_norm(self._experts(i, n), h, pre_w=self.norm_w)
+        return self.head(n.view(self.batch, -1, self.hidden)[:, -1], out=self.logits)
+
+
 def main():
     import torch
     from mxfp4_mixture_experts_softmax_gb300 import libmoe
@@ -134,9 +188,13 @@ def main():
     p.add_argument("--prompt", type=int, default=64)
     p.add_argument("--steps", type=int, default=64)
     p.add_argument("--small", action="store_true", help="a tiny model")
+    p.add_argument("--adapters", type=int, default=0, help="low-rank adapters, of which each sequence has one or none")
     a = p.parse_args()
     size = dict(hidden=256, inner=128, experts=8, top_k=2, vocab=1000) if a.small else {}
-    m = Decoder(layers=a.layers, batch=a.batch, prompt=a.prompt, **size)
+    if a.adapters:
+        m = AdapterDecoder(a.adapters, layers=a.layers, batch=a.batch, prompt=a.prompt, **size)
+    else:
+        m = Decoder(layers=a.layers, batch=a.batch, prompt=a.prompt, **size)
     prompt = torch.randint(0, m.embed.shape[0], (a.batch, a.prompt), device="cuda")
     m.tokens.copy_(m.forward(prompt).argmax(-1))
     graph = m.capture()

@@ -692,16 +692,18 @@ moe_status_t moe_route_grouped(const void* logits, moe_dtype_t logits_type, int6
  *             no other argument (but residual as above).
  * moe_lora_tile_m gives a tile height that suits T tokens of that many adapters.
  * Products of bf16 values are exact (an fp32 x enters as three bf16 terms, exactly)
- * and sums fp32; A x enters the second product rounded to 2^-16 of itself for bf16
- * outputs and 2^-24 for fp32 ones; one rounding to out_type.  Results do not vary
+ * and sums fp32; A x, times scale, enters the second product rounded to 2^-16 of itself for
+ * bf16 outputs and 2^-24 for fp32 ones; one rounding to out_type.  Results do not vary
  * from run to run, nor with the other tokens of the batch, as long as T, adapters
  * and tile_m are the same.  A token whose x holds an infinity or a NaN does not change others.
  * One launch, no workspace.  T = 0 is a no-op.
  * Limits: K % 8 == 0, K <= 65536, N <= 2^24, T <= 2^20, R % 8 == 0, R <=
- * MOE_LORA_MAX_RANK, adapters <= 1025, tile_m 16, 32 or 64.  a and b 16-byte aligned, the
- * others to their element; x, residual and out rows on 16-byte boundaries are read
- * and written faster.  A grouping that names an adapter or a token outside the range
- * is not followed there (moe_device_error value 2).
+ * MOE_LORA_MAX_RANK, adapters <= 1025, tile_m 16, 32, 64 or 128.  a and b 16-byte aligned,
+ * the others to their element; x, residual and out rows on 16-byte boundaries (and N %
+ * 8 == 0) are read and written faster.  Tiles of 128 take bf16 x with such rows and
+ * without `ranks` to the tcgen05 tensor cores, for long prompts; all else runs in pieces
+ * of 16 tokens.  A grouping that names an adapter or a token outside the range is not
+ * followed there (moe_device_error value 2).
  */
 #define MOE_LORA_MAX_RANK 128
 int moe_lora_tile_m(int T, int adapters);

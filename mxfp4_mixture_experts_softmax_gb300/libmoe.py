@@ -470,9 +470,11 @@ def moe_combine(y, T: int, H: int, Kt: int, out, stream=None):
 
 def moe_layer(logits, x, w13, s13, w2, s2, K: int, with_shared: bool = True,
               renormalize: bool = True, tile_m: int = 8, path: int = MOE_PATH_AUTO,
-              bufs: dict | None = None, stream=None):
+              bufs: dict | None = None, stream=None, router: dict | None = None):
     """The whole layer: route -> permute -> ffn, all on one stream.  `bufs`
-    (from alloc_layer) reuses preallocated device buffers."""
+    (from alloc_layer) reuses preallocated device buffers.  `router`: arguments of
+    moe_route_grouped (bias, score, n_groups, topk_groups, group_top, scale, shared_w), which then
+    routes instead of moe_route."""
     T, E = logits.shape
     Et = w13.shape[0]
     if bufs is None:
@@ -481,8 +483,13 @@ def moe_layer(logits, x, w13, s13, w2, s2, K: int, with_shared: bool = True,
                                x.device)
     if Et != E + (1 if with_shared else 0):
         raise ValueError("weights must hold E experts plus the shared one when with_shared")
-    ids, w, perm = moe_route_permute(logits, K, tile_m, with_shared, renormalize, bufs["topk_ids"],
-                                     bufs["topk_w"], bufs["perm"], stream=stream)
+    if router is None:
+        ids, w, perm = moe_route_permute(logits, K, tile_m, with_shared, renormalize, bufs["topk_ids"],
+                                         bufs["topk_w"], bufs["perm"], stream=stream)
+    else:
+        ids, w = moe_route_grouped(logits, K, with_shared=with_shared, renormalize=renormalize, topk_ids=bufs["topk_ids"],
+                                   topk_w=bufs["topk_w"], stream=stream, **router)
+        perm = moe_permute(ids, Et, tile_m, bufs["perm"], stream)
     return moe_ffn(x, w13, s13, w2, s2, w, perm, bufs["out"], bufs["workspace"], path, stream)
 
 
