@@ -126,20 +126,33 @@ __global__ void __launch_bounds__(MOST) combine_norm_kernel(const __grid_constan
     if (p.h) load_row<V, CH>(p.h, p.h_f32, t * p.ldh, c0, step, p.H, h);
     // the slots in order, the loads of several together
     load_row<V, CH>(p.y, p.y_f32, t * p.slots * p.ldy, c0, step, p.H, u);
-    constexpr int kAhead = V == 8 && CH == 1 ? 4 : 2;
-    for (int j = 1; j < p.slots; j += kAhead) {
-        float v[kAhead][CH][V];
+    if constexpr (V == 8 && CH == 1) {
+        for (int j = 1; j < p.slots; j += 4) {
+            float v[4][V];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-            load_row<V, CH>(p.y, p.y_f32, (t * p.slots + min(j + a, p.slots - 1)) * p.ldy, c0, step, p.H, v[a]);
+            for (int a = 0; a < 4; ++a)
+                if (j + a < p.slots && c0 < p.H) load_values<V>(p.y, p.y_f32, (t * p.slots + j + a) * p.ldy + c0, v[a]);
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-            if (j + a < p.slots) {
+            for (int a = 0; a < 4; ++a)
+                if (j + a < p.slots && c0 < p.H) {
 #pragma unroll
-                for (int i = 0; i < CH; ++i)
+                    for (int k = 0; k < V; ++k) u[0][k] += v[a][k];
+                }
+        }
+    } else {
+        for (int j = 1; j < p.slots; j += 2) {
+            float v[2][CH][V];
+            const bool both = j + 1 < p.slots;
+            load_row<V, CH>(p.y, p.y_f32, (t * p.slots + j) * p.ldy, c0, step, p.H, v[0]);
+            load_row<V, CH>(p.y, p.y_f32, (t * p.slots + j + (both ? 1 : 0)) * p.ldy, c0, step, p.H, v[1]);
 #pragma unroll
-                    for (int k = 0; k < V; ++k) u[i][k] += v[a][i][k];
-            }
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    u[i][k] += v[0][i][k];
+                    if (both) u[i][k] += v[1][i][k];
+                }
+        }
     }
     const float inv = 1.0f / (float)p.H;
     if (p.post) {
