@@ -779,21 +779,44 @@ _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 _GATES = {"none": MOE_GATE_NONE, "sigmoid": MOE_GATE_SIGMOID, "silu": MOE_GATE_SILU}
 
 
+_codes: dict = {}
+
+
+def _code(t):
+    """MOE_DTYPE_... of a tensor, -1 for int32, None for other types.  (A dict of torch's types made at the
+    first call: importing torch in every call and function took a fourth of a small call's time.)"""
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.int32: -1})
+    return _codes.get(t.dtype)
+
+
 def _dtype_code(t, what: str) -> int:
     """MOE_DTYPE_... of a tensor."""
-    import torch
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return MOE_DTYPE_BF16
-    assert dt is torch.float32, f"{what} must be bfloat16 or float32"
-    return MOE_DTYPE_F32
+    code = _code(t)
+    assert code is not None and code >= 0, f"{what} must be bfloat16 or float32"
+    return code
 
 
-def _vector(t, n: int, dtype, what: str) -> int:
-    """The address of a contiguous CUDA tensor [n] of this type."""
-    assert t.is_cuda and t.is_contiguous() and t.dtype is dtype and t.shape == (n,), \
-        f"{what} must be a contiguous CUDA tensor of {dtype} [{n}]"
+def _vector(t, n: int, code: int, what: str) -> int:
+    """The address of a contiguous CUDA tensor [n] of the type with this code."""
+    assert t.is_cuda and t.is_contiguous() and _code(t) == code and t.shape == (n,), \
+        f"{what} must be a contiguous CUDA tensor [{n}] of its type"
     return t.data_ptr()
+
+
+_current_stream = None
+
+
+def _stream_handle(stream, t):
+    """The handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        _current_stream = torch._C._cuda_getCurrentRawStream
+    return _current_stream(t.get_device())
 
 
 def moe_route_grouped(logits, K: int, bias=None, score: str = "sigmoid", n_groups: int = 1, topk_groups: int = 1,
@@ -802,24 +825,24 @@ def moe_route_grouped(logits, K: int, bias=None, score: str = "sigmoid", n_group
     """fp32 or bf16 logits [T, E] (rows may be slices of wider ones) -> (int32 ids [T, Kt], fp32
     weights [T, Kt]), by softmax or sigmoid scores plus bias (fp32 [E]), within the topk_groups best
     of n_groups groups of experts, each worth the sum of its group_top largest (include/moe.h)."""
-    import torch
     T, E = logits.shape
     Kt = K + 1 if with_shared else K
     if topk_ids is None or topk_w is None:
+        import torch
         with _on(stream):
             if topk_ids is None:
                 topk_ids = torch.empty((T, Kt), dtype=torch.int32, device=logits.device)
             if topk_w is None:
                 topk_w = torch.empty((T, Kt), dtype=torch.float32, device=logits.device)
-    assert topk_ids.is_cuda and topk_ids.is_contiguous() and topk_ids.dtype is torch.int32 and topk_ids.numel() == T * Kt \
-        and topk_w.is_cuda and topk_w.is_contiguous() and topk_w.dtype is torch.float32 and topk_w.numel() == T * Kt, \
+    assert topk_ids.is_cuda and topk_ids.is_contiguous() and _code(topk_ids) == -1 and topk_ids.numel() == T * Kt \
+        and topk_w.is_cuda and topk_w.is_contiguous() and _code(topk_w) == MOE_DTYPE_F32 and topk_w.numel() == T * Kt, \
         "topk_ids and topk_w must be contiguous CUDA tensors of int32 and float32 [T, Kt]"
     status = (_lib or load()).direct_moe_route_grouped(
         logits.data_ptr(), _dtype_code(logits, "logits"), _row_stride(logits, T, E, "logits"),
-        None if bias is None else _vector(bias, E, torch.float32, "bias"),
-        None if shared_w is None else _vector(shared_w, T, torch.float32, "shared_w"), T, E, K,
+        None if bias is None else _vector(bias, E, MOE_DTYPE_F32, "bias"),
+        None if shared_w is None else _vector(shared_w, T, MOE_DTYPE_F32, "shared_w"), T, E, K,
         _SCORES[score], n_groups, topk_groups, group_top, 1 if with_shared else 0, 1 if renormalize else 0, scale,
-        topk_ids.data_ptr(), topk_w.data_ptr(), _raw_stream(stream, logits))
+        topk_ids.data_ptr(), topk_w.data_ptr(), _stream_handle(stream, logits))
     if status:
         raise MoeError(status, "moe_route_grouped")
     return topk_ids, topk_w
@@ -841,16 +864,15 @@ def moe_lora(x, a, b, plan: dict, scale=None, ranks=None, residual=None, out=Non
     [adapters, R, K], b bf16 [adapters, N, R], plan from moe_lora_plan, scale fp32 and ranks int32
     [adapters], residual [T, N] (may be out) (include/moe.h).  x, residual and out may be row slices of
     wider tensors; out_dtype: torch.bfloat16 (default) or torch.float32."""
-    import torch
     T, K = x.shape
     n, N, R = b.shape
-    bf16 = torch.bfloat16
     assert plan["T"] == T and plan["Kt"] == 1 and plan["Et"] == n, "plan does not match x and the adapters"
-    assert a.shape == (n, R, K) and a.dtype is bf16 and b.dtype is bf16, "a and b must be bfloat16 [n, R, K] and [n, N, R]"
+    assert a.shape == (n, R, K) and _code(a) == MOE_DTYPE_BF16 and _code(b) == MOE_DTYPE_BF16, "a and b must be bfloat16 [n, R, K] and [n, N, R]"
     assert a.is_cuda and a.is_contiguous() and b.is_cuda and b.is_contiguous(), "a and b must be contiguous CUDA tensors"
     if out is None:
+        import torch
         with _on(stream):
-            out = torch.empty((T, N), dtype=out_dtype or bf16, device=x.device)
+            out = torch.empty((T, N), dtype=out_dtype or torch.bfloat16, device=x.device)
         ldo = N
     else:
         assert out.shape == (T, N) and out_dtype in (None, out.dtype), "out must be [T, N]"
@@ -861,11 +883,11 @@ def moe_lora(x, a, b, plan: dict, scale=None, ranks=None, residual=None, out=Non
         res, ldr = residual.data_ptr(), _row_stride(residual, T, N, "residual")
     status = (_lib or load()).direct_moe_lora(
         x.data_ptr(), _dtype_code(x, "x"), _row_stride(x, T, K, "x"), a.data_ptr(), b.data_ptr(),
-        None if scale is None else _vector(scale, n, torch.float32, "scale"),
-        None if ranks is None else _vector(ranks, n, torch.int32, "ranks"),
+        None if scale is None else _vector(scale, n, MOE_DTYPE_F32, "scale"),
+        None if ranks is None else _vector(ranks, n, -1, "ranks"),
         plan["sorted_pairs"].data_ptr(), plan["inv_pairs"].data_ptr(), plan["tile_expert"].data_ptr(),
         plan["num_tiles"].data_ptr(), plan["tile_m"], n, res, ldr, out.data_ptr(), _dtype_code(out, "out"), ldo, T, N, K, R,
-        _raw_stream(stream, x))
+        _stream_handle(stream, x))
     if status:
         raise MoeError(status, "moe_lora")
     return out
@@ -879,11 +901,11 @@ def moe_combine_norm(y, h=None, slots: int = 1, post_w=None, gate=None, gate_act
     h' with pre_w -> (h' [T, H], n [T, H]) (include/moe.h).  h_out may be h, n_out may be y.  Without h, h'
     has h_dtype (default bfloat16) and is not written if h_out is False; n has n_dtype (default
     bfloat16) and is not written if n_out is False."""
-    import torch
     rows, H = y.shape
     T = rows // slots
     assert T * slots == rows, "y must hold slots rows a token"
     if h_out is None or n_out is None:
+        import torch
         with _on(stream):
             if h_out is None:
                 h_out = torch.empty((T, H), dtype=h.dtype if h is not None else h_dtype or torch.bfloat16, device=y.device)
@@ -902,10 +924,12 @@ def moe_combine_norm(y, h=None, slots: int = 1, post_w=None, gate=None, gate_act
         np_, nt, ldn = n_out.data_ptr(), _dtype_code(n_out, "n_out"), _row_stride(n_out, T, H, "n_out")
     w_type, pw, w = 0, None, None
     if pre_w is not None:
-        w_type, w = _dtype_code(pre_w, "pre_w"), _vector(pre_w, H, pre_w.dtype, "pre_w")
+        w_type = _dtype_code(pre_w, "pre_w")
+        w = _vector(pre_w, H, w_type, "pre_w")
     if post_w is not None:
         assert pre_w is None or pre_w.dtype is post_w.dtype, "post_w and pre_w must have one type"
-        w_type, pw = _dtype_code(post_w, "post_w"), _vector(post_w, H, post_w.dtype, "post_w")
+        w_type = _dtype_code(post_w, "post_w")
+        pw = _vector(post_w, H, w_type, "post_w")
     gp, gt, ldg, cols = None, 0, 0, 1
     if gate is not None:
         grows, cols = gate.shape
@@ -915,7 +939,7 @@ def moe_combine_norm(y, h=None, slots: int = 1, post_w=None, gate=None, gate_act
     status = (_lib or load()).direct_moe_combine_norm(
         y.data_ptr(), _dtype_code(y, "y"), _row_stride(y, rows, H, "y"), slots, 0 if pw is None else 1, pw, w, w_type, w_offset,
         eps, gp, gt, ldg, cols, _GATES[gate_act], hp, ldh, alpha, beta, hop, ht, ldho, np_, nt, ldn, T, H,
-        _raw_stream(stream, y))
+        _stream_handle(stream, y))
     if status:
         raise MoeError(status, "moe_combine_norm")
     return h_out, n_out
