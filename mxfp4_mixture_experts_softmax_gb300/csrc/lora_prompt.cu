@@ -5,18 +5,24 @@
 //
 // What has to move is x, the residual and the output once (192 MB for 8192 tokens of 4096 values: 32
 // us); at rank 64 both products are a tenth of that at the tensor cores' rate, but as much as that
-// through warp MMAs, whose operands pass the registers (lora.cu: 188 us).  So:
+// through warp MMAs, whose operands pass the registers (lora.cu: 102 us).  So:
 //   * a cluster of CTAs has a tile; its CTAs split the sum over K, join their parts of v through
-//     distributed shared memory in rank order, and split the N outputs.  One launch, no workspace;
+//     distributed shared memory in rank order (each makes the sums of its share of the rows and gives them to
+//     all), and split the N outputs.  One launch, no workspace;
 //   * producer warp: A, B and x by TMA into a ring of 64-k stages (128-byte swizzle).  The tile's
 //     tokens lie anywhere, but mostly one after another: where 32 or 8 do, one box fetches them, else
 //     gathers of four rows (which alone, at 80 clocks each, take 42 us for 8192 tokens);
 //   * MMA warp: D1[128 x ranks] += x A^T from shared memory; then, for each tile of outputs,
 //     D2[128 x 128] = v B^T with v as the operand in tensor memory, two accumulators in turn;
 //   * eight epilogue warps: four read D1, add the others' parts, scale and write v back to tensor
-//     memory as two bf16 terms (2^-16 of v; three for an fp32 output, 2^-24); all eight then bring D2 through
-//     shared memory into rows, so that residual and output are accessed 128 bytes at a time,
-//     with the residual of the next columns on its way.
+//     memory as two bf16 terms (2^-16 of v; three for an fp32 output, 2^-24).  All eight then take D2, each 32
+//     rows and half of the columns.  Where its 32 tokens lie one after another, residual and output pass
+//     as TMA boxes through a ring of the warp's own; else D2 passes through shared memory into rows, which
+//     are loaded and stored 128 bytes at a time (that way alone: 55 us, the loads waiting for one another in L1).
+//
+// 8192 tokens of 4096 values, rank 64, eleven prompts: 49.5 us (4.3 TB/s); 32768 tokens, rank 16: 162 us (5.0
+// TB/s).  About 15 us of the 49.5 are x's way in, 3 the joining of v, 22 the residual's and the output's, the rest
+// the launch and the ends: with a tile a cluster these follow one another on an SM, and only many tiles let them overlap.
 #include <algorithm>
 
 #include "lora_device.cuh"
@@ -32,8 +38,9 @@ constexpr int kXBytes = kTile * 128;               // 64 k of the tile's tokens
 constexpr int kRing = 128 * 1024;                  // phase 1's stages; then v's parts and B's stages
 constexpr int kBOffset = 68 * 1024, kBBytes = 16 * 1024, kBStages = 3;
 constexpr int kMaxStages = 6;
+constexpr int kAhead = 4, kPieceBytes = 4096;       // an epilogue warp's ring of residual and output, 32 rows x 128 bytes
 constexpr int kPitch = 68;                         // floats of a staged row of 64: rows of 8 lanes in separate banks
-constexpr int kStaging = 8 * 32 * kPitch * 4;
+constexpr int kStaging = 68 * 1024;                // v's sums; then rings (and 8.5 KB where D2 is staged) of four warps
 constexpr size_t kSmem = 1024 + kRing + kStaging;  // 1 KB to align
 constexpr uint32_t kD2 = 0, kV = 256, kColumns = 512;  // tensor memory: D2 twice (D1 over the first), v's terms
 
@@ -75,6 +82,14 @@ __device__ __forceinline__ void st_cluster4(float* p, uint32_t rank, float4 v) {
                  : "memory");
 }
 
+// A box of shared memory to global memory, in the thread's current bulk group.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int c0, int c1, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap), "r"(c0),
+                 "r"(c1), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
     uint32_t remote;
     float4 v;
@@ -106,7 +121,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 template <bool OF32>
 struct Rows {
     static constexpr int kV = OF32 ? 4 : 8, kLanes = 64 / kV, kRows = 32 / kLanes, kPasses = 32 / kRows,
-                         kAhead = OF32 ? 1 : 2;  // pieces whose residual is on its way
+                         kSets = OF32 ? 1 : 2;  // pieces whose residual is on its way
     // Where a staged row has its column c (a multiple of 4): for bf16 the even fours first, so that the lanes
     // of a row, each with two neighbouring fours, read 128 bytes in a row twice.
     __device__ static __forceinline__ int place(int c) { return OF32 ? c : ((c >> 3) << 2) + ((c & 4) << 3); }
@@ -116,10 +131,11 @@ template <bool OF32>
 __global__ void __launch_bounds__(kThreads, 1)
     lora_prompt_kernel(const __grid_constant__ Lora p, const __grid_constant__ CUtensorMap x_map,
                        const __grid_constant__ CUtensorMap x8_map, const __grid_constant__ CUtensorMap x32_map,
-                       const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map) {
+                       const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                       const __grid_constant__ CUtensorMap res_map, const __grid_constant__ CUtensorMap out_map) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], b_full[kBStages], b_empty[kBStages], d2_full[2],
-        d2_empty[2], d1_full, v_ready;
+        d2_empty[2], d1_full, v_ready, res_full[8][kAhead];
     __shared__ uint32_t tmem_slot;
     __shared__ int tok[kTile];
 
@@ -160,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kMaxStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < kBStages; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], readers);
+        for (int i = 0; i < 8 * kAhead; ++i) mbar_init(&res_full[0][0] + i, 1);
         mbar_init(&d1_full, 1);
         mbar_init(&v_ready, 128);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -394,83 +411,159 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&v_ready);
             }
         }
-        // D2, 64 columns at a time
+        // D2, 64 columns at a time.  The warp's 16 KB are v's parts (of the warps that sum them) or sums until v is ready.
         using W = Rows<OF32>;
-        float* stage = reinterpret_cast<float*>(smem + kRing) + (size_t)ew * 32 * kPitch;
-        const int col = (lane % W::kLanes) * W::kV, sub = lane / W::kLanes;
-        const int first = NT == 128 ? 0 : half, every = NT == 128 ? 1 : 2;
-        const auto column = [&](int i) { return (cta + i * ctas) * NT + (NT == 128 ? 64 * half : 0) + col; };
-        // the lane's rows, one for each pass, and what it has of them
-        int rows[W::kPasses];
-#pragma unroll
-        for (int k = 0; k < W::kPasses; ++k) rows[k] = tok[32 * quad + k * W::kRows + sub];
-        uint4 res[W::kAhead][W::kPasses];
-#pragma unroll
-        for (int a = 0; a < W::kAhead; ++a)
-#pragma unroll
-            for (int k = 0; k < W::kPasses; ++k) res[a][k] = make_uint4(0, 0, 0, 0);
-        // Without a choice for each load, which would wait for it: where there is no token or no output, what is
-        // read lies in the first row or the last columns, and goes nowhere.
-        const auto fetch = [&](uint4* to, int i) {
-            if (!p.residual || i >= nn) return;
-            const int n = min(column(i), p.N - W::kV);
-#pragma unroll
-            for (int k = 0; k < W::kPasses; ++k)
-                to[k] = ld_global(static_cast<const uint8_t*>(p.residual) + ((long long)max(rows[k], 0) * p.ldr + n) * (OF32 ? 4 : 2));
-        };
-#pragma unroll
-        for (int a = 0; a < W::kAhead; ++a) fetch(res[a], first + a * every);
-        if (!sums) meet_once();
-        for (int i = first; i < nn && ok; i += W::kAhead * every) {
-#pragma unroll
-            for (int a = 0; a < W::kAhead; ++a) {
-                const int j = i + a * every, buf = j & 1;
-                if (j >= nn || !ok) break;
-                ok = mbar_wait_warp(&d2_full[buf], (j >> 1) & 1);
+        uint8_t* own = smem + (sums ? quad : 4 + quad) * (kAhead * kPieceBytes) + (sums ? 0 : kRing - 4 * kAhead * kPieceBytes);
+        const int first = NT == 128 ? 0 : half, every = NT == 128 ? 1 : 2, at = NT == 128 ? 64 * half : 0;
+        const int row0 = tok[32 * quad];
+        const bool run = p.whole && __all_sync(0xFFFFFFFFu, tok[32 * quad + lane] == row0 + lane && row0 >= 0);
+        if (run) {
+            // 32 tokens one after another: residual and output pass as boxes of 32 rows x 128 bytes through a ring of the
+            // warp's own, a lane its row; the sum is written where the residual lay.
+            constexpr int kCols = OF32 ? 32 : 64, kPer = 64 / kCols;  // columns of a piece, pieces of 64 columns
+            const int pieces = nn > first ? ((nn - first + every - 1) / every) * kPer : 0;
+            const auto column_of = [&](int j) { return (cta + (first + (j / kPer) * every) * ctas) * NT + at + (j % kPer) * kCols; };
+            const auto fetch = [&](int j) {
+                if (lane != 0 || !p.residual || j >= pieces || column_of(j) >= p.N) return;
+                const int b = j % kAhead;
+                mbar_arrive_expect_tx(&res_full[ew][b], kPieceBytes);
+                tma_load_2d(smem_u32(own + b * kPieceBytes), &res_map, column_of(j), row0, &res_full[ew][b]);
+            };
+            if (!sums) meet_once();
+            ok = ok && mbar_wait_warp(&v_ready, 0);
+            if (ok)
+                for (int j = 0; j < kAhead; ++j) fetch(j);
+            for (int j = 0; j < pieces && ok; ++j) {
+                const int t = j / kPer, i = first + t * every, buf = i & 1, b = j % kAhead;
+                if (j % kPer == 0) {
+                    ok = mbar_wait_warp(&d2_full[buf], (i >> 1) & 1);
+                    tc_fence_after();
+                }
+                if (ok && column_of(j) >= p.N) {  // the end of the last tile
+                    if (j % kPer == kPer - 1 && lane == 0) mbar_arrive(&d2_empty[buf]);
+                    continue;
+                }
+                if (p.residual) ok = mbar_wait_warp(&res_full[ew][b], (j / kAhead) & 1) && ok;
                 if (!ok) break;
-                tc_fence_after();
-                const uint32_t from = tmem + kD2 + lanes + buf * 128 + (NT == 128 ? 64 * half : 0);
+                uint8_t* row = own + b * kPieceBytes + lane * 128;
+                const uint32_t from = tmem + kD2 + lanes + buf * 128 + at + (j % kPer) * kCols;
 #pragma unroll
-                for (int h = 0; h < 64; h += 32) {
+                for (int h = 0; h < kCols; h += 32) {
                     uint32_t d[32];
                     tmem_ld16_nowait(from + h, d);
                     tmem_ld16_nowait(from + h + 16, d + 16);
                     tmem_wait_ld();
+                    if (h + 32 == kCols && j % kPer == kPer - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&d2_empty[buf]);
+                    }
+                    constexpr int kV = OF32 ? 4 : 8;  // columns of 16 bytes
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4)
-                        *reinterpret_cast<uint4*>(stage + lane * kPitch + W::place(h + c)) = make_uint4(d[c], d[c + 1], d[c + 2], d[c + 3]);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&d2_empty[buf]);
-                // all sums before the first store: stores that may alias what is read would part the passes
-                const int n = column(j);
-#pragma unroll
-                for (int k = 0; k < W::kPasses; ++k) {
-                    const float* at = stage + (k * W::kRows + sub) * kPitch;
-                    const float4 u = *reinterpret_cast<const float4*>(at + W::place(col));
-                    uint4& q = res[a][k];
-                    if constexpr (OF32) {
-                        q = make_uint4(__float_as_uint(u.x + __uint_as_float(q.x)), __float_as_uint(u.y + __uint_as_float(q.y)),
-                                       __float_as_uint(u.z + __uint_as_float(q.z)), __float_as_uint(u.w + __uint_as_float(q.w)));
-                    } else {
-                        const float4 w = *reinterpret_cast<const float4*>(at + W::place(col + 4));
-                        q = make_uint4(f32x2_to_bf16x2_bits(u.x + bf16_lo(q.x), u.y + bf16_hi(q.x)),
-                                       f32x2_to_bf16x2_bits(u.z + bf16_lo(q.y), u.w + bf16_hi(q.y)),
-                                       f32x2_to_bf16x2_bits(w.x + bf16_lo(q.z), w.y + bf16_hi(q.z)),
-                                       f32x2_to_bf16x2_bits(w.z + bf16_lo(q.w), w.w + bf16_hi(q.w)));
+                    for (int c = 0; c < 32; c += kV) {
+                        // (the 128-byte swizzle: a row's pieces of 16 bytes by its number)
+                        uint4* q = reinterpret_cast<uint4*>(row + ((((h + c) / kV) ^ (lane & 7)) << 4));
+                        uint4 o = p.residual ? *q : make_uint4(0, 0, 0, 0);
+                        const auto f = [&](int k) { return __uint_as_float(d[c + k]); };
+                        if constexpr (OF32)
+                            o = make_uint4(__float_as_uint(f(0) + __uint_as_float(o.x)), __float_as_uint(f(1) + __uint_as_float(o.y)),
+                                           __float_as_uint(f(2) + __uint_as_float(o.z)), __float_as_uint(f(3) + __uint_as_float(o.w)));
+                        else
+                            o = make_uint4(f32x2_to_bf16x2_bits(f(0) + bf16_lo(o.x), f(1) + bf16_hi(o.x)),
+                                           f32x2_to_bf16x2_bits(f(2) + bf16_lo(o.y), f(3) + bf16_hi(o.y)),
+                                           f32x2_to_bf16x2_bits(f(4 % kV) + bf16_lo(o.z), f(5 % kV) + bf16_hi(o.z)),
+                                           f32x2_to_bf16x2_bits(f(6 % kV) + bf16_lo(o.w), f(7 % kV) + bf16_hi(o.w)));
+                        *q = o;
                     }
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&out_map, column_of(j), row0, smem_u32(own + b * kPieceBytes));
+                    // the piece before has been read: its place is free
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                }
+                __syncwarp();
+                if (j > 0) fetch(j - 1 + kAhead);
+            }
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            __syncwarp();
+        } else {
+            float* stage = reinterpret_cast<float*>(own);
+            const int col = (lane % W::kLanes) * W::kV, sub = lane / W::kLanes;
+            const auto column = [&](int i) { return (cta + i * ctas) * NT + at + col; };
+            // the lane's rows, one for each pass, and what it has of them
+            int rows[W::kPasses];
+#pragma unroll
+            for (int k = 0; k < W::kPasses; ++k) rows[k] = tok[32 * quad + k * W::kRows + sub];
+            uint4 res[W::kSets][W::kPasses];
+#pragma unroll
+            for (int a = 0; a < W::kSets; ++a)
+#pragma unroll
+                for (int k = 0; k < W::kPasses; ++k) res[a][k] = make_uint4(0, 0, 0, 0);
+            // Without a choice for each load, which would wait for it: where there is no token or no output, what is
+            // read lies in the first row or the last columns, and goes nowhere.
+            const auto fetch = [&](uint4* to, int i) {
+                if (!p.residual || i >= nn) return;
+                const int n = min(column(i), p.N - W::kV);
 #pragma unroll
                 for (int k = 0; k < W::kPasses; ++k)
-                    if (rows[k] >= 0 && n < p.N)
-                        st_global(static_cast<uint8_t*>(p.out) + ((long long)rows[k] * p.ldo + n) * (OF32 ? 4 : 2), res[a][k]);
-                if (!p.residual) {
+                    to[k] = ld_global(static_cast<const uint8_t*>(p.residual) + ((long long)max(rows[k], 0) * p.ldr + n) * (OF32 ? 4 : 2));
+            };
 #pragma unroll
-                    for (int k = 0; k < W::kPasses; ++k) res[a][k] = make_uint4(0, 0, 0, 0);
+            for (int a = 0; a < W::kSets; ++a) fetch(res[a], first + a * every);
+            if (!sums) meet_once();
+            for (int i = first; i < nn && ok; i += W::kSets * every) {
+#pragma unroll
+                for (int a = 0; a < W::kSets; ++a) {
+                    const int j = i + a * every, buf = j & 1;
+                    if (j >= nn || !ok) break;
+                    ok = mbar_wait_warp(&d2_full[buf], (j >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t from = tmem + kD2 + lanes + buf * 128 + at;
+#pragma unroll
+                    for (int h = 0; h < 64; h += 32) {
+                        uint32_t d[32];
+                        tmem_ld16_nowait(from + h, d);
+                        tmem_ld16_nowait(from + h + 16, d + 16);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<uint4*>(stage + lane * kPitch + W::place(h + c)) = make_uint4(d[c], d[c + 1], d[c + 2], d[c + 3]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&d2_empty[buf]);
+                    // all sums before the first store: stores that may alias what is read would part the passes
+                    const int n = column(j);
+#pragma unroll
+                    for (int k = 0; k < W::kPasses; ++k) {
+                        const float* line = stage + (k * W::kRows + sub) * kPitch;
+                        const float4 u = *reinterpret_cast<const float4*>(line + W::place(col));
+                        uint4& q = res[a][k];
+                        if constexpr (OF32) {
+                            q = make_uint4(__float_as_uint(u.x + __uint_as_float(q.x)), __float_as_uint(u.y + __uint_as_float(q.y)),
+                                           __float_as_uint(u.z + __uint_as_float(q.z)), __float_as_uint(u.w + __uint_as_float(q.w)));
+                        } else {
+                            const float4 w = *reinterpret_cast<const float4*>(line + W::place(col + 4));
+                            q = make_uint4(f32x2_to_bf16x2_bits(u.x + bf16_lo(q.x), u.y + bf16_hi(q.x)),
+                                           f32x2_to_bf16x2_bits(u.z + bf16_lo(q.y), u.w + bf16_hi(q.y)),
+                                           f32x2_to_bf16x2_bits(w.x + bf16_lo(q.z), w.y + bf16_hi(q.z)),
+                                           f32x2_to_bf16x2_bits(w.z + bf16_lo(q.w), w.w + bf16_hi(q.w)));
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < W::kPasses; ++k)
+                        if (rows[k] >= 0 && n < p.N)
+                            st_global(static_cast<uint8_t*>(p.out) + ((long long)rows[k] * p.ldo + n) * (OF32 ? 4 : 2), res[a][k]);
+                    if (!p.residual) {
+#pragma unroll
+                        for (int k = 0; k < W::kPasses; ++k) res[a][k] = make_uint4(0, 0, 0, 0);
+                    }
+                    fetch(res[a], j + W::kSets * every);
                 }
-                fetch(res[a], j + W::kAhead * every);
             }
         }
     } else {
@@ -489,12 +582,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool OF32>
-cudaError_t launch(const Lora& p, const CUtensorMap* x, const CUtensorMap& a, const CUtensorMap& b, int items, cudaStream_t s) {
+cudaError_t launch(const Lora& p, const CUtensorMap* x, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& res,
+                   const CUtensorMap& out, int items, cudaStream_t s) {
     const auto kernel = lora_prompt_kernel<OF32>;
     const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmem);
     if (err != cudaSuccess) return err;
-    if (p.ctas == 1) return launch_pdl(kernel, dim3((unsigned)items), dim3(kThreads), kSmem, s, p, x[0], x[1], x[2], a, b);
-    return launch_pdl_cluster(kernel, dim3((unsigned)(items * p.ctas)), dim3(kThreads), kSmem, s, p.ctas, p, x[0], x[1], x[2], a, b);
+    if (p.ctas == 1) return launch_pdl(kernel, dim3((unsigned)items), dim3(kThreads), kSmem, s, p, x[0], x[1], x[2], a, b, res, out);
+    return launch_pdl_cluster(kernel, dim3((unsigned)(items * p.ctas)), dim3(kThreads), kSmem, s, p.ctas, p, x[0], x[1], x[2], a, b, res, out);
 }
 
 }  // namespace
@@ -503,12 +597,13 @@ cudaError_t launch(const Lora& p, const CUtensorMap* x, const CUtensorMap& a, co
 // a rank would be multiplied), coordinates of 31 bits.
 bool lora_prompt_supported(const Lora& p) {
     return p.tile_m == kTile && !p.x_f32 && p.x_wide && p.ldx >= p.K && p.out_wide && (!p.residual || p.res_wide) &&
-           p.N % 8 == 0 && !p.ranks && (long long)p.adapters * p.N < (1LL << 31) && p.ldx < (1LL << 38);
+           p.N % 8 == 0 && !p.ranks && (long long)p.adapters * p.N < (1LL << 31) && p.ldx < (1LL << 38) &&
+           p.ldo < (1LL << 37) && p.ldr < (1LL << 37);
 }
 
 cudaError_t launch_lora_prompt(const Lora& given, cudaStream_t s) {
     Lora p = given;
-    CUtensorMap x[3], a, b;  // x by 1 (gathers), 8 and 32 rows
+    CUtensorMap x[3], a, b, res, out;  // x by 1 (gathers), 8 and 32 rows
     const int NT = p.R <= 64 ? 128 : 64;
     cudaError_t err = cudaSuccess;
     for (int i = 0; i < 3 && err == cudaSuccess; ++i)
@@ -520,6 +615,15 @@ cudaError_t launch_lora_prompt(const Lora& given, cudaStream_t s) {
     if (err == cudaSuccess)
         err = encode_2d_map(&b, p.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.R, (uint64_t)p.adapters * p.N, (uint64_t)p.R * 2, 64,
                             NT, CU_TENSOR_MAP_SWIZZLE_128B);
+    // residual and output as boxes of 32 rows x 128 bytes, where no rows of the residual overlap
+    p.whole = !p.residual || p.ldr >= p.N;
+    const CUtensorMapDataType type = p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int size = p.out_f32 ? 4 : 2;
+    if (err == cudaSuccess)
+        err = encode_2d_map(&out, p.out, type, p.N, p.T, (uint64_t)p.ldo * size, 128 / size, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    res = out;
+    if (err == cudaSuccess && p.residual && p.whole)
+        err = encode_2d_map(&res, p.residual, type, p.N, p.T, (uint64_t)p.ldr * size, 128 / size, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     if (err != cudaSuccess) return err;
     // CTAs a tile: as many as one for each SM allows, for the tiles there are likely to be (clusters of 8
     // leave a sixth of the SMs out, clusters of 4 some)
@@ -530,7 +634,7 @@ cudaError_t launch_lora_prompt(const Lora& given, cudaStream_t s) {
         p.ctas /= 2;
     const bool in_place = p.residual == p.out && p.ldr == p.ldo;
     const int items = p.tiles + (in_place ? 0 : (p.T + kThreads - 1) / kThreads);
-    return p.out_f32 ? launch<true>(p, x, a, b, items, s) : launch<false>(p, x, a, b, items, s);
+    return p.out_f32 ? launch<true>(p, x, a, b, res, out, items, s) : launch<false>(p, x, a, b, res, out, items, s);
 }
 
 cudaError_t read_device_error_lora_prompt(int* flag, int clear) {
