@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(MOST) combine_norm_kernel(const __grid_constan
                 store_values<V>(p.n_out, p.n_f32, t * p.ldn + c0 + i * step, w[i]);
             }
     }
-    pdl_end();
+    pdl_end_block();
 }
 
 // Eight values as they lie in memory.
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kShortThreads) combine_norm_short_kernel(const
                 }
         }
     }
-    pdl_end();
+    pdl_end_block();
 }
 
 // Many longer rows, no slots.  A block takes rows in turn; one thread keeps the next rows' y, h and
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kStreamThreads) combine_norm_stream_kernel(con
                 }
             }
     }
-    pdl_end();
+    pdl_end_block();
 }
 
 template <int V, int CH, int MOST>

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) lora_kernel(const _
     const int ctas = p.ctas, item = blockIdx.x / ctas, cta = blockIdx.x % ctas;
     if (item >= p.tiles) {
         copy_rows<kThreads>(p, (item - p.tiles) * kThreads, cta, ctas);
-        pdl_end();
+        pdl_end_block();
         return;
     }
     // higher tiles are taken in pieces
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) lora_kernel(const _
     if (ctas > 1) cluster_arrive();
     __syncthreads();
     expand<RT>(p, b, rank, tok, cta, ctas, terms, sum + kTokens * S::kPart);
-    pdl_end();
+    pdl_end_block();
     // a CTA's shared memory has to live until the others have read it
     if (ctas > 1) cluster_wait();
 }

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ctas = p.ctas, item = blockIdx.x / ctas, cta = blockIdx.x % ctas;
     if (item >= p.tiles) {
         copy_rows<kThreads>(p, (item - p.tiles) * kThreads, cta, ctas);
-        pdl_end();
+        pdl_end_block();
         return;
     }
     // (uniform over the cluster: its CTAs read the same words)
@@ -573,10 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // second meeting no CTA reads or writes another's shared memory; the MMAs are done with tensor
     // memory (the epilogue has waited for every one of them).
     __syncwarp();
-    pdl_end();
     if (joins && !sums) cluster_wait();
     tc_fence_before();
     __syncthreads();
+    pdl_end();
     tc_fence_after();
     if (warp == 1) tmem_dealloc<false>(tmem, kColumns);
 }

@@ -34,6 +34,14 @@ __device__ __forceinline__ void pdl_end() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// pdl_end for a kernel whose blocks load from lines that other blocks write (a residual that is the
+// output, rows that share a line): the first thread of a block to give the trigger gives it for the block, so
+// the others' loads come first.  Threads that have exited do not count.
+__device__ __forceinline__ void pdl_end_block() {
+    __syncthreads();
+    pdl_end();
+}
+
 // ------------------------------------------------------------- numerics
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }

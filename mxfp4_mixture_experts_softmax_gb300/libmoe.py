@@ -854,8 +854,14 @@ def moe_lora_tile_m(T: int, adapters: int) -> int:
 
 def moe_lora_plan(adapter_ids, adapters: int, tile_m: int | None = None, out: dict | None = None, stream=None) -> dict:
     """The grouping of tokens by adapter that moe_lora takes: int32 adapter_ids [T] (-1: none) ->
-    moe_permute's dict.  One serves every projection of a step."""
+    moe_permute's dict.  One serves every projection of a step.  `out`: a plan of the same sizes to
+    write to, whose tile height it keeps."""
     T, = adapter_ids.shape
+    assert _code(adapter_ids) == -1, "adapter_ids must be int32"
+    if out is not None:
+        assert out["T"] == T and out["Kt"] == 1 and out["Et"] == adapters and tile_m in (None, out["tile_m"]), \
+            "out is a plan of other sizes"
+        tile_m = out["tile_m"]
     return moe_permute(adapter_ids.view(T, 1), adapters, tile_m or moe_lora_tile_m(T, adapters), out=out, stream=stream)
 
 

@@ -152,6 +152,12 @@ def test_bindings_refuse(recorded):  # noqa: F811
         except AssertionError:
             continue
         pytest.fail(f"{name} took {[(k, getattr(v, 'shape', v)) for k, v in args.items()]}")
+    ids = rand(3, dtype=i32)
+    plan = m.moe_lora_plan(ids, 2, 32, stream=SIDE)
+    assert m.moe_lora_plan(ids, 2, out=plan, stream=SIDE) is plan  # keeps its height
+    for args in (dict(adapter_ids=rand(4, dtype=i32)), dict(adapters=3), dict(tile_m=16), dict(adapter_ids=rand(3, dtype=torch.int64))):
+        with pytest.raises(AssertionError):
+            m.moe_lora_plan(**{**dict(adapter_ids=ids, adapters=2, out=plan), **args}, stream=SIDE)
     with pytest.raises(KeyError):
         m.moe_route_grouped(**dict(r, score="relu"), stream=SIDE)
     with pytest.raises(KeyError):

@@ -105,3 +105,26 @@ def test_the_example_with_adapters(m):
     none = d.adapter < 0
     assert none.any() and torch.equal(after[none], before[none])
     assert not (after[~none] == before[~none]).all(1).any()
+
+
+def test_in_place_calls_one_after_another(m):
+    """A stream that is updated in place by call after call, each launched while the one before still runs: rows and
+    columns of neighbouring blocks share cache lines (widths that are no multiple of 128 bytes)."""
+    torch.manual_seed(0)
+    for T, N, tile in ((70, 200, 16), (400, 264, 128), (33, 77, 16)):
+        a, b, scale = lora.adapters(3, N, 64, 16)
+        x, ids = torch.randn((T, 64), device="cuda").bfloat16(), lora.ids_of(T, 3, 0.2)
+        w = torch.ones(N, device="cuda").bfloat16()
+        plan = m.moe_lora_plan(ids, 3, tile)
+        start = torch.randn((T, N), device="cuda").bfloat16()
+
+        def chain(h, sync):
+            for _ in range(12):
+                m.moe_lora(x, a, b, plan, scale=scale, residual=h, out=h)
+                sync()
+                m.moe_combine_norm(h, h, pre_w=w, alpha=0.25, beta=0.5, h_out=h, n_out=False)
+                sync()
+            return h
+        want = chain(start.clone(), torch.cuda.synchronize)
+        for _ in range(5):
+            assert torch.equal(chain(start.clone(), lambda: None), want)
