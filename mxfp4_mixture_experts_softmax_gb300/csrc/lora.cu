@@ -180,17 +180,35 @@ __device__ __forceinline__ void shrink(const Lora& p, const uint16_t* a, const i
 }
 
 // The residual of a unit of 32 columns and 16 rows, as it lies in memory (what is made of it would wait for it).
-// Wide rows: eight neighbouring columns of rows g and g + 8 a lane.  Others: a column of all 16 rows a lane.
+// Wide rows: eight neighbouring columns of rows g and g + 8 a lane.  Others pass in turns of Q rows, Q = 4, 2 or 1
+// neighbouring columns of a row a lane (p.vec: as many as rows' addresses allow; fp32: 1).
 // What there is no token or no column for is read elsewhere in the residual, and goes nowhere.
 constexpr int kStagePitch = 36;
 struct Residual {
     uint32_t w[16];
-    __device__ __forceinline__ void load(const Lora& p, const int* tok, int at, bool wide) {
+    template <int Q>
+    __device__ __forceinline__ void load_turns(const Lora& p, const int* tok, int at) {
+        const int lane = threadIdx.x & 31, sub = lane / (32 / Q), n = min(at + Q * (lane % (32 / Q)), p.N - Q);
+        const uint16_t* base = static_cast<const uint16_t*>(p.residual) + n;
+#pragma unroll
+        for (int i = 0; i < 16 / Q; ++i) {
+            const uint16_t* from = base + (long long)max(tok[Q * i + sub], 0) * p.ldr;
+            if constexpr (Q == 4) {
+                const uint2 v = *reinterpret_cast<const uint2*>(from);
+                w[2 * i] = v.x, w[2 * i + 1] = v.y;
+            } else if constexpr (Q == 2) {
+                w[i] = *reinterpret_cast<const uint32_t*>(from);
+            } else {
+                w[i] = *from;
+            }
+        }
+    }
+    __device__ __forceinline__ void load(const Lora& p, const int* tok, int at) {
         const int lane = threadIdx.x & 31;
         if (!p.residual) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = 0u;
-        } else if (wide) {
+        } else if (p.whole) {
             const int n = min(at + 8 * (lane & 3), p.N - 8);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -205,17 +223,16 @@ struct Residual {
                     w[8 * i] = a.x, w[8 * i + 1] = a.y, w[8 * i + 2] = a.z, w[8 * i + 3] = a.w;
                 }
             }
-        } else {
+        } else if (p.out_f32) {
             const int n = min(at + lane, p.N - 1);
-            if (p.out_f32) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    w[r] = static_cast<const uint32_t*>(p.residual)[(long long)max(tok[r], 0) * p.ldr + n];
-            } else {
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    w[r] = static_cast<const uint16_t*>(p.residual)[(long long)max(tok[r], 0) * p.ldr + n];
-            }
+            for (int r = 0; r < 16; ++r) w[r] = static_cast<const uint32_t*>(p.residual)[(long long)max(tok[r], 0) * p.ldr + n];
+        } else if (p.vec == 4) {
+            load_turns<4>(p, tok, at);
+        } else if (p.vec == 2) {
+            load_turns<2>(p, tok, at);
+        } else {
+            load_turns<1>(p, tok, at);
         }
     }
     // Wide rows: column k of row g (i = 0) or g + 8 (i = 1).
@@ -223,8 +240,57 @@ struct Residual {
         return p.out_f32 ? __uint_as_float(w[8 * i + k])
                          : __uint_as_float((k & 1) ? w[8 * i + k / 2] & 0xFFFF0000u : w[8 * i + k / 2] << 16);
     }
-    __device__ __forceinline__ float column_value(const Lora& p, int r) const {
-        return __uint_as_float(p.out_f32 ? w[r] : w[r] << 16);
+    // Others: the staged sums of the unit that starts at column `at`, plus this, to out.
+    template <int Q>
+    __device__ __forceinline__ void store_turns(const Lora& p, const int* tok, const float* stage, int at) const {
+        const int lane = threadIdx.x & 31, sub = lane / (32 / Q), c = Q * (lane % (32 / Q));
+        if (at + c >= p.N) return;
+        uint32_t o[16];
+#pragma unroll
+        for (int i = 0; i < 16 / Q; ++i) {
+            const float* v = stage + (Q * i + sub) * kStagePitch + c;
+            if constexpr (Q == 4) {
+                const float4 u = *reinterpret_cast<const float4*>(v);
+                o[2 * i] = f32x2_to_bf16x2_bits(u.x + __uint_as_float(w[2 * i] << 16), u.y + __uint_as_float(w[2 * i] & 0xFFFF0000u));
+                o[2 * i + 1] = f32x2_to_bf16x2_bits(u.z + __uint_as_float(w[2 * i + 1] << 16),
+                                                    u.w + __uint_as_float(w[2 * i + 1] & 0xFFFF0000u));
+            } else if constexpr (Q == 2) {
+                const float2 u = *reinterpret_cast<const float2*>(v);
+                o[i] = f32x2_to_bf16x2_bits(u.x + __uint_as_float(w[i] << 16), u.y + __uint_as_float(w[i] & 0xFFFF0000u));
+            } else {
+                o[i] = f32_to_bf16_bits(v[0] + __uint_as_float(w[i] << 16));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16 / Q; ++i) {
+            const int t = tok[Q * i + sub];
+            if (t < 0) continue;
+            uint16_t* to = static_cast<uint16_t*>(p.out) + (long long)t * p.ldo + at + c;
+            if constexpr (Q == 4)
+                *reinterpret_cast<uint2*>(to) = make_uint2(o[2 * i], o[2 * i + 1]);
+            else if constexpr (Q == 2)
+                *reinterpret_cast<uint32_t*>(to) = o[i];
+            else
+                *to = (uint16_t)o[i];
+        }
+    }
+    __device__ __forceinline__ void store(const Lora& p, const int* tok, const float* stage, int at) const {
+        const int lane = threadIdx.x & 31;
+        if (p.out_f32) {
+            if (at + lane >= p.N) return;
+            float o[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[r] = stage[r * kStagePitch + lane] + __uint_as_float(w[r]);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (tok[r] >= 0) static_cast<float*>(p.out)[(long long)tok[r] * p.ldo + at + lane] = o[r];
+        } else if (p.vec == 4) {
+            store_turns<4>(p, tok, stage, at);
+        } else if (p.vec == 2) {
+            store_turns<2>(p, tok, stage, at);
+        } else {
+            store_turns<1>(p, tok, stage, at);
+        }
     }
 };
 
@@ -281,14 +347,13 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
     const bool wide = p.whole;
     float* stage = staging + warp * 16 * kStagePitch;
     const int t0 = tok[g], t1 = tok[8 + g];
-    const bool upper = tok[8] >= 0;  // (a tile's tokens come first)
     for (int u = u0 + warp; u < u1; u += UN * kWarps) {
         Columns<RT> columns;
         columns.load(p, b, u);
         auto& bw = columns.w;
         Residual res[UN];
 #pragma unroll
-        for (int v = 0; v < UN; ++v) res[v].load(p, tok, (u + v * kWarps) * 32, wide);
+        for (int v = 0; v < UN; ++v) res[v].load(p, tok, (u + v * kWarps) * 32);
         // what lies behind an adapter's rank is not its own, and may be NaN
 #pragma unroll
         for (int q = 0; q < KU; ++q) {
@@ -351,25 +416,7 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
                         make_float4(acc[v][j][2], acc[v][j][3], acc[v][j + 1][2], acc[v][j + 1][3]);
                 }
                 __syncwarp();
-                if (at + lane < p.N) {
-#pragma unroll
-                    for (int h = 0; h < 16; h += 8) {
-                        if (h > 0 && !upper) break;
-                        float r[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) r[k] = stage[(h + k) * kStagePitch + lane] + res[v].column_value(p, h + k);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int t = tok[h + k];
-                            if (t < 0) continue;
-                            const long long to = (long long)t * p.ldo + at + lane;
-                            if (p.out_f32)
-                                static_cast<float*>(p.out)[to] = r[k];
-                            else
-                                static_cast<uint16_t*>(p.out)[to] = f32_to_bf16_bits(r[k]);
-                        }
-                    }
-                }
+                res[v].store(p, tok, stage, at);
                 __syncwarp();
             }
         }
@@ -512,6 +559,10 @@ cudaError_t launch_lora(const Lora& given, cudaStream_t s) {
     p.res_wide = p.residual && wide_rows(p.residual, p.out_f32, p.ldr);
     p.out_wide = wide_rows(p.out, p.out_f32, p.ldo);
     p.whole = p.out_wide && (!p.residual || p.res_wide) && p.N % 8 == 0;
+    p.vec = p.out_f32 ? 1 : 4;
+    while (p.vec > 1 && (p.N % p.vec || p.ldo % p.vec || (uintptr_t)p.out % (2 * p.vec) ||
+                         (p.residual && (p.ldr % p.vec || (uintptr_t)p.residual % (2 * p.vec)))))
+        p.vec /= 2;
     if (lora_prompt_supported(p)) return launch_lora_prompt(p, s);
     p.tiles *= p.tile_m / kTokens;
     // CTAs a piece: two for each SM in all, which run at once (four: 64 tokens of 64 adapters in 18.3 us

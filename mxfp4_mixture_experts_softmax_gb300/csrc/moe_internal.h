@@ -367,8 +367,8 @@ struct Lora {
     long long ldo;
     int T, N, K, R;
     // set by the launcher: most tiles that T tokens can use, CTAs a tile, rows that can be
-    // accessed 16 bytes at a time, residual and output both and no column left over
-    int tiles, ctas, x_wide, res_wide, out_wide, whole;
+    // accessed 16 bytes at a time, residual and output both and no column left over, else by vec values (bf16)
+    int tiles, ctas, x_wide, res_wide, out_wide, whole, vec;
 };
 bool lora_tile_supported(int tile_m);
 int lora_tile_rule(int T, int adapters);

@@ -507,7 +507,7 @@ __device__ __noinline__ void route_again(const RouteGrouped& p, int t, int lane)
 // S lanes a token (32 / S tokens a warp), VPL slots a lane, of which the 8 largest are kept.
 // Needs K <= S, groups <= S, experts of a group in fours.
 template <int S, int VPL, bool BF16>
-__global__ void __launch_bounds__(kManyWarps * 32) route_grouped_many_kernel(const __grid_constant__ RouteGrouped p) {
+__global__ void __launch_bounds__(kManyWarps * 32, 8) route_grouped_many_kernel(const __grid_constant__ RouteGrouped p) {
     constexpr uint32_t kSlots = VPL - 1;
     constexpr int kSLog2 = S == 8 ? 3 : 4, kList = 8;
     pdl_begin();

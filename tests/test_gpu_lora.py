@@ -105,11 +105,11 @@ def test_prompts(m, T, n, N, K, R, out):
     check(m, x, a, b, ids, 128, scale, residual=res, out=res)
 
 
-@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 0), (0, 1), (4, 4)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 0), (0, 1), (4, 4), (2, 2), (6, 4)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_rows_of_wider_tensors(m, pad, shift, dtype):
     torch.manual_seed(pad)
-    T, N, K = 45, 120, 96
+    T, N, K = 45, 120 - pad, 96
     a, b, scale = adapters(4, N, K, 16)
     out = rows(T, N, dtype, pad, shift)
     was = out._base.clone()
