@@ -203,12 +203,13 @@ struct Residual {
             }
         }
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const Lora& p, const int* tok, int at) {
         const int lane = threadIdx.x & 31;
         if (!p.residual) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = 0u;
-        } else if (p.whole) {
+        } else if (WHOLE) {
             const int n = min(at + 8 * (lane & 3), p.N - 8);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -330,7 +331,7 @@ struct Columns {
 };
 
 // out for this CTA's columns, UN times 32 a warp at a time, all tokens of the tile.
-template <int RT>
+template <int RT, bool WHOLE>
 __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int rank, const int* tok, int cta, int ctas,
                                        const uint16_t* terms, float* staging) {
     using S = Shape<RT>;
@@ -343,8 +344,7 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
     const int u0 = (int)((long long)units * cta / ctas), u1 = (int)((long long)units * (cta + 1) / ctas);
     const int nterms = p.out_f32 ? 3 : 2;
     // Rows that do not lie on 16 bytes pass through shared memory, p.vec neighbouring columns a lane (a lane's eight
-    // columns one by one took 190 us for 8192 rows of 4095; through shared memory 4095 take 81 and 4092 take 66).
-    const bool wide = p.whole;
+    // columns one by one took 190 us for 8192 rows of 4095; through shared memory 4095 take 81 and 4092 take 63).
     float* stage = staging + warp * 16 * kStagePitch;
     const int t0 = tok[g], t1 = tok[8 + g];
     for (int u = u0 + warp; u < u1; u += UN * kWarps) {
@@ -353,7 +353,7 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
         auto& bw = columns.w;
         Residual res[UN];
 #pragma unroll
-        for (int v = 0; v < UN; ++v) res[v].load(p, tok, (u + v * kWarps) * 32);
+        for (int v = 0; v < UN; ++v) res[v].template load<WHOLE>(p, tok, (u + v * kWarps) * 32);
         // what lies behind an adapter's rank is not its own, and may be NaN
 #pragma unroll
         for (int q = 0; q < KU; ++q) {
@@ -399,7 +399,7 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
 #pragma unroll
         for (int v = 0; v < UN; ++v) {
             const int at = (u + v * kWarps) * 32, n0 = at + 8 * tq, count = u + v * kWarps < u1 ? p.N - n0 : 0;
-            if (wide) {
+            if (WHOLE) {
                 float r[2][8];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -423,7 +423,9 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
     }
 }
 
-template <int RT, bool XF32>
+// WHOLE: p.whole, known to the compiler.  Asked at run time both forms cost registers, which spilled: 64 tokens of 64
+// adapters 12.4 us against 11.8, 1024 tokens 9.9 against 9.4 (fp32 x and output alone took 151 against 154).
+template <int RT, bool XF32, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) lora_kernel(const __grid_constant__ Lora p) {
     using S = Shape<RT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -509,16 +511,16 @@ __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) lora_kernel(const _
     // this CTA has read the others' sums
     if (ctas > 1) cluster_arrive();
     __syncthreads();
-    expand<RT>(p, b, rank, tok, cta, ctas, terms, sum + kTokens * S::kPart);
+    expand<RT, WHOLE>(p, b, rank, tok, cta, ctas, terms, sum + kTokens * S::kPart);
     pdl_end_block();
     // a CTA's shared memory has to live until the others have read it
     if (ctas > 1) cluster_wait();
 }
 
-template <int RT, bool XF32>
+template <int RT, bool XF32, bool WHOLE>
 cudaError_t launch_one(const Lora& p, int items, cudaStream_t s) {
-    const auto kernel = lora_kernel<RT, XF32>;
-    const size_t smem = Shape<RT>::kBytes + (p.whole ? 0 : kWarps * 16 * kStagePitch * 4);
+    const auto kernel = lora_kernel<RT, XF32, WHOLE>;
+    const size_t smem = Shape<RT>::kBytes + (WHOLE ? 0 : kWarps * 16 * kStagePitch * 4);
     // (the limit without it is on static and dynamic shared memory together)
     const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem + 1024);
     if (err != cudaSuccess) return err;
@@ -526,12 +528,12 @@ cudaError_t launch_one(const Lora& p, int items, cudaStream_t s) {
     return launch_pdl_cluster(kernel, dim3((unsigned)(items * p.ctas)), dim3(kThreads), smem, s, p.ctas, p);
 }
 
-template <bool XF32>
+template <bool XF32, bool WHOLE>
 cudaError_t launch_ranks(const Lora& p, int items, cudaStream_t s) {
-    if (p.R <= 16) return launch_one<2, XF32>(p, items, s);
-    if (p.R <= 32) return launch_one<4, XF32>(p, items, s);
-    if (p.R <= 64) return launch_one<8, XF32>(p, items, s);
-    return launch_one<16, XF32>(p, items, s);
+    if (p.R <= 16) return launch_one<2, XF32, WHOLE>(p, items, s);
+    if (p.R <= 32) return launch_one<4, XF32, WHOLE>(p, items, s);
+    if (p.R <= 64) return launch_one<8, XF32, WHOLE>(p, items, s);
+    return launch_one<16, XF32, WHOLE>(p, items, s);
 }
 
 bool wide_rows(const void* p, int f32, long long ld) {
@@ -573,7 +575,8 @@ cudaError_t launch_lora(const Lora& given, cudaStream_t s) {
     while (p.ctas > 1 && (likely * p.ctas > 2LL * num_sms() || p.ctas * 64 > widest)) p.ctas /= 2;
     const bool in_place = p.residual == p.out && p.ldr == p.ldo;
     const int items = p.tiles + (in_place ? 0 : (p.T + kThreads - 1) / kThreads);
-    return p.x_f32 ? launch_ranks<true>(p, items, s) : launch_ranks<false>(p, items, s);
+    if (p.whole) return p.x_f32 ? launch_ranks<true, true>(p, items, s) : launch_ranks<false, true>(p, items, s);
+    return p.x_f32 ? launch_ranks<true, false>(p, items, s) : launch_ranks<false, false>(p, items, s);
 }
 
 cudaError_t read_device_error_lora(int* flag, int clear) {
