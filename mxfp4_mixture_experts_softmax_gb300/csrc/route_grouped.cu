@@ -248,6 +248,13 @@ __device__ __forceinline__ uint32_t packed_key(float v, uint32_t low_bits, uint3
     return ((u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) & ~low_bits) | low;
 }
 
+// The value of such a key up to its lowest bits.  Keys below that of the lowest finite value are -inf's, which
+// would be a NaN without its lowest bits, or empty.
+__device__ __forceinline__ float cut_value(uint32_t key, uint32_t low_bits) {
+    const uint32_t k = key & ~low_bits;
+    return k < 0x00800000u ? -INFINITY : key_to_float(k);
+}
+
 // V neighbouring logits from expert e on.
 template <int V, bool BF16>
 __device__ __forceinline__ void load_logits(const void* row, int e, float* l) {
@@ -605,26 +612,28 @@ __global__ void __launch_bounds__(kManyWarps * 32, 8) route_grouped_many_kernel(
     if (p.groups > 1) {
         // group values from the keys, which give a value up to its lowest bits: 2^-23 kSlots of it
         const bool real = L.group < p.groups;
-        float m1 = key[0] ? key_to_float(key[0] & ~kSlots) : -INFINITY, m2 = key[1] ? key_to_float(key[1] & ~kSlots) : -INFINITY;
+        float m1 = cut_value(key[0], kSlots), m2 = cut_value(key[1], kSlots);
         for (int o = 1; o < L.P; o <<= 1) {
             const float o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
             m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
             m1 = fmaxf(m1, o1);
         }
         constexpr float kCut = 2.0f * VPL * 0x1p-23f;
-        float value = m1, err = 2.0f * kErr + kCut * fabsf(m1);
+        const auto size = [](float v) { return v == -INFINITY ? 0.0f : fabsf(v); };  // (nothing is cut off -inf)
+        float value = m1, err = 2.0f * kErr + kCut * size(m1);
         if (p.top == 2) {
             float s1 = m1, s2 = m2;
             if (!biased) {
                 s1 = value32(p, m1, 0.0f, m, 1.0f);
                 s2 = value32(p, m2, 0.0f, m, 1.0f);
                 // a score's slope is at most 1/4 (sigmoid) or itself
-                err = 0x1p-19f + kCut * (fabsf(m1) + fabsf(m2) + 2.0f * fabsf(m));
+                err = 0x1p-19f + kCut * (size(m1) + size(m2) + 2.0f * fabsf(m));
             } else {
                 err = 4.0f * kErr + kCut * (fabsf(s1) + fabsf(s2));
             }
             value = s1 + s2;
         }
+        if (!(value == value)) err = INFINITY;  // compares with it say nothing: the token is routed again
         int before = 0;
         for (int g = 0; g < p.groups; ++g) {
             const float other = __shfl_sync(kAll, value, (lane & ~(S - 1)) + (g << log2P));
