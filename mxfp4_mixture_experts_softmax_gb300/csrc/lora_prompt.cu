@@ -408,6 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
+                // v's parts and sums have been read: their place goes to the TMA
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(&v_ready);
             }
         }
@@ -431,6 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (!sums) meet_once();
             ok = ok && mbar_wait_warp(&v_ready, 0);
+            // (the sums were stored by the other CTAs' threads too)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             if (ok)
                 for (int j = 0; j < kAhead; ++j) fetch(j);
             for (int j = 0; j < pieces && ok; ++j) {
