@@ -157,10 +157,11 @@ __device__ __noinline__ int settle(const RouteGrouped& p, const Token& t, const 
         c = p.sigmoid ? e + b : e * (double)inv_z + b;
         c = c == c ? c : -INFINITY;
     }
-    for (;;) {
-        // nearly in order: neighbours change places until none has to
+    for (int pass = 0; pass < 2; ++pass) {
+        // Nearly in order: neighbours change places until none has to.  Any n values are in order after n phases
+        // and two more see it, which bounds the loop whatever the values are.
         bool unclear = false;
-        for (int phase = 0, still = 0; still < 2; ++phase) {
+        for (int phase = 0, still = 0; still < 2 && phase < 34; ++phase) {
             const int other = ((lane + phase) & 1) ? lane - 1 : lane + 1;
             const bool pair = in && other >= 0 && other < n;
             const double oc = __shfl_sync(kAll, c, other & 31), oe = __shfl_sync(kAll, e, other & 31);
@@ -176,12 +177,13 @@ __device__ __noinline__ int settle(const RouteGrouped& p, const Token& t, const 
             id = move ? oid : id;
             still = __any_sync(kAll, move) ? 0 : still + 1;
         }
-        if (!__any_sync(kAll, unclear)) return id;
+        if (!__any_sync(kAll, unclear)) break;  // (never in the second pass)
         const double z = sum64<V, BF16>(p, t, L);
         c = in ? e / z + (double)__ldg(p.bias + id) : -INFINITY;
         c = c == c ? c : -INFINITY;
         rough = false;
     }
+    return id;
 }
 
 // Whether a group stays, by exact values.  u1 and u2 are what this lane contributes: the
