@@ -142,10 +142,12 @@ __device__ __noinline__ int choose64(const RouteGrouped& p, const Token& t, cons
 
 // The order of the n candidates that lanes 0 .. n - 1 hold, by their exact values: lane k
 // returns the k-th.  Without a bias the logits themselves are the values.  Softmax's
-// denominator in fp32, good to 2^-18, does for two experts unless it matters for their
-// difference; then it is summed in 64 bits.
+// denominator in fp32, whose inverse is good to z_err (which grows with the slots of a lane: see
+// route_one), does for two experts unless it matters for their difference; then it is
+// summed in 64 bits.
 template <int V, bool BF16>
-__device__ __noinline__ int settle(const RouteGrouped& p, const Token& t, const Lanes<V>& L, int id, int n, float inv_z, int lane) {
+__device__ __noinline__ int settle(const RouteGrouped& p, const Token& t, const Lanes<V>& L, int id, int n, float inv_z, float z_err,
+                                   int lane) {
     const bool in = lane < n;
     const double l = in ? (double)load_logit<BF16>(t.row, id) : -INFINITY;
     const double b = p.bias && in ? (double)__ldg(p.bias + id) : 0.0;
@@ -168,7 +170,7 @@ __device__ __noinline__ int settle(const RouteGrouped& p, const Token& t, const 
             const int oid = __shfl_sync(kAll, id, other & 31);
             const bool above = oc > c || (oc == c && oid < id);  // the other belongs above this one
             if (rough) {
-                const double tol = fabs(oe - e) * (double)inv_z * 0x1p-18;
+                const double tol = fabs(oe - e) * (double)z_err;
                 unclear = unclear || (pair && tol > 0.0 && !(fabs(oc - c) > tol));
             }
             const bool move = pair && above == (other > lane);
@@ -494,7 +496,7 @@ __device__ __forceinline__ void route_one(const RouteGrouped& p, int t, int lane
     const bool sure = cw - cn > tol || (!biased && cw > cn) || (lw == ln && bw == bn && id < idn);
     unsure = __any_sync(kAll, unsure) != 0;
     if (unsure || __any_sync(kAll, lane + 1 < n && !sure)) {
-        id = unsure ? choose64<VPL, V, BF16>(p, tk, L, lane) : settle<V, BF16>(p, tk, L, id, n, inv_z, lane);
+        id = unsure ? choose64<VPL, V, BF16>(p, tk, L, lane) : settle<V, BF16>(p, tk, L, id, n, inv_z, kErr, lane);
         if (lane < p.K) lw = load_logit<BF16>(tk.row, id);
     }
     finish<32>(p, t, lane, id, lw, m, sum_all);
