@@ -3,7 +3,7 @@
  * ctypes converts a call's 20 to 30 arguments in about 3 us, more than the launch itself takes;
  * these wrappers take 0.3.  Same names, same argument order as include/moe.h; pointers are integers
  * or None.  The library is the one that the binding has loaded: bind(name, address) hands over each
- * function. */
+ * function.  Python's lock is given up for the call, which may wait for a full queue. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -58,8 +58,12 @@ static PyObject* call_route(PyObject* self, PyObject* const* args, Py_ssize_t n)
     const float scale = f32(&a);
     void *ids = ptr(&a), *w = ptr(&a), *stream = ptr(&a);
     if (PyErr_Occurred()) return NULL;
-    return PyLong_FromLong(route(logits, (moe_dtype_t)type, ld, bias, shared_w, v[0], v[1], v[2], (moe_score_t)v[3], v[4],
-                                 v[5], v[6], v[7], v[8], scale, ids, w, stream));
+    moe_status_t status;
+    Py_BEGIN_ALLOW_THREADS
+    status = route(logits, (moe_dtype_t)type, ld, bias, shared_w, v[0], v[1], v[2], (moe_score_t)v[3], v[4], v[5], v[6], v[7],
+                   v[8], scale, ids, w, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
 }
 
 static PyObject* call_lora(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -79,8 +83,12 @@ static PyObject* call_lora(PyObject* self, PyObject* const* args, Py_ssize_t n) 
     const int T = i32(&a), N = i32(&a), K = i32(&a), R = i32(&a);
     void* stream = ptr(&a);
     if (PyErr_Occurred()) return NULL;
-    return PyLong_FromLong(lora(x, (moe_dtype_t)x_type, ldx, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], tile_m, adapters,
-                                residual, ldr, out, (moe_dtype_t)out_type, ldo, T, N, K, R, stream));
+    moe_status_t status;
+    Py_BEGIN_ALLOW_THREADS
+    status = lora(x, (moe_dtype_t)x_type, ldx, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], tile_m, adapters, residual, ldr,
+                  out, (moe_dtype_t)out_type, ldo, T, N, K, R, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
 }
 
 static PyObject* call_norm(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -109,9 +117,13 @@ static PyObject* call_norm(PyObject* self, PyObject* const* args, Py_ssize_t n) 
     const int T = i32(&a), H = i32(&a);
     void* stream = ptr(&a);
     if (PyErr_Occurred()) return NULL;
-    return PyLong_FromLong(norm(y, (moe_dtype_t)y_type, ldy, slots, post, post_w, pre_w, (moe_dtype_t)w_type, offset, eps,
-                                gate, (moe_dtype_t)gate_type, ldg, cols, (moe_gate_act_t)act, h, ldh, alpha, beta, h_out,
-                                (moe_dtype_t)h_type, ldho, n_out, (moe_dtype_t)n_type, ldn, T, H, stream));
+    moe_status_t status;
+    Py_BEGIN_ALLOW_THREADS
+    status = norm(y, (moe_dtype_t)y_type, ldy, slots, post, post_w, pre_w, (moe_dtype_t)w_type, offset, eps, gate,
+                  (moe_dtype_t)gate_type, ldg, cols, (moe_gate_act_t)act, h, ldh, alpha, beta, h_out, (moe_dtype_t)h_type, ldho,
+                  n_out, (moe_dtype_t)n_type, ldn, T, H, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
 }
 
 static PyObject* bind(PyObject* self, PyObject* args) {
