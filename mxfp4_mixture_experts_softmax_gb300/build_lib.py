@@ -5,18 +5,21 @@ Each .cu file compiles to an object in parallel, then one shared-library link.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "lib", "libmoe.so")
-PYCALL = os.path.join(HERE, "lib", "_pycall.so")
+# (named for the interpreter whose headers it is compiled with)
+PYCALL = os.path.join(HERE, "lib", "_pycall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["moe_api.cu", "route.cu", "permute.cu", "ffn_decode.cu", "ffn_prefill.cu",
            "ffn_mxfp4act.cu", "ffn_fp8x2.cu", "linear_mxfp4.cu", "layer_few.cu",
            "moe_noalloc.cu", "route_grouped.cu", "lora.cu", "lora_prompt.cu",
@@ -58,7 +61,13 @@ def build_pycall(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    build_pycall(force)
+    try:
+        build_pycall(force)
+    except (OSError, RuntimeError) as e:
+        # the binding then makes these calls through ctypes; wrappers of older sources are not to be loaded
+        with contextlib.suppress(FileNotFoundError):
+            os.unlink(PYCALL)
+        warnings.warn(f"pycall.c was not built, three calls take 3 us more each: {e}", RuntimeWarning, stacklevel=2)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

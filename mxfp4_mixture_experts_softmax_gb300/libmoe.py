@@ -179,13 +179,18 @@ def load(build: bool = True):
         L.moe_combine_norm.restype = ci
         L.moe_device_error.argtypes = [vp, ci]
         L.moe_device_error.restype = ci
-        # the same functions without ctypes' conversion of every argument (csrc/pycall.c)
-        spec = importlib.util.spec_from_file_location("_pycall", build_lib.PYCALL)
-        direct = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(direct)
+        # the same functions without ctypes' conversion of every argument (csrc/pycall.c), or with it
+        # where there is no such module for this interpreter
+        try:
+            spec = importlib.util.spec_from_file_location("_pycall", build_lib.PYCALL)
+            direct = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(direct)
+        except ImportError:
+            direct = None
         for name in ("moe_route_grouped", "moe_lora", "moe_combine_norm"):
-            direct.bind(name, ctypes.cast(getattr(L, name), vp).value)
-            setattr(L, "direct_" + name, getattr(direct, name))
+            if direct is not None:
+                direct.bind(name, ctypes.cast(getattr(L, name), vp).value)
+            setattr(L, "direct_" + name, getattr(direct or L, name))
         _lib = L
         return L
 
