@@ -276,6 +276,13 @@ __device__ __forceinline__ void load_logits(const void* row, int e, float* l) {
     for (int i = 0; i < V; ++i) l[i] = fmaxf(l[i], -INFINITY);  // NaN becomes -inf
 }
 
+// e^(a - b) to the exponential's own error: what the difference loses by its rounding (2^-24 of it, 60 parts of 2^24 of
+// the result at a distance of 60) comes back as a factor.
+__device__ __forceinline__ float exp_difference(float a, float b) {
+    const float d = a - b, t = d - a, lost = (a - (d - t)) - (b + t), v = expf(d);
+    return fabsf(d) < INFINITY ? fmaf(v, lost, v) : v;
+}
+
 // Weights of the chosen experts and the stores, S lanes a token, lane k of them with the k-th
 // expert (id, logit lw).  sum_all: softmax's denominator, where it is needed.
 template <int S>
@@ -291,7 +298,7 @@ __device__ __forceinline__ void finish(const RouteGrouped& p, int t, int k, int 
         for (int o = S / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
         if (p.sigmoid) top = fminf(top, 0.0f);
         if (top == -INFINITY) top = 0.0f;
-        w = mine ? expf((p.sigmoid ? fminf(lw, 0.0f) : lw) - top) : 0.0f;
+        w = mine ? exp_difference(p.sigmoid ? fminf(lw, 0.0f) : lw, top) : 0.0f;
         if (p.sigmoid) w /= 1.0f + expf(-fabsf(lw));
         float sum = w;
 #pragma unroll
@@ -301,7 +308,7 @@ __device__ __forceinline__ void finish(const RouteGrouped& p, int t, int k, int 
         const float e = expf(-fabsf(lw));
         w = (lw >= 0.0f ? 1.0f : e) / (1.0f + e);
     } else {
-        w = sum_all > 0.0f ? expf(lw - m) / sum_all : 0.0f;
+        w = sum_all > 0.0f ? exp_difference(lw, m) / sum_all : 0.0f;
     }
     const int Kt = p.K + p.shared;
     const size_t at = (size_t)t * Kt + k;
