@@ -114,3 +114,16 @@ def test_captured_in_place(m, H, turns):
         a, b = m.moe_combine_norm(y, h=a, pre_w=w, beta=0.5)
         a, b = m.moe_combine_norm(b, h=a, pre_w=w, alpha=0.25)
     assert torch.equal(h, a) and torch.equal(n, b)
+
+
+@pytest.mark.parametrize("T,H", [(3, 4096), (3, 77), (None, 128), (None, 2088)])
+def test_squares_beyond_fp32(m, T, H):
+    """A norm whose sum of squares leaves fp32's range is 0; the other rows are as ever."""
+    T = T or enough(H)
+    y, w = rows(T, H, F32), rows(1, H, BF16)[0]
+    want = m.moe_combine_norm(y, pre_w=w, h_dtype=F32)
+    y[1] = 1e20
+    h, n = m.moe_combine_norm(y, pre_w=w, h_dtype=F32)
+    assert (h[1] == y[1]).all() and not n[1].any()
+    keep = [t for t in range(T) if t != 1] if T < 9 else slice(2, None)
+    assert torch.equal(h[keep], want[0][keep]) and torch.equal(n[keep], want[1][keep])

@@ -82,3 +82,19 @@ def test_more_chosen_than_are_left(m, T, top, G, chosen, K, score):
         want, _ = route.definition(plain, K, None, score, G, chosen, top)
     got = ids.cpu().numpy()
     assert not (got != want).any(), f"{(got != want).any(1).sum()} of {T} tokens differ"
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [50, 4100])
+def test_masks_of_the_lowest_value(m, T, dtype, score):
+    """Masked by the type's lowest value instead of -inf: an expert like any other, whose score rounds to 0."""
+    plain, given = masked(T, dtype, False, 3, 0.85)
+    low = torch.finfo(dtype).min
+    given = given.clamp(min=low)
+    plain = np.where(np.isfinite(plain), plain, np.float32(low))
+    for G, chosen, top in ((8, 4, 2), (8, 4, 1), (4, 1, 2), (1, 1, 1)):
+        ids, w = m.moe_route_grouped(given, K, None, score, G, chosen, top, with_shared=False)
+        with np.errstate(invalid="ignore"):
+            want, _ = route.definition(plain, K, None, score, G, chosen, top)
+        assert np.array_equal(ids.cpu().numpy(), want) and torch.isfinite(w).all()
