@@ -7,8 +7,8 @@
 // CTAs split the sum over K (v = A x), join their parts through distributed shared memory in rank order, and
 // split the N outputs.  x and the residual are read once, out is written once, and v never leaves the chip; A
 // and B are read once per 16 tokens, from L2 after the first.  It is bound by latency for few tokens and by the
-// weights of all their adapters for more: 64 tokens with 64 adapters of rank 16 at 4096 x 8192 take 10.7 us (26
-// MB, 2.5 TB/s).  Long prompts of one adapter go to lora_prompt.cu where they can.
+// weights of all their adapters for more: 64 tokens with 64 adapters of rank 16 at 4096 x 8192 take 10.0 us in a graph
+// with the weights in L2 and 12.0 with weights from HBM (26 MB: 2.2 TB/s).  Long prompts of one adapter go to lora_prompt.cu where they can.
 //
 // The products run as warp MMAs (bf16, m16n8k16) straight from global memory into registers.  Both operands
 // of an MMA may permute their k alike, so a lane takes 8 neighbouring k of a row (16 bytes) as its four k of
@@ -424,7 +424,7 @@ __device__ __forceinline__ void expand(const Lora& p, const uint16_t* b, int ran
 }
 
 // WHOLE: p.whole, known to the compiler.  Asked at run time both forms cost registers, which spilled: 64 tokens of 64
-// adapters 12.4 us against 11.8, 1024 tokens 9.9 against 9.4 (fp32 x and output alone took 151 against 154).
+// adapters in a graph, weights from HBM, 12.4 us against 11.8, 1024 tokens 9.9 against 9.4 (fp32 x and output alone took 151 against 154).
 template <int RT, bool XF32, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, RT <= 8 ? 2 : 1) lora_kernel(const __grid_constant__ Lora p) {
     using S = Shape<RT>;
@@ -546,7 +546,8 @@ bool lora_tile_supported(int tile_m) { return tile_m == 16 || tile_m == 32 || ti
 
 // Tile height: 128 where prompts fill such tiles and there are enough of them for the SMs (4096 tokens of 4
 // adapters at 4096 x 4096, rank 64: 32.8 us in tiles of 128, 52.6 in tiles of 16; rank 16: 30.1 and 31.0;
-// 2048 tokens at rank 16: 27 and 18.5), else 16.
+// 2048 tokens at rank 16: 27 and 18.5), else 16.  (`adapters` may be a pool of which few are used: then 16, where 8192
+// tokens of four prompts of a pool of 128 take 101 us at rank 64, and 70 in tiles of 128.)
 int lora_tile_rule(int T, int adapters) {
     const int each = T / std::max(1, std::min(T, adapters));
     return each >= 96 && T >= 2560 ? 128 : 16;

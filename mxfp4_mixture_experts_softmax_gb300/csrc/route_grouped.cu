@@ -30,6 +30,9 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.44269504f;
+// From so many tokens on several share a warp.  In us, a warp a token against several: 64 experts, top-6, 2048 tokens 2.8 and
+// 2.5, 4096 3.9 and 2.8, 32768 21 and 9.5; 256 in groups with a bias, top-8, 4096 8.3 and 11.8, 16384 20.5 and 19.9, 32768
+// 37 and 28, 131072 133 and 76; 512 with a bias, top-10, 4096 14.0 and 15.9, 8192 20.7 and 19.5, 32768 60 and 40.
 constexpr int kManyTokens = 4096, kManyWarps = 4;
 
 __device__ __forceinline__ float not_nan(float v) { return v == v ? v : -INFINITY; }  // a NaN is never preferred
@@ -524,7 +527,8 @@ __device__ __noinline__ void route_again(const RouteGrouped& p, int t, int lane)
 
 // S lanes a token (32 / S tokens a warp), VPL slots a lane, of which the 8 largest are kept.
 // Needs K <= S, groups <= S, experts of a group in fours.  Eight blocks an SM, which leaves 64 registers:
-// 131072 tokens with groups and a bias in 77 us, with the compiler's own choice in 90 (32768: the same).
+// 131072 tokens with groups and a bias in 77 us, with the compiler's own choice in 90 (32768: the same).  A warp loads its
+// tokens, works and ends, so it waits for memory: 37% of the issue slots are used at 32768 tokens, the main stall is that on loads.
 template <int S, int VPL, bool BF16>
 __global__ void __launch_bounds__(kManyWarps * 32, 8) route_grouped_many_kernel(const __grid_constant__ RouteGrouped p) {
     constexpr uint32_t kSlots = VPL - 1;

@@ -860,7 +860,9 @@ def moe_lora_tile_m(T: int, adapters: int) -> int:
 def moe_lora_plan(adapter_ids, adapters: int, tile_m: int | None = None, out: dict | None = None, stream=None) -> dict:
     """The grouping of tokens by adapter that moe_lora takes: int32 adapter_ids [T] (-1: none) ->
     moe_permute's dict.  One serves every projection of a step.  `out`: a plan of the same sizes to
-    write to, whose tile height it keeps."""
+    write to, whose tile height it keeps (15 us instead of 47 for five new tensors, 3 to 5 in a graph).  tile_m
+    goes by `adapters` if it is None; with a pool of which few are used, moe_lora_tile_m(T, those in use) suits prompts
+    better."""
     T, = adapter_ids.shape
     assert _code(adapter_ids) == -1, "adapter_ids must be int32"
     if out is not None:
